@@ -60,6 +60,8 @@ typedef enum {
 #define OSCAR_DEVERR_SEQ_LEN 0x4u   /* decode: seq_len < 0 or > max_seq_len (clamped)         */
 #define OSCAR_DEVERR_TIMEOUT 0x8u   /* a bounded wait on an async copy ran out (work skipped) */
 #define OSCAR_DEVERR_POSITION 0x10u /* append_mixed: sequence id or position out of range (BF16 row skipped) */
+#define OSCAR_DEVERR_NO_PAGES 0x20u /* pages_reserve / pages_fork: no free page left (request not granted) */
+#define OSCAR_DEVERR_VALUE 0x40u    /* kv8_append: a NaN in k or v (stored as 0)                        */
 
 /* Cache geometry. */
 typedef struct {
@@ -440,6 +442,201 @@ oscar_status_t oscar_calibrate(const oscar_dims_t* dims, int64_t num_samples, co
                                int32_t centered, double clip_quantile, const oscar_calib_out_t* out_k,
                                const oscar_calib_out_t* out_v, void* workspace, size_t workspace_bytes,
                                void* stream);
+
+/*
+ * ---- 8-bit paged cache ---------------------------------------------------------
+ *
+ * Between the INT2 pool and the BF16 pool: K and V unrotated, one byte per element,
+ * one scale per block of 16 tokens (a page) and KV head, for K and for V apart.
+ * The OSCAR pages have no counterpart; a serving engine keeps the layers or the
+ * requests that do not take 2 bits in such a cache, under the same page tables.
+ *   kv8_pages   device uint8 [num_pages][Hkv][2 = K,V][P][D], codes
+ *   kv8_scales  device fp32  [num_pages][Hkv][2]; a value is code * scale
+ * Formats (kv_format):
+ *   OSCAR_KV8_E4M3  code = e4m3 (4 exponent, 3 mantissa bits; no infinities), |code| <= 448 = M
+ *   OSCAR_KV8_INT8  code = int8 in [-127, 127], M = 127
+ * A scale is a power of two 2^e, -100 <= e <= 119 (e4m3) or 121 (int8): code * scale is
+ * exact in bf16 and fp32, and taking a block to a larger scale loses nothing but what the
+ * larger step cannot hold.
+ */
+#define OSCAR_KV8_E4M3 0
+#define OSCAR_KV8_INT8 1
+
+/*
+ * oscar_kv8_append -- quantise new tokens into the 8-bit pool.
+ *
+ * The new tokens of sequence b are rows t_start[b] .. t_start[b+1]-1 of k and v and sit
+ * at the last n_b = t_start[b+1] - t_start[b] positions of the sequence, in order
+ * (seq_lens counts them).  For every page that gets tokens, every KV head, K and V apart:
+ *   a     = max |x| over the new tokens in the page;
+ *   need  = the smallest 2^e in range with a <= M * 2^e (a = 0: 2^-100);
+ *   scale = need if the page's first token is new, else max(stored scale, need);
+ *   the new tokens' codes are rn(x / scale) (ties to even, saturating at +-M);
+ *   when the scale grew, the page's earlier codes c become rn(c * stored / scale).
+ * Rows behind the last token of a page are left as they are.  +-infinity saturates; a NaN
+ * is stored as 0 and flags OSCAR_DEVERR_VALUE.
+ * Arguments
+ *   max_tokens_per_seq  host bound on every n_b (sizes the grid)
+ *   k, v          device bf16 [num_tokens][Hkv][D], 16-byte aligned
+ *   t_start       device int32 [batch + 1], non-decreasing, t_start[0] = 0,
+ *                 t_start[batch] = num_tokens; n_b = 0 appends nothing
+ *   page_table    device int32 [batch][max_pages_per_seq]; the pages of the new tokens are
+ *                 there already (oscar_pages_reserve) and belong to one sequence only
+ *   seq_lens      device int32 [batch], lengths after this append
+ * A sequence whose n_b is negative, above max_tokens_per_seq or above its length, or whose
+ * length is above max_pages_per_seq * P, is skipped and flags OSCAR_DEVERR_POSITION; a page id
+ * out of range skips that page (OSCAR_DEVERR_PAGE_ID).  num_tokens == 0 is a no-op.
+ */
+oscar_status_t oscar_kv8_append(const oscar_dims_t* dims, int32_t kv_format, int32_t batch, int64_t num_tokens,
+                                int32_t max_tokens_per_seq, const void* k, const void* v, const int32_t* t_start,
+                                const int32_t* page_table, const int32_t* seq_lens, uint8_t* kv8_pages,
+                                float* kv8_scales, void* stream);
+
+/*
+ * oscar_kv8_decode -- paged GQA decode attention over the 8-bit cache, with an
+ * optional sliding window whose first tokens stay visible (sinks).
+ * For sequence b of length L = seq_lens[b], query head hq, KV head hq / (Hq/Hkv):
+ *   window_len == 0   every position j < L is visible (sink_len is ignored)
+ *   window_len >= 1   j < L is visible if j >= L - window_len or j < sink_len
+ *   out = sum_j w_j v_j / sum_j w_j,  w_j = exp(sm_scale * q.k_j - max)
+ * A sequence with L == 0 gets zeros.  Pages without a visible position are not read: their
+ * page table entries may hold anything (oscar_pages_trim sets them to -1).
+ * Arguments
+ *   max_seq_len   host bound on every seq_lens[b] (<= max_pages_per_seq * P); larger or negative
+ *                 device values are clamped and flagged (OSCAR_DEVERR_SEQ_LEN)
+ *   pages_per_split  0 = chosen from the grid size; else >= 1 pages of one split (at most
+ *                 65535 splits per sequence; batch <= 65535)
+ *   q, out        device bf16 [batch][Hq][D], q 16-byte aligned, out 16-byte aligned.  The output has the
+ *                 type of q (the projection that follows reads it); sums and softmax statistics are fp32
+ *   kv8_pages, kv8_scales, page_table  as oscar_kv8_append
+ *   sm_scale      softmax scale; <= 0 selects 1/sqrt(D)
+ *   workspace     at least oscar_kv8_decode_workspace_bytes(...) bytes, 256-byte aligned; needs no
+ *                 initialisation
+ * A page id out of range attends nothing of that page and flags OSCAR_DEVERR_PAGE_ID.
+ */
+size_t oscar_kv8_decode_workspace_bytes(const oscar_dims_t* dims, int32_t batch, int32_t max_seq_len,
+                                        int32_t pages_per_split, int32_t sink_len, int32_t window_len);
+oscar_status_t oscar_kv8_decode(const oscar_dims_t* dims, int32_t kv_format, int32_t batch, int32_t max_seq_len,
+                                int32_t pages_per_split, const void* q, const uint8_t* kv8_pages,
+                                const float* kv8_scales, const int32_t* page_table, const int32_t* seq_lens,
+                                int32_t sink_len, int32_t window_len, float sm_scale, void* out, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
+ * oscar_kv8_extend_varlen -- attention of several query rows per sequence over the 8-bit
+ * cache (prompt chunks, draft verification): rows q_start[b] .. q_start[b+1]-1 sit at the last
+ * n_b positions of sequence b, whose tokens have been appended.  The row at position p sees
+ * j <= p, and with window_len >= 1 only j > p - window_len or j < sink_len; otherwise as
+ * oscar_kv8_decode.  Arguments as oscar_extend_varlen and oscar_kv8_decode:
+ *   num_rows          q_start[batch]; q and out are bf16 [num_rows][Hq][D]
+ *   max_rows_per_seq  host bound on every n_b (sizes the grid)
+ *   pages_per_split   0 = chosen from the grid size; else >= 1
+ *   q_start           device int32 [batch + 1], non-decreasing, q_start[0] = 0
+ * Rows that outnumber their sequence's tokens (n_b > L) have no position: they give zeros and
+ * flag OSCAR_DEVERR_POSITION.  A q_start that decreases, leaves [0, num_rows] or makes n_b larger
+ * than max_rows_per_seq flags it too, and rows beyond the bound are not written.
+ */
+size_t oscar_kv8_extend_varlen_workspace_bytes(const oscar_dims_t* dims, int32_t batch, int32_t num_rows,
+                                               int32_t max_seq_len, int32_t max_rows_per_seq,
+                                               int32_t pages_per_split, int32_t sink_len, int32_t window_len);
+oscar_status_t oscar_kv8_extend_varlen(const oscar_dims_t* dims, int32_t kv_format, int32_t batch, int32_t num_rows,
+                                       int32_t max_seq_len, int32_t max_rows_per_seq, int32_t pages_per_split,
+                                       const void* q, const int32_t* q_start, const uint8_t* kv8_pages,
+                                       const float* kv8_scales, const int32_t* page_table, const int32_t* seq_lens,
+                                       int32_t sink_len, int32_t window_len, float sm_scale, void* out,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---- Pages ----------------------------------------------------------------------
+ *
+ * Operations on the pages of a paged cache, whatever they hold: the INT2 codes and
+ * scale/zero pools, the BF16 pool, the 8-bit codes and scales (the OSCAR pages name a paged
+ * KV cache and leave its management to the serving engine).  They run on the device in stream
+ * order and read no length on the host, so a serving step with them can be captured in a graph.
+ * Every array is the caller's:
+ *   page_table  device int32 [batch][max_pages_per_seq]; sequence b holds the entries
+ *               j < ceil(seq_lens[b] / P) that are >= 0; other entries are neither read nor
+ *               counted
+ *   seq_lens    device int32 [batch]
+ *   page_refs   device int32 [num_pages]: the number of page table entries that hold the page;
+ *               0 is free.  This is the allocator's whole state (all zeros at the start)
+ *   pools       host array of num_pools (0 .. OSCAR_MAX_POOLS) pools; base is 16-byte aligned, page i is
+ *               the page_bytes bytes at base + i * page_bytes, page_bytes a multiple of 4
+ * Free pages are handed out lowest id first, in the order of the requests, so results do not
+ * depend on timing.  A page is written by one sequence only as long as a partial last page is
+ * never shared: oscar_pages_fork copies it.
+ * Lengths outside [0, max_pages_per_seq * P] and sequence ids outside [0, batch) skip that
+ * request and flag OSCAR_DEVERR_POSITION; page ids out of range, and a release of a page that
+ * is free already, are skipped and flag OSCAR_DEVERR_PAGE_ID.
+ * Workspace: oscar_pages_workspace_bytes(dims, batch, num_forks) bytes for reserve, fork and
+ * compact (num_forks 0 where there is no fork), 256-byte aligned, no initialisation.
+ */
+#define OSCAR_MAX_POOLS 8
+typedef struct {
+  void* base;
+  int64_t page_bytes;
+} oscar_page_pool_t;
+
+size_t oscar_pages_workspace_bytes(const oscar_dims_t* dims, int32_t batch, int32_t num_forks);
+
+/*
+ * oscar_pages_copy -- page dst[i] of every pool becomes a copy of page src[i] (device int32
+ * [num_copies]); a negative src or dst skips the pair.  The dst pages are distinct and none of
+ * them is a src page.  With (base, bytes per sequence) in the place of a pool, and dims.num_pages =
+ * batch, it copies per-sequence buffers (the BF16 sink and window of a forked INT2 cache).
+ */
+oscar_status_t oscar_pages_copy(const oscar_dims_t* dims, int32_t num_pools, const oscar_page_pool_t* pools,
+                                int32_t num_copies, const int32_t* src, const int32_t* dst, void* stream);
+
+/*
+ * oscar_pages_reserve -- room for new_tokens[b] >= 0 more tokens of every sequence: the pages that
+ * positions [L, L + new_tokens[b]) need beyond those held get free pages (count 1), and
+ * seq_lens[b] becomes L + new_tokens[b].  granted[b] (device int32, may be NULL) is 1, or 0 where
+ * the request was refused: sequences are served in order, and one whose pages, together with
+ * those that all sequences before it asked for, outnumber the free pages is refused (nothing of it
+ * changes; OSCAR_DEVERR_NO_PAGES).
+ */
+oscar_status_t oscar_pages_reserve(const oscar_dims_t* dims, int32_t batch, const int32_t* new_tokens,
+                                   int32_t* page_table, int32_t* seq_lens, int32_t* page_refs, int32_t* granted,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * oscar_pages_fork -- sequence dst_seq[i] becomes a copy of src_seq[i], for every i < num_forks:
+ * full pages are shared (their counts grow), a partial last page (L % P != 0) is copied in every
+ * pool into a free page, and seq_lens[dst] = L.  dst has length 0 before the call (a sequence in
+ * use is refused, OSCAR_DEVERR_POSITION); where several forks name one dst, the lowest i counts and
+ * the others are refused.  Any number of forks may share a src.  granted[i] (device int32, may be
+ * NULL) is 1, or 0 where fork i was refused, also for want of a free page (as reserve).
+ */
+oscar_status_t oscar_pages_fork(const oscar_dims_t* dims, int32_t num_pools, const oscar_page_pool_t* pools,
+                                int32_t batch, int32_t num_forks, const int32_t* src_seq, const int32_t* dst_seq,
+                                int32_t* page_table, int32_t* seq_lens, int32_t* page_refs, int32_t* granted,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * oscar_pages_free -- releases every page of the sequences seqs[0 .. num_seqs) (device int32; the
+ * same one twice is released once): counts fall, table entries become -1, lengths 0.
+ */
+oscar_status_t oscar_pages_free(const oscar_dims_t* dims, int32_t batch, int32_t num_seqs, const int32_t* seqs,
+                                int32_t* page_table, int32_t* seq_lens, int32_t* page_refs, void* stream);
+
+/*
+ * oscar_pages_trim -- releases the pages that attention with (sink_len, window_len >= 1) does not
+ * see any more: of every sequence the pages that lie wholly in positions [sink_len, L - window_len).
+ * Their entries become -1; lengths stay.  Query rows at positions >= L - 1 see the same as before.
+ */
+oscar_status_t oscar_pages_trim(const oscar_dims_t* dims, int32_t batch, int32_t sink_len, int32_t window_len,
+                                int32_t* page_table, const int32_t* seq_lens, int32_t* page_refs, void* stream);
+
+/*
+ * oscar_pages_compact -- moves the pages in use to the lowest ids, in place: with n pages in use, the
+ * i-th used page with id >= n goes to the i-th free id below n, in every pool, its count with it, and
+ * the page table entries of all sequences follow.  num_used (device int32[1], may be NULL) receives n: the
+ * pool's pages from n on are free, and can be given back.
+ */
+oscar_status_t oscar_pages_compact(const oscar_dims_t* dims, int32_t num_pools, const oscar_page_pool_t* pools,
+                                   int32_t batch, int32_t* page_table, const int32_t* seq_lens, int32_t* page_refs,
+                                   int32_t* num_used, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* oscar_status_string(oscar_status_t status);

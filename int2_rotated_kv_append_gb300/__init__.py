@@ -29,6 +29,13 @@ OSCAR_DEVERR_PAGE_ID = 0x2
 OSCAR_DEVERR_SEQ_LEN = 0x4
 OSCAR_DEVERR_TIMEOUT = 0x8
 OSCAR_DEVERR_POSITION = 0x10
+OSCAR_DEVERR_NO_PAGES = 0x20
+OSCAR_DEVERR_VALUE = 0x40
+
+OSCAR_KV8_E4M3 = 0
+OSCAR_KV8_INT8 = 1
+
+OSCAR_MAX_POOLS = 8
 
 
 class OscarError(RuntimeError):
@@ -47,6 +54,10 @@ class oscar_calib_out_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("R", "clip", "eigenvalues", "cov", "sweeps")]
 
 
+class oscar_page_pool_t(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"OSCAR CUDA library not built ({LIB_PATH} missing); run "
@@ -54,6 +65,7 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, I64, F32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
     D = ctypes.POINTER(oscar_dims_t)
+    L = ctypes.POINTER(oscar_page_pool_t)
     sigs = {
         "oscar_append": (I32, [D, I64, P, P, P, P, P, P, P, P, P, P, P, P]),
         "oscar_append_mixed": (I32, [D, I64, P, P, P, P, P, P, P, P, P, P, P, P, I32, I32, I32, P, P, P, P, P]),
@@ -75,6 +87,18 @@ def _load():
         "oscar_calibrate_workspace_bytes": (SZ, [D, I64]),
         "oscar_calibrate": (I32, [D, I64, P, P, I32, ctypes.c_double, ctypes.POINTER(oscar_calib_out_t),
                                   ctypes.POINTER(oscar_calib_out_t), P, SZ, P]),
+        "oscar_kv8_append": (I32, [D, I32, I32, I64, I32, P, P, P, P, P, P, P, P]),
+        "oscar_kv8_decode_workspace_bytes": (SZ, [D, I32, I32, I32, I32, I32]),
+        "oscar_kv8_decode": (I32, [D, I32, I32, I32, I32, P, P, P, P, P, I32, I32, F32, P, P, SZ, P]),
+        "oscar_kv8_extend_varlen_workspace_bytes": (SZ, [D, I32, I32, I32, I32, I32, I32, I32]),
+        "oscar_kv8_extend_varlen": (I32, [D, I32, I32, I32, I32, I32, I32, P, P, P, P, P, P, I32, I32, F32, P, P, SZ, P]),
+        "oscar_pages_workspace_bytes": (SZ, [D, I32, I32]),
+        "oscar_pages_copy": (I32, [D, I32, L, I32, P, P, P]),
+        "oscar_pages_reserve": (I32, [D, I32, P, P, P, P, P, P, SZ, P]),
+        "oscar_pages_fork": (I32, [D, I32, L, I32, I32, P, P, P, P, P, P, P, SZ, P]),
+        "oscar_pages_free": (I32, [D, I32, I32, P, P, P, P, P]),
+        "oscar_pages_trim": (I32, [D, I32, I32, I32, P, P, P, P]),
+        "oscar_pages_compact": (I32, [D, I32, L, I32, P, P, P, P, P, SZ, P]),
         "oscar_status_string": (ctypes.c_char_p, [I32]),
         "oscar_device_errors": (I32, [ctypes.POINTER(ctypes.c_uint32), I32]),
         "oscar_test_stall_page_waits": (I32, [I64]),
@@ -292,6 +316,123 @@ def oscar_calibrate(dims, num_samples, k, v, centered, clip_quantile, out_k, out
     _check(lib.oscar_calibrate(ctypes.byref(_dims(dims)), int(num_samples), _ptr(k), _ptr(v), int(centered),
                                float(clip_quantile), _calib_out(out_k), _calib_out(out_v), _ptr(workspace),
                                workspace.numel() * workspace.element_size(), _stream(stream)), "oscar_calibrate")
+
+
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size()
+
+
+def oscar_kv8_append(dims, kv_format, batch, max_tokens_per_seq, k, v, t_start, page_table, seq_lens, kv8_pages,
+                     kv8_scales, stream=None):
+    """Quantise the new tokens k, v (bf16 [T][Hkv][D]; rows t_start[b] .. t_start[b+1]-1 are the
+    last positions of sequence b) into the 8-bit pool: codes and a power-of-two scale per
+    (page, KV head, K | V)."""
+    _check(lib.oscar_kv8_append(ctypes.byref(_dims(dims)), int(kv_format), int(batch), int(k.shape[0]),
+                                int(max_tokens_per_seq), _ptr(k), _ptr(v), _ptr(t_start), _ptr(page_table),
+                                _ptr(seq_lens), _ptr(kv8_pages), _ptr(kv8_scales), _stream(stream)),
+           "oscar_kv8_append")
+
+
+def oscar_kv8_decode_workspace_bytes(dims, batch, max_seq_len, pages_per_split, sink_len, window_len) -> int:
+    return int(lib.oscar_kv8_decode_workspace_bytes(ctypes.byref(_dims(dims)), int(batch), int(max_seq_len),
+                                                    int(pages_per_split), int(sink_len), int(window_len)))
+
+
+def oscar_kv8_decode(dims, kv_format, batch, max_seq_len, pages_per_split, q, kv8_pages, kv8_scales, page_table,
+                     seq_lens, sink_len, window_len, sm_scale, out, workspace, stream=None):
+    """One decode step over the 8-bit cache; window_len >= 1: only the last window_len positions
+    and the first sink_len are visible.  Writes bf16 out [B][Hq][D]."""
+    _check(lib.oscar_kv8_decode(ctypes.byref(_dims(dims)), int(kv_format), int(batch), int(max_seq_len),
+                                int(pages_per_split), _ptr(q), _ptr(kv8_pages), _ptr(kv8_scales), _ptr(page_table),
+                                _ptr(seq_lens), int(sink_len), int(window_len), float(sm_scale), _ptr(out),
+                                _ptr(workspace), _nbytes(workspace), _stream(stream)), "oscar_kv8_decode")
+
+
+def oscar_kv8_extend_varlen_workspace_bytes(dims, batch, num_rows, max_seq_len, max_rows_per_seq, pages_per_split,
+                                            sink_len, window_len) -> int:
+    return int(lib.oscar_kv8_extend_varlen_workspace_bytes(ctypes.byref(_dims(dims)), int(batch), int(num_rows),
+                                                           int(max_seq_len), int(max_rows_per_seq),
+                                                           int(pages_per_split), int(sink_len), int(window_len)))
+
+
+def oscar_kv8_extend_varlen(dims, kv_format, batch, max_seq_len, max_rows_per_seq, pages_per_split, q, q_start,
+                            kv8_pages, kv8_scales, page_table, seq_lens, sink_len, window_len, sm_scale, out,
+                            workspace, stream=None):
+    """Causal attention of the rows q [rows][Hq][D] (rows q_start[b] .. q_start[b+1]-1 are the last
+    positions of sequence b) over the 8-bit cache, full or with a window and sinks.  Writes bf16
+    out [rows][Hq][D]."""
+    _check(lib.oscar_kv8_extend_varlen(ctypes.byref(_dims(dims)), int(kv_format), int(batch), int(q.shape[0]),
+                                       int(max_seq_len), int(max_rows_per_seq), int(pages_per_split), _ptr(q),
+                                       _ptr(q_start), _ptr(kv8_pages), _ptr(kv8_scales), _ptr(page_table),
+                                       _ptr(seq_lens), int(sink_len), int(window_len), float(sm_scale), _ptr(out),
+                                       _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "oscar_kv8_extend_varlen")
+
+
+def _pools(pools, num_pages):
+    """The pools' tensors, num_pages pages each, as the C array."""
+    arr = (oscar_page_pool_t * max(len(pools), 1))()
+    for i, t in enumerate(pools):
+        nbytes = _nbytes(t)
+        if not t.is_contiguous() or nbytes == 0 or nbytes % num_pages:
+            raise ValueError("a page pool is a contiguous tensor of num_pages equal pages")
+        arr[i].base, arr[i].page_bytes = t.data_ptr(), nbytes // num_pages
+    return arr
+
+
+def oscar_pages_workspace_bytes(dims, batch, num_forks) -> int:
+    return int(lib.oscar_pages_workspace_bytes(ctypes.byref(_dims(dims)), int(batch), int(num_forks)))
+
+
+def oscar_pages_copy(dims, pools, src, dst, stream=None):
+    """Page dst[i] of every pool (a list of tensors of dims.num_pages pages) becomes a copy of page
+    src[i] (int32 device tensors)."""
+    d = _dims(dims)
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst have one entry per copy")
+    _check(lib.oscar_pages_copy(ctypes.byref(d), len(pools), _pools(pools, d.num_pages), int(src.numel()), _ptr(src),
+                                _ptr(dst), _stream(stream)), "oscar_pages_copy")
+
+
+def oscar_pages_reserve(dims, new_tokens, page_table, seq_lens, page_refs, granted, workspace, stream=None):
+    """Free pages for new_tokens[b] more tokens of every sequence; seq_lens grows; granted[b] is 0
+    where the free pages ran out."""
+    _check(lib.oscar_pages_reserve(ctypes.byref(_dims(dims)), int(seq_lens.shape[0]), _ptr(new_tokens),
+                                   _ptr(page_table), _ptr(seq_lens), _ptr(page_refs), _ptr(granted), _ptr(workspace),
+                                   _nbytes(workspace), _stream(stream)), "oscar_pages_reserve")
+
+
+def oscar_pages_fork(dims, pools, src_seq, dst_seq, page_table, seq_lens, page_refs, granted, workspace, stream=None):
+    """Sequence dst_seq[i] becomes a copy of src_seq[i]: full pages shared, a partial last page copied."""
+    d = _dims(dims)
+    if src_seq.numel() != dst_seq.numel():
+        raise ValueError("src_seq and dst_seq have one entry per fork")
+    _check(lib.oscar_pages_fork(ctypes.byref(d), len(pools), _pools(pools, d.num_pages), int(seq_lens.shape[0]),
+                                int(src_seq.numel()), _ptr(src_seq), _ptr(dst_seq), _ptr(page_table), _ptr(seq_lens),
+                                _ptr(page_refs), _ptr(granted), _ptr(workspace), _nbytes(workspace),
+                                _stream(stream)), "oscar_pages_fork")
+
+
+def oscar_pages_free(dims, seqs, page_table, seq_lens, page_refs, stream=None):
+    """Release every page of the sequences seqs (int32 device tensor)."""
+    _check(lib.oscar_pages_free(ctypes.byref(_dims(dims)), int(seq_lens.shape[0]), int(seqs.numel()), _ptr(seqs),
+                                _ptr(page_table), _ptr(seq_lens), _ptr(page_refs), _stream(stream)),
+           "oscar_pages_free")
+
+
+def oscar_pages_trim(dims, sink_len, window_len, page_table, seq_lens, page_refs, stream=None):
+    """Release the pages that attention with (sink_len, window_len) does not see any more."""
+    _check(lib.oscar_pages_trim(ctypes.byref(_dims(dims)), int(seq_lens.shape[0]), int(sink_len), int(window_len),
+                                _ptr(page_table), _ptr(seq_lens), _ptr(page_refs), _stream(stream)),
+           "oscar_pages_trim")
+
+
+def oscar_pages_compact(dims, pools, page_table, seq_lens, page_refs, num_used, workspace, stream=None):
+    """Move the pages in use to the lowest ids, in place; num_used (int32 [1] or None) receives their number."""
+    d = _dims(dims)
+    _check(lib.oscar_pages_compact(ctypes.byref(d), len(pools), _pools(pools, d.num_pages), int(seq_lens.shape[0]),
+                                   _ptr(page_table), _ptr(seq_lens), _ptr(page_refs), _ptr(num_used), _ptr(workspace),
+                                   _nbytes(workspace), _stream(stream)), "oscar_pages_compact")
 
 
 def oscar_test_stall_page_waits(cycles: int) -> None:

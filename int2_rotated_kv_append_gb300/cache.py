@@ -2,17 +2,22 @@
 
 ``Int2Cache`` owns the INT2 code pool, the fp16 scale/zero pool and the BF16
 sink/window buffers of a workload; ``Bf16Cache`` owns the all-BF16 pool of the
-speedup reference.  Both only allocate torch memory and call the library, as does
-``calibrate`` (the offline step that produces R and the clipping thresholds).
+speedup reference; ``Kv8Cache`` owns an 8-bit pool whose pages it manages itself
+(reserve, fork, free, trim, compact).  They only allocate torch memory and call the
+library, as does ``calibrate`` (the offline step that produces R and the clipping
+thresholds).
 """
 
 from __future__ import annotations
 
 import torch
 
-from . import (make_dims, oscar_append, oscar_append_mixed, oscar_bf16_append, oscar_bf16_decode, oscar_bf16_decode_workspace_bytes,
-               oscar_calibrate, oscar_calibrate_workspace_bytes, oscar_decode, oscar_decode_workspace_bytes,
-               oscar_extend, oscar_extend_varlen, oscar_extend_varlen_workspace_bytes, oscar_extend_workspace_bytes)
+from . import (OSCAR_KV8_E4M3, make_dims, oscar_append, oscar_append_mixed, oscar_bf16_append, oscar_bf16_decode,
+               oscar_bf16_decode_workspace_bytes, oscar_calibrate, oscar_calibrate_workspace_bytes, oscar_decode,
+               oscar_decode_workspace_bytes, oscar_extend, oscar_extend_varlen, oscar_extend_varlen_workspace_bytes,
+               oscar_extend_workspace_bytes, oscar_kv8_append, oscar_kv8_decode, oscar_kv8_decode_workspace_bytes,
+               oscar_kv8_extend_varlen, oscar_kv8_extend_varlen_workspace_bytes, oscar_pages_compact, oscar_pages_fork,
+               oscar_pages_free, oscar_pages_reserve, oscar_pages_trim, oscar_pages_workspace_bytes)
 from .synth import Workload
 
 SENTINEL = 0xA5
@@ -154,6 +159,82 @@ class Bf16Cache:
         oscar_bf16_decode(self.dims, w.batch, w.max_seq_len, self.pps, q, self.pages, self.page_table,
                           self.seq_lens, sm_scale, out, self.workspace(), stream)
         return out
+
+
+class Kv8Cache:
+    """An 8-bit paged cache for up to ``batch`` sequences, with its page table, lengths and page
+    counts.  With ``window_len`` >= 1 attention sees the last window_len positions and the first
+    sink_len, and ``trim`` gives back the pages behind the window."""
+
+    def __init__(self, num_q_heads, num_kv_heads, head_dim, num_pages, batch, max_seq_len, kv_format=OSCAR_KV8_E4M3,
+                 sink_len=0, window_len=0, device="cuda"):
+        self.device = torch.device(device)
+        self.batch, self.max_seq_len, self.kv_format = batch, max_seq_len, kv_format
+        self.sink_len, self.window_len = sink_len, window_len
+        self.dims = make_dims(num_q_heads, num_kv_heads, head_dim, 16, head_dim, num_pages, max(1, -(-max_seq_len // 16)))
+        d = self.device
+        self.pages = torch.zeros((num_pages, num_kv_heads, 2, 16, head_dim), dtype=torch.uint8, device=d)
+        self.scales = torch.zeros((num_pages, num_kv_heads, 2), dtype=torch.float32, device=d)
+        self.page_table = torch.full((batch, self.dims.max_pages_per_seq), -1, dtype=torch.int32, device=d)
+        self.seq_lens = torch.zeros(batch, dtype=torch.int32, device=d)
+        self.page_refs = torch.zeros(num_pages, dtype=torch.int32, device=d)
+        self.granted = torch.zeros(batch, dtype=torch.int32, device=d)
+        self._ws = []  # the last one is used; smaller ones stay for captured graphs that point to them
+
+    def _workspace(self, nbytes):
+        if nbytes == 0:
+            raise ValueError("invalid arguments for workspace sizing")
+        if not self._ws or self._ws[-1].numel() < nbytes:
+            self._ws.append(torch.empty(nbytes, dtype=torch.uint8, device=self.device))
+        return self._ws[-1]
+
+    def reserve(self, new_tokens, stream=None):
+        """Pages for new_tokens[b] (int32 device [batch]) more tokens of each sequence; returns ``granted``."""
+        oscar_pages_reserve(self.dims, new_tokens, self.page_table, self.seq_lens, self.page_refs, self.granted,
+                            self._workspace(oscar_pages_workspace_bytes(self.dims, self.batch, 0)), stream)
+        return self.granted
+
+    def append(self, k, v, t_start, max_tokens_per_seq, stream=None):
+        """Quantise the reserved tokens k, v [T][Hkv][D]; t_start int32 device [batch + 1]."""
+        oscar_kv8_append(self.dims, self.kv_format, self.batch, max_tokens_per_seq, k, v, t_start, self.page_table,
+                         self.seq_lens, self.pages, self.scales, stream)
+
+    def decode(self, q, out=None, sm_scale=0.0, pages_per_split=0, stream=None):
+        if out is None:
+            out = torch.empty_like(q)
+        ws = self._workspace(oscar_kv8_decode_workspace_bytes(self.dims, self.batch, self.max_seq_len, pages_per_split,
+                                                              self.sink_len, self.window_len))
+        oscar_kv8_decode(self.dims, self.kv_format, self.batch, self.max_seq_len, pages_per_split, q, self.pages,
+                         self.scales, self.page_table, self.seq_lens, self.sink_len, self.window_len, sm_scale, out, ws,
+                         stream)
+        return out
+
+    def extend(self, q, q_start, max_rows_per_seq, out=None, sm_scale=0.0, pages_per_split=0, stream=None):
+        if out is None:
+            out = torch.empty_like(q)
+        ws = self._workspace(oscar_kv8_extend_varlen_workspace_bytes(
+            self.dims, self.batch, q.shape[0], self.max_seq_len, max_rows_per_seq, pages_per_split, self.sink_len,
+            self.window_len))
+        oscar_kv8_extend_varlen(self.dims, self.kv_format, self.batch, self.max_seq_len, max_rows_per_seq,
+                                pages_per_split, q, q_start, self.pages, self.scales, self.page_table, self.seq_lens,
+                                self.sink_len, self.window_len, sm_scale, out, ws, stream)
+        return out
+
+    def fork(self, src_seq, dst_seq, granted=None, stream=None):
+        oscar_pages_fork(self.dims, [self.pages, self.scales], src_seq, dst_seq, self.page_table, self.seq_lens,
+                         self.page_refs, granted,
+                         self._workspace(oscar_pages_workspace_bytes(self.dims, self.batch, src_seq.numel())), stream)
+
+    def free(self, seqs, stream=None):
+        oscar_pages_free(self.dims, seqs, self.page_table, self.seq_lens, self.page_refs, stream)
+
+    def trim(self, stream=None):
+        oscar_pages_trim(self.dims, self.sink_len, self.window_len, self.page_table, self.seq_lens, self.page_refs,
+                         stream)
+
+    def compact(self, num_used=None, stream=None):
+        oscar_pages_compact(self.dims, [self.pages, self.scales], self.page_table, self.seq_lens, self.page_refs,
+                            num_used, self._workspace(oscar_pages_workspace_bytes(self.dims, self.batch, 0)), stream)
 
 
 def calibrate(k=None, v=None, centered: bool = True, clip_quantile: float = 1.0, with_cov: bool = False,

@@ -85,6 +85,25 @@ static inline cudaError_t set_smem_limit_once(const void* func, size_t bytes) {
   return e;
 }
 
+// Launches `kernel` with programmatic stream serialisation: it may overlap the
+// tail of the preceding kernel in the stream and must call grid_dep_wait()
+// before reading that kernel's output.
+template <typename... Args>
+cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                       Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 __device__ __forceinline__ float bf16_bits_to_float(uint32_t bits16) { return __uint_as_float(bits16 << 16); }
 
 }  // namespace oscar
@@ -106,3 +125,6 @@ oscar_status_t oscar_internal_decode_fused_errors(uint32_t* flags, int reset);
 oscar_status_t oscar_internal_decode_bf16_errors(uint32_t* flags, int reset);
 oscar_status_t oscar_internal_decode_umma_errors(uint32_t* flags, int reset);
 oscar_status_t oscar_internal_calib_errors(uint32_t* flags, int reset);
+oscar_status_t oscar_internal_kv8_append_errors(uint32_t* flags, int reset);
+oscar_status_t oscar_internal_kv8_attn_errors(uint32_t* flags, int reset);
+oscar_status_t oscar_internal_pages_errors(uint32_t* flags, int reset);

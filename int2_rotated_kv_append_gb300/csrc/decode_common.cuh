@@ -122,25 +122,6 @@ int int2_fused_max_pps(int gqa);
 int int2_fused_ctas_per_sm(int gqa, int G);
 cudaError_t int2_fused_decode(const Params& p, cudaStream_t stream);
 
-// Launches `kernel` with programmatic stream serialisation: it may overlap the
-// tail of the preceding kernel in the stream and must call grid_dep_wait()
-// before reading that kernel's output.
-template <typename... Args>
-cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                       Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 
 namespace {  // internal linkage in every unit that includes this header
 
