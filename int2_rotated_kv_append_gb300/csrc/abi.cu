@@ -24,7 +24,8 @@ extern "C" oscar_status_t oscar_device_errors(uint32_t* flags, int32_t reset) {
   if (st == OSCAR_OK) st = oscar_internal_decode_umma_errors(flags, reset);
   if (st == OSCAR_OK) st = oscar_internal_calib_errors(flags, reset);
   if (st == OSCAR_OK) st = oscar_internal_kv8_append_errors(flags, reset);
-  if (st == OSCAR_OK) st = oscar_internal_kv8_attn_errors(flags, reset);
+  if (st == OSCAR_OK) st = oscar_internal_kv8_decode_errors(flags, reset);
+  if (st == OSCAR_OK) st = oscar_internal_kv8_extend_errors(flags, reset);
   if (st == OSCAR_OK) st = oscar_internal_pages_errors(flags, reset);
   return st;
 }

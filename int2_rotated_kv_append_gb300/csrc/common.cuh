@@ -126,5 +126,6 @@ oscar_status_t oscar_internal_decode_bf16_errors(uint32_t* flags, int reset);
 oscar_status_t oscar_internal_decode_umma_errors(uint32_t* flags, int reset);
 oscar_status_t oscar_internal_calib_errors(uint32_t* flags, int reset);
 oscar_status_t oscar_internal_kv8_append_errors(uint32_t* flags, int reset);
-oscar_status_t oscar_internal_kv8_attn_errors(uint32_t* flags, int reset);
+oscar_status_t oscar_internal_kv8_decode_errors(uint32_t* flags, int reset);
+oscar_status_t oscar_internal_kv8_extend_errors(uint32_t* flags, int reset);
 oscar_status_t oscar_internal_pages_errors(uint32_t* flags, int reset);

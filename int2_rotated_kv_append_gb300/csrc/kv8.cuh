@@ -73,5 +73,56 @@ __device__ __forceinline__ int scale_exponent(float a) {
   return min(max(e, kExpLo), F == kE4M3 ? 119 : 121);
 }
 
+// The two 16-bit halves of a word, each a pair of codes -> two fp16 pairs, exact.
+template <int F>
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (F == kE4M3) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  } else {
+    // with the sign bit flipped a code is c + 128: as the low byte of an fp16 in [1024, 2048) it
+    // counts ones, so subtracting 1152 leaves c
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+
+// Positions of a sequence that a row at position `row` sees: [0, sink_end) and [lo, row], as a list of
+// pages: the first nA pages, then pages first_b ... of the window (a page that holds both ends is
+// in the first part).
+struct Visible {
+  int sink_end, lo, end;  // positions
+  int n_a, first_b, n;    // pages
+  __device__ __forceinline__ int page(int v) const { return v < n_a ? v : first_b + v - n_a; }
+  __device__ __forceinline__ bool sees(int pos) const { return pos < end && (pos < sink_end || pos >= lo); }
+};
+
+// Rows first_row .. last_row (>= 0) of one sequence together.
+__device__ __forceinline__ Visible visible(int first_row, int last_row, int sink, int window) {
+  Visible v;
+  v.end = last_row + 1;
+  v.lo = window > 0 ? max(0, first_row - window + 1) : 0;
+  v.sink_end = min(sink, v.lo);
+  v.n_a = (v.sink_end + kPageSize - 1) / kPageSize;
+  v.first_b = max(v.lo / kPageSize, v.n_a);
+  v.n = v.n_a + max(0, (v.end + kPageSize - 1) / kPageSize - v.first_b);
+  return v;
+}
+
+// Host bound on Visible::n for lengths up to max_seq_len and runs of `rows` rows.
+static inline long long max_visible_pages(long long max_seq_len, int sink, int window, long long rows) {
+  const long long all = (max_seq_len + kPageSize - 1) / kPageSize;
+  if (window <= 0) return all;
+  const long long some = (static_cast<long long>(sink) + kPageSize - 1) / kPageSize +
+                         (window + rows + 2LL * kPageSize - 3) / kPageSize + 1;
+  return some < all ? some : all;
+}
+
 }  // namespace kv8
 }  // namespace oscar

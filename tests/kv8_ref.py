@@ -79,7 +79,10 @@ def attention(codes, scales, q, row_seq, row_pos, table, fmt, sink, window, sm_s
 
     The tolerance counts roundings: the weights may be held in bf16 (half a step 2^-8 each, so 2^-8 of
     A = sum w |v| / sum w), the output is bf16 (2^-8 of itself), logits are fp32 sums of D products
-    (an error of d in a logit changes weights by a factor 1 + d, numerator and denominator)."""
+    (an error of d in a logit changes weights by a factor 1 + d, numerator and denominator).  Weights
+    held as fp16 parts have a smallest step of 2^-14 2^-12 2^-24 = 2^-50 of the largest weight beside them, so
+    a weight is off by at most 2^-51 of the largest: n 2^-51 max |v| for n visible tokens (it matters only
+    where every larger weight meets a value of 0)."""
     R, hq, D = q.shape
     H = codes.shape[1]
     out = torch.zeros(R, hq, D, dtype=torch.float64, device=q.device)
@@ -112,7 +115,7 @@ def attention(codes, scales, q, row_seq, row_pos, table, fmt, sink, window, sm_s
             o, a = w @ vv / total, w @ vv.abs() / total
             dlog = (D + 16) * 2.0 ** -24 * (qq.abs() @ kk.abs().T * scale).amax(1, keepdim=True)
             out[rows, h] = o
-            tol[rows, h] = 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.0 ** -12) * a + 2 * dlog * a + 2.0 ** -120
+            tol[rows, h] = 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.0 ** -12) * a + 2 * dlog * a + see.sum(1, keepdim=True) * 2.0 ** -51 * vv.abs().max()
     return out, tol
 
 
