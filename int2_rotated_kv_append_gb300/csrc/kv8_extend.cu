@@ -1,84 +1,665 @@
-// Attention over the 8-bit paged cache: decode (one row per sequence) and extend (the last
-// rows of each sequence), full or with a sliding window and sinks.
+// Extend attention over the 8-bit paged cache (oscar_kv8_extend_varlen): the last rows of each sequence,
+// causal, full or with a sliding window and sinks, on tcgen05.
 //
-// One warp per (row, query head): lane l holds channels l, l + 32, ... of q and of the output,
-// positions one after another with an online softmax.
+// One CTA per (split, tile, KV head, sequence).  A tile is MT x 128 query rows, a row being one (position, query
+// head of the group): MT = 2 for prompts, 1 where a sequence has at most 128 rows (drafts).  The pages that any row
+// of the tile sees go through in blocks of 8 (128 tokens).  Roles of the 16 warps:
+//   warp 13       page ids and scales of the coming blocks; K and V codes into a ring by bulk copies;
+//   warps 8..11   codes -> fp16 (exact) K and V operands in shared memory, two blocks deep, once per CTA;
+//   warp 12       one thread issues S = Q K^T and O += P V (A = P from TMEM);
+//   warps 0..7    softmax, one thread per row, one warpgroup per 128 rows: 128 logits from TMEM, weights back to
+//                 TMEM as fp16 over the logits' own columns.
+// With MT = 2 the two row tiles alternate on the tensor cores: while one tile's softmax runs the other tile's
+// products do.  With MT = 1 the logits are double-buffered over blocks instead.
+// Scales stay out of the operands.  Q is scaled per row by a power of two to below 2, where fp16 holds
+// it to 2^-25 of the row's largest element; a page's K scale multiplies its 16 logits.  V codes carry the ratio of their page's scale to the
+// block's largest, vmax (a power of two, exact down to 2^-24), and the weights carry vmax / vref, vref the largest
+// scale so far.  Weights are p 2^7 vmax / vref, rounded to fp16 (11 bits: a tenth of the output's own
+// rounding), where p = 2^(s - m) <= 2^8 as the running maximum m is only moved when a logit passes it
+// by 8.  O is rescaled in TMEM when m or vref moves.  Sums are fp32 over the unrounded weights.
+// Bound by the tensor cores for long runs of rows, by the pages' bytes for short ones.
 #include <math.h>
 
 #include "kv8_attn.cuh"
+#include "umma.cuh"
 
 namespace {
 
 using namespace oscar;
 using namespace oscar::kv8;
 
-template <int F, int D>
-__global__ void __launch_bounds__(128) kv8_attn_kernel(AttnArgs a) {
-  constexpr int C = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int hq = blockIdx.y * 4 + (threadIdx.x >> 5);
-  const int b = blockIdx.z;
-  if (hq >= a.Hq) return;
-  const int L = clamped_len(a, b);
-  int row = b, pos = L - 1;
-  if (true) {
-    const int q0 = a.q_start[b], q1 = a.q_start[b + 1], n = q1 - q0;
-    if (n < 0 || n > a.max_rows || q0 < 0 || q1 > a.rows) {
-      record_error(OSCAR_DEVERR_POSITION);
-      return;
-    }
-    if (static_cast<int>(blockIdx.x) >= n) return;
-    row = q0 + blockIdx.x;
-    pos = L - n + blockIdx.x;
-    if (pos < 0) record_error(OSCAR_DEVERR_POSITION);
+constexpr int kThreads = 512;
+constexpr int kTok = 128;
+constexpr int kBlkPages = kTok / kPageSize;
+constexpr int kInfo = 8;          // blocks whose scales and positions are kept
+constexpr float kLazy = 8.f;      // log2: how far a logit may pass the maximum in use
+constexpr int kBoost = 7;         // weights are stored times 2^kBoost: 2^(kLazy + kBoost) < 65504
+constexpr int kFetchWarp = 13, kMmaWarp = 12;
+// Registers a thread: 512 x 128 at launch = 2 x 128 x 192 + 128 x 88 + 128 x 40
+constexpr int kRegsLaunch = 128;
+
+template <int D, int MT>
+struct Geo {
+  static constexpr uint32_t kOp = kTok * D * 2;   // one fp16 operand: D / 64 blocks of 128 rows x 128 bytes
+  static constexpr uint32_t kHalf = kTok * D;     // K or V codes of a block
+  static constexpr int kRing = D == 128 ? (MT == 2 ? 2 : 4) : 8;
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kK = MT * kOp;
+  static constexpr uint32_t kV = kK + 2 * kOp;
+  static constexpr uint32_t kRaw = kV + 2 * kOp;
+  static constexpr uint32_t kBars = kRaw + kRing * kHalf;
+  // raw full, raw empty | K full, K empty, V full, V empty (2 each) | S full (2) | P full, PV done (2 each) | info | end
+  static constexpr int kNumBars = 2 * kRing + 8 + 2 + 4 + kInfo + 1;
+  static constexpr uint32_t kScale = kBars + ((kNumBars * 8 + 15) & ~15);  // [kInfo][8] K, V scales, positions
+  static constexpr uint32_t kQs = kScale + kInfo * 3 * 32;
+  static constexpr uint32_t kMisc = kQs + MT * 128 * 4;
+  static constexpr size_t kSmem = 1024 + kMisc + 16;
+};
+
+struct ExtArgs {
+  AttnArgs a;
+  float* part_o;   // [rows x Hq][ns][D]
+  float* part_ml;  // [rows x Hq][ns][2]
+  int ns, bps, tiles;
+};
+
+// A tile's rows and the pages they see.
+struct Tile {
+  int q0, n, L, r0, rows;  // first query row and rows of the sequence, its length; first row of the tile, rows
+  Visible vis;
+  int blocks;
+  bool ok;
+};
+
+template <int TM>
+__device__ __forceinline__ Tile tile_of(const AttnArgs& a, int b, int tile) {
+  Tile t;
+  t.q0 = __ldg(a.q_start + b);
+  const int q1 = __ldg(a.q_start + b + 1);
+  t.n = q1 - t.q0;
+  t.ok = t.n >= 0 && t.n <= a.max_rows && t.q0 >= 0 && q1 <= a.rows;
+  if (!t.ok) {
+    record_error(OSCAR_DEVERR_POSITION);
+    return t;
   }
-  const int h = hq / (a.Hq / a.H);
-  const size_t rq = (static_cast<size_t>(row) * a.Hq + hq) * D;
-  float q[C], o[C], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    q[c] = __bfloat162float(a.q[rq + lane + 32 * c]);
-    o[c] = 0.f;
+  const int gqa = a.Hq / a.H;
+  t.r0 = tile * TM;
+  t.rows = min(TM, t.n * gqa - t.r0);
+  t.ok = t.rows > 0;
+  if (!t.ok) return t;
+  t.L = clamped_len(a, b);
+  const int first = t.L - t.n + t.r0 / gqa, last = t.L - t.n + (t.r0 + t.rows - 1) / gqa;
+  if (first < 0) record_error(OSCAR_DEVERR_POSITION);
+  t.vis = visible(max(first, 0), last, a.sink, a.window);
+  if (last < 0) t.vis.n = 0;
+  t.blocks = (t.vis.n + kBlkPages - 1) / kBlkPages;
+  return t;
+}
+
+template <uint32_t N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <uint32_t N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t half2_bits(float x, float y) {
+  const __half2 v = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int F, int D, int MT>
+__global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
+  using G = Geo<D, MT>;
+  extern __shared__ uint8_t raw_smem[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(sm);
+  const AttnArgs& a = ea.a;
+  const int split = blockIdx.x / ea.tiles, tile = ea.tiles - 1 - blockIdx.x % ea.tiles;  // the longest tiles first
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gqa = a.Hq / a.H;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const Tile T = tile_of<MT * 128>(a, b, tile);
+  if (!T.ok) return;
+  const int blk0 = split * ea.bps, cnt = min(ea.bps, T.blocks - blk0);
+  // output row (query row, head) of tile row r
+  auto out_row = [&](int r) {
+    const int x = T.r0 + r;
+    return static_cast<size_t>(T.q0 + x / gqa) * a.Hq + h * gqa + x % gqa;
+  };
+  if (cnt <= 0) {
+    if (split == 0)  // rows without any position
+      for (int i = tid; i < T.rows * (D / 8); i += kThreads)
+        reinterpret_cast<uint4*>(a.out + out_row(i / (D / 8)) * D)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+    return;
   }
-  const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-  const int sink_end = min(a.sink, lo);
-  for (int j = 0; j <= pos; ++j) {
-    if (j >= sink_end && j < lo) j = lo;
-    const int pid = a.page_table[static_cast<size_t>(b) * a.max_pages + j / kPageSize];
-    if (pid < 0 || pid >= a.num_pages) {
-      record_error(OSCAR_DEVERR_PAGE_ID);
-      continue;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + G::kBars);
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  constexpr int kRawFull = 0, kRawEmpty = G::kRing, kOpFull = 2 * G::kRing, kOpEmpty = kOpFull + 4,
+                kSFull = kOpEmpty + 4, kPFull = kSFull + 2, kPvDone = kPFull + 2, kInfoFull = kPvDone + 2,
+                kEnd = kInfoFull + kInfo;  // operand barriers: 2 x side + buffer
+  float* k_scale = reinterpret_cast<float*>(sm + G::kScale);
+  float* v_scale = k_scale + kInfo * 8;
+  int* page_pos = reinterpret_cast<int*>(v_scale + kInfo * 8);
+  float* q_scale = reinterpret_cast<float*>(sm + G::kQs);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(sm + G::kMisc);  // TMEM base
+  const int active = (T.rows + 127) / 128;
+  if (tid == 0) {
+    for (int i = 0; i < G::kRing; ++i) {
+      mbar_init(bar(kRawFull + i), 1);
+      mbar_init(bar(kRawEmpty + i), 128);
     }
-    const size_t block = (static_cast<size_t>(pid) * a.H + h) * 2;
-    const uint8_t* k = a.pages + block * (kPageSize * D) + (j % kPageSize) * D + lane;
-    const uint8_t* v = k + kPageSize * D;
-    float s = 0.f;
-    float x[4];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      decode4<F>(k[32 * c], x);
-      s = fmaf(q[c], x[0], s);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(kOpFull + i), 128);
+      mbar_init(bar(kOpEmpty + i), 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kSFull + i), 1);
+      mbar_init(bar(kPFull + i), 128);
+      mbar_init(bar(kPvDone + i), 1);
+    }
+    for (int i = 0; i < kInfo; ++i) mbar_init(bar(kInfoFull + i), 1);
+    mbar_init(bar(kEnd), 1);
+    mbar_init_fence();
+  }
+  if (warp == kMmaWarp) umma::tmem_alloc(smem_u32(misc), 512);
+  // Q as fp16, K-major with the 128-byte swizzle; a warp per row, lane l channels (D / 32) l ..
+  {
+    constexpr int kPer = D / 32;
+    for (int r = warp; r < MT * 128; r += kThreads / 32) {
+      uint32_t x[kPer / 2];
 #pragma unroll
-    for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= a.scales[block] * a.scale_log2;
-    const float m_new = fmaxf(m, s);
-    const float alpha = fast_exp2(m - m_new), p = fast_exp2(s - m_new);
-    m = m_new;
-    l = l * alpha + p;
+      for (int c = 0; c < kPer / 2; ++c) x[c] = 0u;
+      if (r < T.rows) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + out_row(r) * D) + lane * (kPer / 2);
+        if constexpr (kPer == 4) {
+          const uint2 y = __ldg(reinterpret_cast<const uint2*>(src));
+          x[0] = y.x;
+          x[1] = y.y;
+        } else {
+          x[0] = __ldg(src);
+        }
+      }
+      uint32_t mx = x[0] & 0x7fff7fffu;
+      if constexpr (kPer == 4) mx = __vmaxu2(mx, x[1] & 0x7fff7fffu);
+      mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+      const int e = min(max(static_cast<int>(mx >> 7) - 127, -126), 126);
+      const float inv = pow2i(-e);
+      uint32_t y[kPer / 2];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      decode4<F>(v[32 * c], x);
-      o[c] = o[c] * alpha + p * x[0] * a.scales[block + 1];
+      for (int c = 0; c < kPer / 2; ++c)
+        y[c] = half2_bits(__uint_as_float(x[c] << 16) * inv, __uint_as_float(x[c] & 0xffff0000u) * inv);
+      const uint32_t dst = sb + G::kQ + (r >> 7) * G::kOp + umma::sw128_offset(r & 127, lane * kPer, 128);
+      if constexpr (kPer == 4)
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(y[0]), "r"(y[1]) : "memory");
+      else
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(y[0]) : "memory");
+      if (lane == 0) q_scale[r] = pow2i(e) * a.scale_log2;
     }
   }
+  fence_async();
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  const uint32_t tmem = misc[0];
+  const uint32_t s_tmem[2] = {tmem, tmem + 128};       // logits / weights
+  const uint32_t o_tmem[2] = {tmem + 256, tmem + 256 + D};
+
+  const int wg = warp >> 2;
+  if (wg < 2) {
+    // ---- softmax ---------------------------------------------------------------------------
+    reg_inc<192>();
+    if (wg < active) {
+      const int r = wg * 128 + (tid & 127);
+      const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const float qs = q_scale[r];
+      const int last_r = min(T.rows, wg * 128 + 128) - 1;  // rows behind it are zeros and not stored
+      const int pos = T.L - T.n + (T.r0 + min(r, last_r)) / gqa;
+      const int after = a.window > 0 ? max(pos - a.window, -1) : -1;  // visible: behind it, or a sink
+      // what every row of this 128 sees: positions up to p_lo, and after p_hi_after (or in the sink)
+      const int p_lo = T.L - T.n + (T.r0 + wg * 128) / gqa;
+      const int p_hi = T.L - T.n + (T.r0 + last_r) / gqa;
+      const int hi_after = a.window > 0 ? max(p_hi - a.window, -1) : -1;
+      float m = -INFINITY, l = 0.f, vref = 0.f;
+      bool ok = true;
+      for (int j = 0; j < cnt && ok; ++j) {
+        const int sbuf = MT == 2 ? wg : j & 1;
+        const int info = j & (kInfo - 1);
+        ok = mbar_wait_bounded(bar(kInfoFull + info), (j / kInfo) & 1) &&
+             mbar_wait_bounded(bar(kSFull + sbuf), MT == 2 ? j & 1 : (j >> 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        umma::fence_after_sync();
+        uint32_t v[4][32];
 #pragma unroll
-  for (int c = 0; c < C; ++c) a.out[rq + lane + 32 * c] = __float2bfloat16_rn(l > 0.f ? o[c] / l : 0.f);
+        for (int c = 0; c < 4; ++c) umma::tmem_ld32(s_tmem[sbuf] + t_lane + 32 * c, v[c]);
+        umma::tmem_ld_wait();
+        float ks[8];
+        int pp[8];
+        float vmax = 0.f;
+        bool full = true;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          ks[c] = fmaxf(k_scale[info * 8 + c] * qs, 1.2e-38f);  // (never 0: -inf stays -inf)
+          pp[c] = page_pos[info * 8 + c];
+          vmax = fmaxf(vmax, v_scale[info * 8 + c]);
+          full = full && pp[c] <= p_lo - (kPageSize - 1) && (pp[c] > hi_after || pp[c] + kPageSize <= a.sink);
+        }
+        if (!full) {
+#pragma unroll
+          for (int pg = 0; pg < 8; ++pg) {
+            const int c_hi = pos - pp[pg], c_lo = after - pp[pg], c_sink = a.sink - pp[pg];
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              if (c > c_hi || (c <= c_lo && c >= c_sink)) v[pg >> 1][(pg & 1) * 16 + c] = 0xff800000u;
+          }
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int pg = 0; pg < 8; ++pg) {
+          const uint32_t* x = &v[pg >> 1][(pg & 1) * 16];
+          float y = __uint_as_float(x[0]);
+#pragma unroll
+          for (int c = 1; c + 1 < 16; c += 2) y = fmax3(y, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+          y = fmaxf(y, __uint_as_float(x[15]));
+          mx = fmaxf(mx, y * ks[pg]);
+        }
+        const bool move = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
+        const bool v_move = vmax > vref;
+        if (__any_sync(0xffffffffu, move) || v_move) {
+          const float m_new = move ? mx : m;
+          const float am = move ? (m == -INFINITY ? 0.f : fast_exp2(m - m_new)) : 1.f;
+          l *= am;
+          m = m_new;
+          float alpha = am;
+          if (v_move) {
+            alpha *= vref / vmax;
+            vref = vmax;
+          }
+          if (j > 0) {
+            ok = mbar_wait_bounded(bar(kPvDone + (MT == 2 ? wg : 0)), (j - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              break;
+            }
+            umma::fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              umma::tmem_ld16(o_tmem[wg] + t_lane + 16 * c, o);
+              umma::tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              umma::tmem_st16(o_tmem[wg] + t_lane + 16 * c, o);
+            }
+          }
+        }
+        // weights: 2^(s - m + lb), lb = kBoost + log2(vmax / vref)
+        const int lb = vref > 0.f ? max(kBoost + static_cast<int>(__float_as_uint(vmax) >> 23) -
+                                            static_cast<int>(__float_as_uint(vref) >> 23), -110)
+                                  : 0;
+        const float off = static_cast<float>(lb) - (m == -INFINITY ? 0.f : m);
+        const float2 off2 = make_float2(off, off);
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t p[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int col = half * 64 + 2 * c;
+            const float k = ks[col >> 4];
+            const float2 e = f2fma(make_float2(__uint_as_float(v[col >> 5][col & 31]),
+                                               __uint_as_float(v[col >> 5][(col & 31) + 1])),
+                                   make_float2(k, k), off2);
+            const float2 w = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+            sum = f2add(sum, w);
+            p[c] = half2_bits(w.x, w.y);
+          }
+          umma::tmem_st32(s_tmem[sbuf] + t_lane + 32 * half, p);
+        }
+        umma::tmem_st_wait();
+        umma::fence_before_sync();
+        mbar_arrive(bar(kPFull + (MT == 2 ? wg : 0)));
+        l = fmaf(sum.x + sum.y, pow2i(-lb), l);
+      }
+      if (ok) ok = mbar_wait_bounded(bar(kPvDone + (MT == 2 ? wg : 0)), (cnt - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok && lane == 0) record_error(OSCAR_DEVERR_TIMEOUT);
+      umma::fence_after_sync();
+      const bool single = T.blocks <= ea.bps;
+      const bool store = r < T.rows;
+      const size_t row = store ? out_row(r) : 0;
+      const float unit = ok ? vref * (1.f / (1 << kBoost)) : 0.f;
+      if (!ok) l = 0.f;
+      const float inv = l > 0.f ? unit / l : 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t o[16];
+        __syncwarp();
+        umma::tmem_ld16(o_tmem[wg] + t_lane + 16 * c, o);
+        umma::tmem_ld_wait();
+        if (store && single) {
+          uint32_t y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const __nv_bfloat162 z = __floats2bfloat162_rn(l > 0.f ? __uint_as_float(o[2 * e]) * inv : 0.f,
+                                                           l > 0.f ? __uint_as_float(o[2 * e + 1]) * inv : 0.f);
+            y[e] = *reinterpret_cast<const uint32_t*>(&z);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + 16 * c);
+          dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+          dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+        } else if (store) {
+          float4* dst = reinterpret_cast<float4*>(ea.part_o + (row * ea.ns + split) * D + 16 * c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[e] = l > 0.f ? make_float4(__uint_as_float(o[4 * e]) * unit, __uint_as_float(o[4 * e + 1]) * unit,
+                                           __uint_as_float(o[4 * e + 2]) * unit, __uint_as_float(o[4 * e + 3]) * unit)
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+      if (store && !single)
+        *reinterpret_cast<float2*>(ea.part_ml + (row * ea.ns + split) * 2) =
+            make_float2(l > 0.f ? m : -INFINITY, l);
+    }
+  } else if (wg == 2) {
+    // ---- codes -> fp16 operands ---------------------------------------------------------------
+    reg_dec<88>();
+    const int pt = tid - 256;
+    constexpr int kChunks = D / 16;                    // 16-byte chunks of a row of codes
+    constexpr int kUnits = kTok * kChunks / 128;       // per thread
+    bool ok = true;
+    for (int j = 0; j < cnt && ok; ++j) {
+      const int info = j & (kInfo - 1);
+      for (int side = 0; side < 2 && ok; ++side) {
+        const int hf = 2 * j + side, st = hf % G::kRing, op = 2 * side + (j & 1);
+        ok = mbar_wait_bounded(bar(kRawFull + st), (hf / G::kRing) & 1) &&
+             (j < 2 || mbar_wait_bounded(bar(kOpEmpty + op), ((j >> 1) - 1) & 1));
+        if (!ok) break;
+        float vmax = 0.f;
+        if (side == 1) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) vmax = fmaxf(vmax, v_scale[info * 8 + c]);
+        }
+        const float inv = vmax > 0.f ? 1.f / vmax : 0.f;  // exact: a power of two
+        const uint32_t src = sb + G::kRaw + st * G::kHalf;
+        const uint32_t dst = sb + (side ? G::kV : G::kK) + (j & 1) * G::kOp;
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+          const int u = i * 128 + pt, r = u / kChunks, c = u % kChunks;
+          uint32_t w[4], y[8];
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(src + u * 16)
+                       : "memory");
+          if (side == 1) {
+            const int p0 = page_pos[info * 8 + (r >> 4)];
+            if (p0 + (r & 15) >= T.L || p0 < 0) w[0] = w[1] = w[2] = w[3] = 0u;  // any bits: behind the last token, no page
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) codes_to_f16<F>(w[e], y[2 * e], y[2 * e + 1]);
+          if (side == 1) {
+            const float ratio = v_scale[info * 8 + (r >> 4)] * inv;
+            if (ratio != 1.f) {
+              const __half2 f = __float2half2_rn(ratio);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&y[e]), f);
+                y[e] = *reinterpret_cast<const uint32_t*>(&z);
+              }
+            }
+          }
+          // channels 16 c .. + 15 of row r: two 16-byte chunks of 64-channel block c / 4.  Lanes of the second
+          // block write their second chunk first, so that the eight lanes of a row meet eight banks.
+          const uint32_t row = dst + (c >> 2) * (kTok * 128) + r * 128;
+          const int c0 = 2 * (c & 3), sw = r & 7;
+          const bool flip = D == 128 && c >= 4;
+          const uint32_t a0 = row + ((c0 ^ sw) << 4), a1 = row + (((c0 + 1) ^ sw) << 4);
+          st_shared_v4(flip ? a1 : a0, flip ? y[4] : y[0], flip ? y[5] : y[1], flip ? y[6] : y[2], flip ? y[7] : y[3]);
+          st_shared_v4(flip ? a0 : a1, flip ? y[0] : y[4], flip ? y[1] : y[5], flip ? y[2] : y[6], flip ? y[3] : y[7]);
+        }
+        fence_async();
+        mbar_arrive(bar(kOpFull + op));
+        mbar_arrive(bar(kRawEmpty + st));
+      }
+    }
+    if (!ok && lane == 0) record_error(OSCAR_DEVERR_TIMEOUT);
+  } else {
+    reg_dec<40>();
+    if (warp == kFetchWarp) {
+      // ---- page ids, scales, copies of codes -------------------------------------------------------
+      const int32_t* table = a.page_table + static_cast<size_t>(b) * a.max_pages;
+      int pid = -1, base = -1;
+      float2 sc = make_float2(1.f, 0.f);
+      auto look_up = [&](int j) {  // lane < 8: page lane of block j
+        const int v = (blk0 + j) * kBlkPages + lane;
+        pid = -1;
+        base = -1;
+        sc = make_float2(1.f, 0.f);
+        if (lane < kBlkPages && j < cnt && v < T.vis.n) {
+          const int page = T.vis.page(v);
+          pid = __ldg(table + page);
+          if (pid < 0 || pid >= a.num_pages) {
+            record_error(OSCAR_DEVERR_PAGE_ID);
+            pid = -1;
+          } else {
+            base = page * kPageSize;
+            sc = __ldg(reinterpret_cast<const float2*>(a.scales) + static_cast<size_t>(pid) * a.H + h);
+          }
+        }
+      };
+      look_up(0);
+      bool ok = true;
+      int issued = 0;
+      for (int j = 0; j < cnt && ok; ++j) {
+        const int info = j & (kInfo - 1);
+        const int id = pid;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * (kPageSize * D);
+        const float2 s_now = sc;
+        const int b_now = base;
+        look_up(j + 1);
+        for (int side = 0; side < 2; ++side) {
+          const int hf = 2 * j + side, st = hf % G::kRing;
+          if (hf >= G::kRing) ok = mbar_wait_bounded(bar(kRawEmpty + st), (hf / G::kRing - 1) & 1);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          if (side == 0) {
+            // (block j - 8's readers are done: their weights came before the products that freed this stage)
+            if (lane < kBlkPages) {
+              k_scale[info * 8 + lane] = s_now.x;
+              v_scale[info * 8 + lane] = s_now.y;
+              page_pos[info * 8 + lane] = b_now < 0 ? 0x7fffffff - kPageSize : b_now;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kInfoFull + info));
+          }
+          if (lane == 0) {
+            if (bytes > 0) mbar_arrive_expect_tx(bar(kRawFull + st), bytes);
+            else mbar_arrive(bar(kRawFull + st));
+          }
+          __syncwarp();
+          if (id >= 0)
+            bulk_g2s(sb + G::kRaw + st * G::kHalf + lane * (kPageSize * D),
+                     a.pages + ((static_cast<size_t>(id) * a.H + h) * 2 + side) * (kPageSize * D), kPageSize * D,
+                     bar(kRawFull + st));
+          issued = hf + 1;
+        }
+      }
+      if (!ok) {  // wait for the copies in flight
+        if (lane == 0) record_error(OSCAR_DEVERR_TIMEOUT);
+        for (int hf = max(0, issued - G::kRing); hf < issued; ++hf)
+          mbar_wait_bounded(bar(kRawFull + hf % G::kRing), (hf / G::kRing) & 1);
+      }
+    } else if (warp == kMmaWarp && lane == 0) {
+      // ---- products ---------------------------------------------------------------------------------
+      constexpr uint32_t kIdQk = umma::idesc_f16_f32(128, kTok, false), kIdPv = umma::idesc_f16_f32_b_mn(128, D);
+      bool ok = true;
+      auto wait = [&](int i, int parity) {
+        if (ok) ok = mbar_wait_bounded(bar(i), parity & 1);
+        umma::fence_after_sync();
+      };
+      auto qk = [&](int t, int j, int sbuf) {
+        const uint32_t qb = sb + G::kQ + t * G::kOp, kb = sb + G::kK + (j & 1) * G::kOp;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * (kTok * 128) + (ks & 3) * 32;
+          umma::mma_bf16(s_tmem[sbuf], umma::desc_k_sw128(qb + off), umma::desc_k_sw128(kb + off), kIdQk, ks > 0);
+        }
+        umma::commit(bar(kSFull + sbuf));
+      };
+      auto pv = [&](int t, int j, int sbuf) {
+        const uint32_t vb = sb + G::kV + (j & 1) * G::kOp;
+#pragma unroll
+        for (int ks = 0; ks < kTok / 16; ++ks)
+          umma::mma_f16_ts(o_tmem[t], s_tmem[sbuf] + ks * 8, umma::desc_mn_sw128(vb + ks * 2048, kTok * 128), kIdPv,
+                           j > 0 || ks > 0);
+        umma::commit(bar(kPvDone + t));
+      };
+      const int nt = MT == 2 ? active : 1;
+      wait(kOpFull + 0, 0);
+      if (ok)
+        for (int t = 0; t < nt; ++t) qk(t, 0, t);
+      if (ok) umma::commit(bar(kOpEmpty + 0));
+      for (int j = 0; j < cnt && ok; ++j) {
+        const bool more = j + 1 < cnt;
+        if (MT == 1) {
+          if (more) {
+            wait(kOpFull + ((j + 1) & 1), (j + 1) >> 1);
+            if (!ok) break;
+            qk(0, j + 1, (j + 1) & 1);
+            umma::commit(bar(kOpEmpty + ((j + 1) & 1)));
+          }
+          wait(kPFull + 0, j);
+          wait(kOpFull + 2 + (j & 1), j >> 1);
+          if (!ok) break;
+          pv(0, j, j & 1);
+          umma::commit(bar(kOpEmpty + 2 + (j & 1)));
+        } else {
+          for (int t = 0; t < nt && ok; ++t) {
+            wait(kPFull + t, j);
+            if (t == 0) wait(kOpFull + 2 + (j & 1), j >> 1);
+            if (!ok) break;
+            pv(t, j, t);
+            if (t == nt - 1) umma::commit(bar(kOpEmpty + 2 + (j & 1)));
+            if (more) {
+              if (t == 0) wait(kOpFull + ((j + 1) & 1), (j + 1) >> 1);
+              if (!ok) break;
+              qk(t, j + 1, t);
+              if (t == nt - 1) umma::commit(bar(kOpEmpty + ((j + 1) & 1)));
+            }
+          }
+        }
+      }
+      if (!ok) record_error(OSCAR_DEVERR_TIMEOUT);
+      umma::commit(bar(kEnd));  // every product is over before TMEM is freed
+      mbar_wait_bounded(bar(kEnd), 0);
+    }
+  }
+  __syncwarp();
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  if (warp == kMmaWarp) umma::tmem_dealloc(tmem, 512);
+}
+
+// One CTA per (tile, KV head, sequence): the merge of its rows' splits, a warp per row.
+template <int D, int TM>
+__global__ void __launch_bounds__(256) kv8_extend_merge_kernel(ExtArgs ea) {
+  const AttnArgs& a = ea.a;
+  grid_dep_wait();
+  const Tile T = tile_of<TM>(a, blockIdx.z, blockIdx.x);
+  if (!T.ok) return;
+  const int n = (T.blocks + ea.bps - 1) / ea.bps;
+  if (n <= 1) return;  // written by the attention kernel
+  const int gqa = a.Hq / a.H, lane = threadIdx.x & 31;
+  for (int r = threadIdx.x >> 5; r < T.rows; r += 8) {
+    const int x = T.r0 + r;
+    const size_t row = static_cast<size_t>(T.q0 + x / gqa) * a.Hq + blockIdx.y * gqa + x % gqa;
+    merge_row<D>(ea.part_o + row * ea.ns * D, ea.part_ml + row * ea.ns * 2, n, a.out + row * D, lane);
+  }
+}
+
+struct Plan {
+  int mt, tiles, ns, bps;
+  size_t off_ml, total;
+};
+
+bool make_plan(const oscar_dims_t* d, int batch, int rows, int max_seq_len, int max_rows, int pps, int sink, int window,
+               Plan* p) {
+  if (check_dims(d) != OSCAR_OK || batch < 0 || batch > 65535 || rows < 0 || max_rows < 0 || max_seq_len < 0 ||
+      pps < 0 || sink < 0 || window < 0)
+    return false;
+  if (max_seq_len > static_cast<long long>(d->max_pages_per_seq) * kPageSize || d->num_kv_heads > 65535) return false;
+  const int gqa = d->num_q_heads / d->num_kv_heads;
+  if (max_rows > rows) max_rows = rows;
+  const long long per_seq = static_cast<long long>(max_rows) * gqa;
+  p->mt = per_seq > 128 ? 2 : 1;
+  const int tm = 128 * p->mt;
+  const long long tiles = (per_seq + tm - 1) / tm;
+  const long long pages = max_visible_pages(max_seq_len, sink, window, tm / gqa + 1);
+  const long long blocks = (pages + kBlkPages - 1) / kBlkPages;
+  long long bps;
+  if (pps > 0) {
+    bps = (pps + kBlkPages - 1) / kBlkPages;
+  } else {
+    // tiles that have rows: at most one ragged tile per sequence beyond the even ones
+    long long units = static_cast<long long>(rows) * gqa / tm + batch;
+    if (units > tiles * batch) units = tiles * batch;
+    units *= d->num_kv_heads;
+    const long long want = (p->mt == 1 ? 4LL : 2LL) * num_sms();
+    const long long splits = units > 0 && units < want ? want / units : 1;
+    bps = (blocks + splits - 1) / splits;
+    if (bps < 4) bps = 4;
+  }
+  if (bps < 1) bps = 1;
+  const long long ns = blocks > 0 ? (blocks + bps - 1) / bps : 1;
+  if (ns > 65535 || tiles * ns > 0x7fffffffLL || bps > 0x7fffffffLL / kBlkPages) return false;
+  p->tiles = static_cast<int>(tiles > 0 ? tiles : 1);
+  p->ns = static_cast<int>(ns);
+  p->bps = static_cast<int>(bps);
+  const size_t parts = ns > 1 ? static_cast<size_t>(rows) * d->num_q_heads * ns : 0;
+  p->off_ml = align_up(parts * d->head_dim * sizeof(float), 256);
+  p->total = p->off_ml + align_up(parts * 2 * sizeof(float), 256) + 256;
+  return true;
+}
+
+// Whether the kernel has the launch registers that its warpgroups divide among themselves (if it had
+// fewer, they would wait for registers that nobody gives back).
+bool has_launch_registers(const void* f) {
+  cudaFuncAttributes at{};
+  return cudaFuncGetAttributes(&at, f) == cudaSuccess && at.numRegs == kRegsLaunch;
+}
+
+template <int F, int D, int MT>
+cudaError_t launch(const ExtArgs& ea, cudaStream_t stream) {
+  auto k = kv8_extend_kernel<F, D, MT>;
+  static const bool regs = has_launch_registers(reinterpret_cast<const void*>(k));
+  if (!regs) return cudaErrorInvalidConfiguration;
+  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(k), Geo<D, MT>::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(k, dim3(static_cast<unsigned>(ea.tiles * ea.ns), ea.a.H, ea.a.batch), dim3(kThreads),
+                 Geo<D, MT>::kSmem, stream, ea);
+  if (e != cudaSuccess || ea.ns == 1) return e;
+  return launch_pdl(kv8_extend_merge_kernel<D, MT * 128>, dim3(ea.tiles, ea.a.H, ea.a.batch), dim3(256), 0, stream, ea);
 }
 
 template <int F, int D>
-void launch(const AttnArgs& a, cudaStream_t stream) {
-  kv8_attn_kernel<F, D><<<dim3(a.max_rows, (a.Hq + 3) / 4, a.batch), 128, 0, stream>>>(a);
+cudaError_t launch_mt(int mt, const ExtArgs& ea, cudaStream_t stream) {
+  return mt == 2 ? launch<F, D, 2>(ea, stream) : launch<F, D, 1>(ea, stream);
 }
 
 }  // namespace
@@ -87,8 +668,10 @@ extern "C" size_t oscar_kv8_extend_varlen_workspace_bytes(const oscar_dims_t* di
                                                           int32_t max_seq_len, int32_t max_rows_per_seq,
                                                           int32_t pages_per_split, int32_t sink_len,
                                                           int32_t window_len) {
-  if (num_rows < 0 || max_rows_per_seq < 0) return 0;
-  return oscar_kv8_decode_workspace_bytes(dims, batch, max_seq_len, pages_per_split, sink_len, window_len);
+  Plan p;
+  return make_plan(dims, batch, num_rows, max_seq_len, max_rows_per_seq, pages_per_split, sink_len, window_len, &p)
+             ? p.total
+             : 0;
 }
 
 extern "C" oscar_status_t oscar_kv8_extend_varlen(const oscar_dims_t* dims, int32_t kv_format, int32_t batch,
@@ -98,26 +681,36 @@ extern "C" oscar_status_t oscar_kv8_extend_varlen(const oscar_dims_t* dims, int3
                                                   const int32_t* page_table, const int32_t* seq_lens,
                                                   int32_t sink_len, int32_t window_len, float sm_scale, void* out,
                                                   void* workspace, size_t workspace_bytes, void* stream) {
-  const oscar_status_t st = check_dims(dims);
+  oscar_status_t st = check_dims(dims);
   if (st != OSCAR_OK) return st;
   if (bad_format(kv_format) || batch < 0 || num_rows < 0 || max_seq_len < 0 || max_rows_per_seq < 0 ||
       pages_per_split < 0 || sink_len < 0 || window_len < 0)
     return OSCAR_ERR_INVALID_ARG;
   if (num_rows == 0) return OSCAR_OK;
   if (batch == 0 || max_rows_per_seq == 0 || !q_start) return OSCAR_ERR_INVALID_ARG;
-  const size_t need = oscar_kv8_extend_varlen_workspace_bytes(dims, batch, num_rows, max_seq_len, max_rows_per_seq,
-                                                              pages_per_split, sink_len, window_len);
-  if (need == 0) return OSCAR_ERR_INVALID_ARG;
-  AttnArgs a;
-  const oscar_status_t sa = make_args(dims, batch, num_rows, max_rows_per_seq, max_seq_len, q, q_start, kv8_pages,
-                                      kv8_scales, page_table, seq_lens, sink_len, window_len, sm_scale, out, workspace,
-                                      need, workspace_bytes, &a);
-  if (sa != OSCAR_OK) return sa;
+  Plan plan;
+  if (!make_plan(dims, batch, num_rows, max_seq_len, max_rows_per_seq, pages_per_split, sink_len, window_len, &plan))
+    return OSCAR_ERR_INVALID_ARG;
+  if (static_cast<long long>(max_rows_per_seq) * (dims->num_q_heads / dims->num_kv_heads) > 0x7fffffffLL ||
+      static_cast<long long>(num_rows) * (dims->num_q_heads / dims->num_kv_heads) > 0x7fffffffLL - 256)
+    return OSCAR_ERR_UNSUPPORTED;
+  ExtArgs ea;
+  st = make_args(dims, batch, num_rows, max_rows_per_seq < num_rows ? max_rows_per_seq : num_rows, max_seq_len, q,
+                 q_start, kv8_pages, kv8_scales, page_table, seq_lens, sink_len, window_len, sm_scale, out, workspace,
+                 plan.total, workspace_bytes, &ea.a);
+  if (st != OSCAR_OK) return st;
+  char* w = static_cast<char*>(workspace);
+  ea.part_o = reinterpret_cast<float*>(w);
+  ea.part_ml = reinterpret_cast<float*>(w + plan.off_ml);
+  ea.ns = plan.ns;
+  ea.bps = plan.bps;
+  ea.tiles = plan.tiles;
   cudaStream_t s = as_stream(stream);
   const bool d128 = dims->head_dim == 128;
-  if (kv_format == OSCAR_KV8_E4M3) d128 ? launch<kE4M3, 128>(a, s) : launch<kE4M3, 64>(a, s);
-  else d128 ? launch<kInt8, 128>(a, s) : launch<kInt8, 64>(a, s);
-  return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
+  const cudaError_t e = kv_format == OSCAR_KV8_E4M3
+                            ? (d128 ? launch_mt<kE4M3, 128>(plan.mt, ea, s) : launch_mt<kE4M3, 64>(plan.mt, ea, s))
+                            : (d128 ? launch_mt<kInt8, 128>(plan.mt, ea, s) : launch_mt<kInt8, 64>(plan.mt, ea, s));
+  return e == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
 oscar_status_t oscar_internal_kv8_extend_errors(uint32_t* flags, int reset) {

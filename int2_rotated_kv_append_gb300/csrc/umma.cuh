@@ -104,6 +104,20 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
+// kind::f16 with fp16 operands, A from TMEM (128 lanes, two fp16 a column), B in shared
+// memory: instruction descriptor, B MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16_f32_b_mn(int M, int N) { return idesc_f16_f32(M, N, false) | (1u << 16); }
+
+// One thread: D[tmem] (+)= A[tmem] . B[smem].
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // One thread: the mbarrier receives one arrival once every MMA this thread has
 // issued so far has completed.
 __device__ __forceinline__ void commit(uint32_t bar) {
