@@ -35,8 +35,10 @@ constexpr int kInfo = 8;          // blocks whose scales and positions are kept
 constexpr float kLazy = 8.f;      // log2: how far a logit may pass the maximum in use
 constexpr int kBoost = 7;         // weights are stored times 2^kBoost: 2^(kLazy + kBoost) < 65504
 constexpr int kFetchWarp = 13, kMmaWarp = 12;
-// Registers a thread: 512 x 128 at launch = 2 x 128 x 192 + 128 x 88 + 128 x 40
+// Registers a thread: 512 x 128 at launch, divided as 2 x 128 x 184 + 128 x 80 + 128 x 64
 constexpr int kRegsLaunch = 128;
+constexpr int kRegsSoftmax = 184, kRegsExpand = 80, kRegsIssue = 64;
+static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsIssue == 4 * kRegsLaunch, "the warpgroups share what was launched");
 
 template <int D, int MT>
 struct Geo {
@@ -175,36 +177,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
   if (warp == kMmaWarp) umma::tmem_alloc(smem_u32(misc), 512);
   // Q as fp16, K-major with the 128-byte swizzle; a warp per row, lane l channels (D / 32) l ..
   {
-    constexpr int kPer = D / 32;
-    for (int r = warp; r < MT * 128; r += kThreads / 32) {
-      uint32_t x[kPer / 2];
+    constexpr int kPer = D / 32, kWords = kPer / 2, kBatch = 8;  // rows whose loads are in flight at once
+    for (int r0 = warp; r0 < active * 128; r0 += kBatch * (kThreads / 32)) {
+      uint32_t x[kBatch][kWords];
 #pragma unroll
-      for (int c = 0; c < kPer / 2; ++c) x[c] = 0u;
-      if (r < T.rows) {
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + out_row(r) * D) + lane * (kPer / 2);
-        if constexpr (kPer == 4) {
-          const uint2 y = __ldg(reinterpret_cast<const uint2*>(src));
-          x[0] = y.x;
-          x[1] = y.y;
-        } else {
-          x[0] = __ldg(src);
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + i * (kThreads / 32);
+#pragma unroll
+        for (int c = 0; c < kWords; ++c) x[i][c] = 0u;
+        if (r < T.rows) {
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + out_row(r) * D) + lane * kWords;
+          if constexpr (kWords == 2) {
+            const uint2 y = __ldg(reinterpret_cast<const uint2*>(src));
+            x[i][0] = y.x;
+            x[i][1] = y.y;
+          } else {
+            x[i][0] = __ldg(src);
+          }
         }
       }
-      uint32_t mx = x[0] & 0x7fff7fffu;
-      if constexpr (kPer == 4) mx = __vmaxu2(mx, x[1] & 0x7fff7fffu);
-      mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
-      const int e = min(max(static_cast<int>(mx >> 7) - 127, -126), 126);
-      const float inv = pow2i(-e);
-      uint32_t y[kPer / 2];
 #pragma unroll
-      for (int c = 0; c < kPer / 2; ++c)
-        y[c] = half2_bits(__uint_as_float(x[c] << 16) * inv, __uint_as_float(x[c] & 0xffff0000u) * inv);
-      const uint32_t dst = sb + G::kQ + (r >> 7) * G::kOp + umma::sw128_offset(r & 127, lane * kPer, 128);
-      if constexpr (kPer == 4)
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(y[0]), "r"(y[1]) : "memory");
-      else
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(y[0]) : "memory");
-      if (lane == 0) q_scale[r] = pow2i(e) * a.scale_log2;
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + i * (kThreads / 32);
+        uint32_t mx = x[i][0] & 0x7fff7fffu;
+        if constexpr (kWords == 2) mx = __vmaxu2(mx, x[i][1] & 0x7fff7fffu);
+        mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+        const int e = min(max(static_cast<int>(mx >> 7) - 127, -126), 126);
+        const float inv = pow2i(-e);
+        uint32_t y[kWords];
+#pragma unroll
+        for (int c = 0; c < kWords; ++c)
+          y[c] = half2_bits(__uint_as_float(x[i][c] << 16) * inv, __uint_as_float(x[i][c] & 0xffff0000u) * inv);
+        const uint32_t dst = sb + G::kQ + (r >> 7) * G::kOp + umma::sw128_offset(r & 127, lane * kPer, 128);
+        if constexpr (kWords == 2)
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(y[0]), "r"(y[1]) : "memory");
+        else
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(y[0]) : "memory");
+        if (lane == 0) q_scale[r] = pow2i(e) * a.scale_log2;
+      }
     }
   }
   fence_async();
@@ -218,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
   const int wg = warp >> 2;
   if (wg < 2) {
     // ---- softmax ---------------------------------------------------------------------------
-    reg_inc<192>();
+    reg_inc<kRegsSoftmax>();
     if (wg < active) {
       const int r = wg * 128 + (tid & 127);
       const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -247,20 +257,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
         for (int c = 0; c < 4; ++c) umma::tmem_ld32(s_tmem[sbuf] + t_lane + 32 * c, v[c]);
         umma::tmem_ld_wait();
         float ks[8];
-        int pp[8];
         float vmax = 0.f;
         bool full = true;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           ks[c] = fmaxf(k_scale[info * 8 + c] * qs, 1.2e-38f);  // (never 0: -inf stays -inf)
-          pp[c] = page_pos[info * 8 + c];
           vmax = fmaxf(vmax, v_scale[info * 8 + c]);
-          full = full && pp[c] <= p_lo - (kPageSize - 1) && (pp[c] > hi_after || pp[c] + kPageSize <= a.sink);
+          const int pp = page_pos[info * 8 + c];
+          full = full && pp <= p_lo - (kPageSize - 1) && (pp > hi_after || pp + kPageSize <= a.sink);
         }
         if (!full) {
 #pragma unroll
           for (int pg = 0; pg < 8; ++pg) {
-            const int c_hi = pos - pp[pg], c_lo = after - pp[pg], c_sink = a.sink - pp[pg];
+            const int pp = page_pos[info * 8 + pg];
+            const int c_hi = pos - pp, c_lo = after - pp, c_sink = a.sink - pp;
 #pragma unroll
             for (int c = 0; c < 16; ++c)
               if (c > c_hi || (c <= c_lo && c >= c_sink)) v[pg >> 1][(pg & 1) * 16 + c] = 0xff800000u;
@@ -330,6 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           umma::tmem_st32(s_tmem[sbuf] + t_lane + 32 * half, p);
         }
         umma::tmem_st_wait();
+        // every phase of this barrier is waited for in its turn (a parity says nothing two phases ahead)
+        if (j > 0 && !mbar_wait_bounded(bar(kPvDone + (MT == 2 ? wg : 0)), (j - 1) & 1)) ok = false;
         umma::fence_before_sync();
         mbar_arrive(bar(kPFull + (MT == 2 ? wg : 0)));
         l = fmaf(sum.x + sum.y, pow2i(-lb), l);
@@ -376,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
     }
   } else if (wg == 2) {
     // ---- codes -> fp16 operands ---------------------------------------------------------------
-    reg_dec<88>();
+    reg_dec<kRegsExpand>();
     const int pt = tid - 256;
     constexpr int kChunks = D / 16;                    // 16-byte chunks of a row of codes
     constexpr int kUnits = kTok * kChunks / 128;       // per thread
@@ -437,39 +449,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
     }
     if (!ok && lane == 0) record_error(OSCAR_DEVERR_TIMEOUT);
   } else {
-    reg_dec<40>();
+    reg_dec<kRegsIssue>();
     if (warp == kFetchWarp) {
       // ---- page ids, scales, copies of codes -------------------------------------------------------
       const int32_t* table = a.page_table + static_cast<size_t>(b) * a.max_pages;
-      int pid = -1, base = -1;
-      float2 sc = make_float2(1.f, 0.f);
-      auto look_up = [&](int j) {  // lane < 8: page lane of block j
-        const int v = (blk0 + j) * kBlkPages + lane;
-        pid = -1;
-        base = -1;
-        sc = make_float2(1.f, 0.f);
-        if (lane < kBlkPages && j < cnt && v < T.vis.n) {
-          const int page = T.vis.page(v);
-          pid = __ldg(table + page);
-          if (pid < 0 || pid >= a.num_pages) {
-            record_error(OSCAR_DEVERR_PAGE_ID);
-            pid = -1;
-          } else {
-            base = page * kPageSize;
-            sc = __ldg(reinterpret_cast<const float2*>(a.scales) + static_cast<size_t>(pid) * a.H + h);
-          }
-        }
+      // Four blocks at a time, a page a lane: the ids are loaded two groups ahead and the scales one,
+      // so that neither is waited for.
+      auto look_up = [&](int g) {  // page id (-1: none)
+        const int v = blk0 * kBlkPages + g * 32 + lane;
+        return g * 32 + lane < cnt * kBlkPages && v < T.vis.n ? __ldg(table + T.vis.page(v)) : -2;
       };
-      look_up(0);
+      auto checked = [&](int id) {
+        if (id != -2 && (id < 0 || id >= a.num_pages)) record_error(OSCAR_DEVERR_PAGE_ID);
+        return id >= 0 && id < a.num_pages ? id : -1;
+      };
+      auto scales = [&](int id) {
+        return id >= 0 ? __ldg(reinterpret_cast<const float2*>(a.scales) + static_cast<size_t>(id) * a.H + h)
+                       : make_float2(1.f, 0.f);
+      };
+      int pid = -1, pid1 = checked(look_up(0)), pid2 = look_up(1);
+      float2 sc = make_float2(1.f, 0.f), sc1 = scales(pid1);
       bool ok = true;
       int issued = 0;
       for (int j = 0; j < cnt && ok; ++j) {
         const int info = j & (kInfo - 1);
-        const int id = pid;
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * (kPageSize * D);
-        const float2 s_now = sc;
-        const int b_now = base;
-        look_up(j + 1);
+        if ((j & 3) == 0) {
+          pid = pid1;
+          sc = sc1;
+          pid1 = checked(pid2);
+          sc1 = scales(pid1);
+          pid2 = look_up((j >> 2) + 2);
+        }
+        const bool mine = (lane >> 3) == (j & 3);  // this lane holds a page of block j
+        const bool have = mine && pid >= 0;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, have)) * (kPageSize * D);
         for (int side = 0; side < 2; ++side) {
           const int hf = 2 * j + side, st = hf % G::kRing;
           if (hf >= G::kRing) ok = mbar_wait_bounded(bar(kRawEmpty + st), (hf / G::kRing - 1) & 1);
@@ -479,10 +492,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           }
           if (side == 0) {
             // (block j - 8's readers are done: their weights came before the products that freed this stage)
-            if (lane < kBlkPages) {
-              k_scale[info * 8 + lane] = s_now.x;
-              v_scale[info * 8 + lane] = s_now.y;
-              page_pos[info * 8 + lane] = b_now < 0 ? 0x7fffffff - kPageSize : b_now;
+            if (mine) {
+              const int at = info * 8 + (lane & 7);
+              k_scale[at] = sc.x;
+              v_scale[at] = sc.y;
+              page_pos[at] = pid < 0 ? 0x7fffffff - kPageSize : T.vis.page((blk0 + j) * kBlkPages + (lane & 7)) * kPageSize;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kInfoFull + info));
@@ -492,9 +506,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
             else mbar_arrive(bar(kRawFull + st));
           }
           __syncwarp();
-          if (id >= 0)
-            bulk_g2s(sb + G::kRaw + st * G::kHalf + lane * (kPageSize * D),
-                     a.pages + ((static_cast<size_t>(id) * a.H + h) * 2 + side) * (kPageSize * D), kPageSize * D,
+          if (have)
+            bulk_g2s(sb + G::kRaw + st * G::kHalf + (lane & 7) * (kPageSize * D),
+                     a.pages + ((static_cast<size_t>(pid) * a.H + h) * 2 + side) * (kPageSize * D), kPageSize * D,
                      bar(kRawFull + st));
           issued = hf + 1;
         }
@@ -513,20 +527,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
         umma::fence_after_sync();
       };
       auto qk = [&](int t, int j, int sbuf) {
-        const uint32_t qb = sb + G::kQ + t * G::kOp, kb = sb + G::kK + (j & 1) * G::kOp;
+        const uint64_t dq = umma::desc_k_sw128(sb + G::kQ + t * G::kOp);
+        const uint64_t dk = umma::desc_k_sw128(sb + G::kK + (j & 1) * G::kOp);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * (kTok * 128) + (ks & 3) * 32;
-          umma::mma_bf16(s_tmem[sbuf], umma::desc_k_sw128(qb + off), umma::desc_k_sw128(kb + off), kIdQk, ks > 0);
+          const uint32_t off = ((ks >> 2) * (kTok * 128) + (ks & 3) * 32) >> 4;  // within the address field
+          umma::mma_bf16(s_tmem[sbuf], dq + off, dk + off, kIdQk, ks > 0);
         }
         umma::commit(bar(kSFull + sbuf));
       };
       auto pv = [&](int t, int j, int sbuf) {
-        const uint32_t vb = sb + G::kV + (j & 1) * G::kOp;
+        const uint64_t dv = umma::desc_mn_sw128(sb + G::kV + (j & 1) * G::kOp, kTok * 128);
 #pragma unroll
         for (int ks = 0; ks < kTok / 16; ++ks)
-          umma::mma_f16_ts(o_tmem[t], s_tmem[sbuf] + ks * 8, umma::desc_mn_sw128(vb + ks * 2048, kTok * 128), kIdPv,
-                           j > 0 || ks > 0);
+          umma::mma_f16_ts(o_tmem[t], s_tmem[sbuf] + ks * 8, dv + ks * (2048 >> 4), kIdPv, j > 0 || ks > 0);
         umma::commit(bar(kPvDone + t));
       };
       const int nt = MT == 2 ? active : 1;
