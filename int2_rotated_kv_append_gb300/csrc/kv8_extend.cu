@@ -257,14 +257,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
         for (int c = 0; c < 4; ++c) umma::tmem_ld32(s_tmem[sbuf] + t_lane + 32 * c, v[c]);
         umma::tmem_ld_wait();
         float ks[8];
-        float vmax = 0.f;
+        float vmax;
         bool full = true;
+        {
+          const float4 x = *reinterpret_cast<const float4*>(k_scale + info * 8);
+          const float4 y = *reinterpret_cast<const float4*>(k_scale + info * 8 + 4);
+          const float4 z = *reinterpret_cast<const float4*>(v_scale + info * 8);
+          const float4 w = *reinterpret_cast<const float4*>(v_scale + info * 8 + 4);
+          const int4 p = *reinterpret_cast<const int4*>(page_pos + info * 8);
+          const int4 q = *reinterpret_cast<const int4*>(page_pos + info * 8 + 4);
+          const float k8[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          const int p8[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+          vmax = fmax3(fmax3(z.x, z.y, z.z), fmax3(z.w, w.x, w.y), fmaxf(w.z, w.w));
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          ks[c] = fmaxf(k_scale[info * 8 + c] * qs, 1.2e-38f);  // (never 0: -inf stays -inf)
-          vmax = fmaxf(vmax, v_scale[info * 8 + c]);
-          const int pp = page_pos[info * 8 + c];
-          full = full && pp <= p_lo - (kPageSize - 1) && (pp > hi_after || pp + kPageSize <= a.sink);
+          for (int c = 0; c < 8; ++c) {
+            ks[c] = fmaxf(k8[c] * qs, 1.2e-38f);  // (never 0: -inf stays -inf)
+            full = full && p8[c] <= p_lo - (kPageSize - 1) && (p8[c] > hi_after || p8[c] + kPageSize <= a.sink);
+          }
         }
         if (!full) {
 #pragma unroll
@@ -400,47 +409,58 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
         ok = mbar_wait_bounded(bar(kRawFull + st), (hf / G::kRing) & 1) &&
              (j < 2 || mbar_wait_bounded(bar(kOpEmpty + op), ((j >> 1) - 1) & 1));
         if (!ok) break;
-        float vmax = 0.f;
-        if (side == 1) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) vmax = fmaxf(vmax, v_scale[info * 8 + c]);
-        }
-        const float inv = vmax > 0.f ? 1.f / vmax : 0.f;  // exact: a power of two
         const uint32_t src = sb + G::kRaw + st * G::kHalf;
         const uint32_t dst = sb + (side ? G::kV : G::kK) + (j & 1) * G::kOp;
+        // every load first: the units are independent, and a load waits for nothing but itself
+        uint32_t w[kUnits][4];
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                       : "r"(src + (i * 128 + pt) * 16)
+                       : "memory");
+        float ratio[kUnits];
+        bool scaled = false;  // some page's scale is not the block's largest
+        if (side == 1) {
+          const float* vs = v_scale + info * 8;
+          const int* pp = page_pos + info * 8;
+          float vmax = 0.f;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) vmax = fmaxf(vmax, vs[c]);
+          const float inv = vmax > 0.f ? 1.f / vmax : 0.f;  // exact: a power of two
+          bool tail = false;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            scaled = scaled || vs[c] != vmax;
+            tail = tail || pp[c] + kPageSize > T.L;
+          }
+#pragma unroll
+          for (int i = 0; i < kUnits; ++i) {
+            const int pg = (i * 128 + pt) / (kChunks * kPageSize);  // the unit's page
+            ratio[i] = vs[pg] * inv;
+            if (tail && pp[pg] + (i * 128 + pt) / kChunks % kPageSize >= T.L)
+              w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;  // any bits: behind the last token, or no page
+          }
+        }
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
           const int u = i * 128 + pt, r = u / kChunks, c = u % kChunks;
-          uint32_t w[4], y[8];
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                       : "r"(src + u * 16)
-                       : "memory");
-          if (side == 1) {
-            const int p0 = page_pos[info * 8 + (r >> 4)];
-            if (p0 + (r & 15) >= T.L || p0 < 0) w[0] = w[1] = w[2] = w[3] = 0u;  // any bits: behind the last token, no page
-          }
+          uint32_t y[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) codes_to_f16<F>(w[e], y[2 * e], y[2 * e + 1]);
-          if (side == 1) {
-            const float ratio = v_scale[info * 8 + (r >> 4)] * inv;
-            if (ratio != 1.f) {
-              const __half2 f = __float2half2_rn(ratio);
+          for (int e = 0; e < 4; ++e) codes_to_f16<F>(w[i][e], y[2 * e], y[2 * e + 1]);
+          if (scaled) {
+            const __half2 f = __float2half2_rn(ratio[i]);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&y[e]), f);
-                y[e] = *reinterpret_cast<const uint32_t*>(&z);
-              }
+            for (int e = 0; e < 8; ++e) {
+              const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&y[e]), f);
+              y[e] = *reinterpret_cast<const uint32_t*>(&z);
             }
           }
-          // channels 16 c .. + 15 of row r: two 16-byte chunks of 64-channel block c / 4.  Lanes of the second
-          // block write their second chunk first, so that the eight lanes of a row meet eight banks.
+          // channels 16 c .. + 15 of row r: two 16-byte chunks of 64-channel block c / 4
           const uint32_t row = dst + (c >> 2) * (kTok * 128) + r * 128;
           const int c0 = 2 * (c & 3), sw = r & 7;
-          const bool flip = D == 128 && c >= 4;
-          const uint32_t a0 = row + ((c0 ^ sw) << 4), a1 = row + (((c0 + 1) ^ sw) << 4);
-          st_shared_v4(flip ? a1 : a0, flip ? y[4] : y[0], flip ? y[5] : y[1], flip ? y[6] : y[2], flip ? y[7] : y[3]);
-          st_shared_v4(flip ? a0 : a1, flip ? y[0] : y[4], flip ? y[1] : y[5], flip ? y[2] : y[6], flip ? y[3] : y[7]);
+          st_shared_v4(row + ((c0 ^ sw) << 4), y[0], y[1], y[2], y[3]);
+          st_shared_v4(row + (((c0 + 1) ^ sw) << 4), y[4], y[5], y[6], y[7]);
         }
         fence_async();
         mbar_arrive(bar(kOpFull + op));
