@@ -40,6 +40,18 @@ constexpr int kRegsLaunch = 128;
 constexpr int kRegsSoftmax = 184, kRegsExpand = 80, kRegsIssue = 64;
 static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsIssue == 4 * kRegsLaunch, "the warpgroups share what was launched");
 
+// What the fetching warp finds out about a block, for the warps that expand it and those that weigh it.
+struct alignas(16) BlockInfo {
+  float k_scale[kBlkPages];  // 1 where there is no page
+  int pos[kBlkPages];        // first position; kNoPage: none
+  __half v_ratio[kBlkPages];  // a page's V scale over vmax (below 2^-24: 0)
+  float vmax;                // largest V scale
+  uint32_t flags;
+};
+constexpr int kNoPage = 0x7fffffff - kPageSize;
+// flags: every row of row tile 0 / 1 sees the whole block; some ratio is not 1; some row is behind the last token
+constexpr uint32_t kFull0 = 1, kScaled = 4, kTail = 8;
+
 template <int D, int MT>
 struct Geo {
   static constexpr uint32_t kOp = kTok * D * 2;   // one fp16 operand: D / 64 blocks of 128 rows x 128 bytes
@@ -52,8 +64,8 @@ struct Geo {
   static constexpr uint32_t kBars = kRaw + kRing * kHalf;
   // raw full, raw empty | K full, K empty, V full, V empty (2 each) | S full (2) | P full, PV done (2 each) | info | end
   static constexpr int kNumBars = 2 * kRing + 8 + 2 + 4 + kInfo + 1;
-  static constexpr uint32_t kScale = kBars + ((kNumBars * 8 + 15) & ~15);  // [kInfo][8] K, V scales, positions
-  static constexpr uint32_t kQs = kScale + kInfo * 3 * 32;
+  static constexpr uint32_t kScale = kBars + ((kNumBars * 8 + 15) & ~15);  // [kInfo] BlockInfo
+  static constexpr uint32_t kQs = kScale + kInfo * sizeof(BlockInfo);
   static constexpr uint32_t kMisc = kQs + MT * 128 * 4;
   static constexpr size_t kSmem = 1024 + kMisc + 16;
 };
@@ -150,9 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
   constexpr int kRawFull = 0, kRawEmpty = G::kRing, kOpFull = 2 * G::kRing, kOpEmpty = kOpFull + 4,
                 kSFull = kOpEmpty + 4, kPFull = kSFull + 2, kPvDone = kPFull + 2, kInfoFull = kPvDone + 2,
                 kEnd = kInfoFull + kInfo;  // operand barriers: 2 x side + buffer
-  float* k_scale = reinterpret_cast<float*>(sm + G::kScale);
-  float* v_scale = k_scale + kInfo * 8;
-  int* page_pos = reinterpret_cast<int*>(v_scale + kInfo * 8);
+  BlockInfo* infos = reinterpret_cast<BlockInfo*>(sm + G::kScale);
   float* q_scale = reinterpret_cast<float*>(sm + G::kQs);
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + G::kMisc);  // TMEM base
   const int active = (T.rows + 127) / 128;
@@ -236,10 +246,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       const int last_r = min(T.rows, wg * 128 + 128) - 1;  // rows behind it are zeros and not stored
       const int pos = T.L - T.n + (T.r0 + min(r, last_r)) / gqa;
       const int after = a.window > 0 ? max(pos - a.window, -1) : -1;  // visible: behind it, or a sink
-      // what every row of this 128 sees: positions up to p_lo, and after p_hi_after (or in the sink)
-      const int p_lo = T.L - T.n + (T.r0 + wg * 128) / gqa;
-      const int p_hi = T.L - T.n + (T.r0 + last_r) / gqa;
-      const int hi_after = a.window > 0 ? max(p_hi - a.window, -1) : -1;
       float m = -INFINITY, l = 0.f, vref = 0.f;
       bool ok = true;
       for (int j = 0; j < cnt && ok; ++j) {
@@ -256,33 +262,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) umma::tmem_ld32(s_tmem[sbuf] + t_lane + 32 * c, v[c]);
         umma::tmem_ld_wait();
+        const BlockInfo& bi = infos[info];
+        const float vmax = bi.vmax;
         float ks[8];
-        float vmax;
-        bool full = true;
         {
-          const float4 x = *reinterpret_cast<const float4*>(k_scale + info * 8);
-          const float4 y = *reinterpret_cast<const float4*>(k_scale + info * 8 + 4);
-          const float4 z = *reinterpret_cast<const float4*>(v_scale + info * 8);
-          const float4 w = *reinterpret_cast<const float4*>(v_scale + info * 8 + 4);
-          const int4 p = *reinterpret_cast<const int4*>(page_pos + info * 8);
-          const int4 q = *reinterpret_cast<const int4*>(page_pos + info * 8 + 4);
+          const float4 x = *reinterpret_cast<const float4*>(bi.k_scale), y = *reinterpret_cast<const float4*>(bi.k_scale + 4);
           const float k8[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-          const int p8[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-          vmax = fmax3(fmax3(z.x, z.y, z.z), fmax3(z.w, w.x, w.y), fmaxf(w.z, w.w));
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            ks[c] = fmaxf(k8[c] * qs, 1.2e-38f);  // (never 0: -inf stays -inf)
-            full = full && p8[c] <= p_lo - (kPageSize - 1) && (p8[c] > hi_after || p8[c] + kPageSize <= a.sink);
-          }
+          for (int c = 0; c < 8; ++c) ks[c] = fmaxf(k8[c] * qs, 1.2e-38f);  // (never 0: -inf stays -inf)
         }
-        if (!full) {
+        if ((bi.flags & (kFull0 << wg)) == 0) {
 #pragma unroll
           for (int pg = 0; pg < 8; ++pg) {
-            const int pp = page_pos[info * 8 + pg];
+            const int pp = bi.pos[pg];
             const int c_hi = pos - pp, c_lo = after - pp, c_sink = a.sink - pp;
 #pragma unroll
             for (int c = 0; c < 16; ++c)
-              if (c > c_hi || (c <= c_lo && c >= c_sink)) v[pg >> 1][(pg & 1) * 16 + c] = 0xff800000u;
+              if ((c > c_hi) | ((c <= c_lo) & (c >= c_sink))) v[pg >> 1][(pg & 1) * 16 + c] = 0xff800000u;
           }
         }
         float mx = -INFINITY;
@@ -419,26 +415,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
                        : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
                        : "r"(src + (i * 128 + pt) * 16)
                        : "memory");
-        float ratio[kUnits];
-        bool scaled = false;  // some page's scale is not the block's largest
-        if (side == 1) {
-          const float* vs = v_scale + info * 8;
-          const int* pp = page_pos + info * 8;
-          float vmax = 0.f;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) vmax = fmaxf(vmax, vs[c]);
-          const float inv = vmax > 0.f ? 1.f / vmax : 0.f;  // exact: a power of two
-          bool tail = false;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            scaled = scaled || vs[c] != vmax;
-            tail = tail || pp[c] + kPageSize > T.L;
-          }
+        const BlockInfo& bi = infos[info];
+        const uint32_t flags = side == 1 ? bi.flags : 0u;
+        if (flags & kTail) {
 #pragma unroll
           for (int i = 0; i < kUnits; ++i) {
-            const int pg = (i * 128 + pt) / (kChunks * kPageSize);  // the unit's page
-            ratio[i] = vs[pg] * inv;
-            if (tail && pp[pg] + (i * 128 + pt) / kChunks % kPageSize >= T.L)
+            const int r = (i * 128 + pt) / kChunks;
+            if (bi.pos[r >> 4] + (r & 15) >= T.L)
               w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;  // any bits: behind the last token, or no page
           }
         }
@@ -448,8 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           uint32_t y[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) codes_to_f16<F>(w[i][e], y[2 * e], y[2 * e + 1]);
-          if (scaled) {
-            const __half2 f = __float2half2_rn(ratio[i]);
+          if (flags & kScaled) {
+            const __half2 f = __half2half2(bi.v_ratio[r >> 4]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&y[e]), f);
@@ -512,11 +495,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           }
           if (side == 0) {
             // (block j - 8's readers are done: their weights came before the products that freed this stage)
+            const int pos = pid < 0 ? kNoPage : T.vis.page((blk0 + j) * kBlkPages + (lane & 7)) * kPageSize;
+            float vmax = sc.y;
+#pragma unroll
+            for (int o = 1; o < kBlkPages; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+            const float ratio = pid >= 0 && vmax > 0.f ? sc.y / vmax : 1.f;  // exact: powers of two
+            auto any = [&](bool x) { return __any_sync(0xffffffffu, mine && x); };
+            uint32_t flags = 0;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+              // every row of this row tile sees positions up to p_lo that are behind p_after, or in the sink
+              const int p_lo = T.L - T.n + (T.r0 + t * 128) / gqa;
+              const int p_hi = T.L - T.n + (T.r0 + min(T.rows, t * 128 + 128) - 1) / gqa;
+              const int p_after = a.window > 0 ? p_hi - a.window : -1;
+              if (!any(pos > p_lo - (kPageSize - 1) || (pos <= p_after && pos > a.sink - kPageSize))) flags |= kFull0 << t;
+            }
+            if (any(ratio != 1.f)) flags |= kScaled;
+            if (any(pid < 0 || pos > T.L - kPageSize)) flags |= kTail;
             if (mine) {
-              const int at = info * 8 + (lane & 7);
-              k_scale[at] = sc.x;
-              v_scale[at] = sc.y;
-              page_pos[at] = pid < 0 ? 0x7fffffff - kPageSize : T.vis.page((blk0 + j) * kBlkPages + (lane & 7)) * kPageSize;
+              BlockInfo& bi = infos[info];
+              bi.k_scale[lane & 7] = sc.x;
+              bi.v_ratio[lane & 7] = __float2half_rn(ratio);
+              bi.pos[lane & 7] = pos;
+              if ((lane & 7) == 0) {
+                bi.vmax = vmax;
+                bi.flags = flags;
+              }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kInfoFull + info));
@@ -538,36 +542,51 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
         for (int hf = max(0, issued - G::kRing); hf < issued; ++hf)
           mbar_wait_bounded(bar(kRawFull + hf % G::kRing), (hf / G::kRing) & 1);
       }
-    } else if (warp == kMmaWarp && lane == 0) {
+    } else if (warp == kMmaWarp) {
       // ---- products ---------------------------------------------------------------------------------
+      // The whole warp goes through this code and one elected lane issues: with uniform control flow the
+      // operands stay in uniform registers (65 clocks a 128 x 128 x 16 product with A in TMEM, the pipe's rate, where a branch
+      // on the lane number took 112).
       constexpr uint32_t kIdQk = umma::idesc_f16_f32(128, kTok, false), kIdPv = umma::idesc_f16_f32_b_mn(128, D);
+      const bool issuer = umma::elect_one();
       bool ok = true;
       auto wait = [&](int i, int parity) {
-        if (ok) ok = mbar_wait_bounded(bar(i), parity & 1);
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(i), parity & 1));
         umma::fence_after_sync();
+      };
+      auto commit = [&](int i) {
+        if (issuer) umma::commit(bar(i));
+        __syncwarp();
       };
       auto qk = [&](int t, int j, int sbuf) {
         const uint64_t dq = umma::desc_k_sw128(sb + G::kQ + t * G::kOp);
         const uint64_t dk = umma::desc_k_sw128(sb + G::kK + (j & 1) * G::kOp);
+        if (issuer) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = ((ks >> 2) * (kTok * 128) + (ks & 3) * 32) >> 4;  // within the address field
-          umma::mma_bf16(s_tmem[sbuf], dq + off, dk + off, kIdQk, ks > 0);
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * (kTok * 128) + (ks & 3) * 32) >> 4;  // within the address field
+            umma::mma_bf16(s_tmem[sbuf], dq + off, dk + off, kIdQk, ks > 0);
+          }
+          umma::commit(bar(kSFull + sbuf));
         }
-        umma::commit(bar(kSFull + sbuf));
+        __syncwarp();
       };
       auto pv = [&](int t, int j, int sbuf) {
         const uint64_t dv = umma::desc_mn_sw128(sb + G::kV + (j & 1) * G::kOp, kTok * 128);
+        if (issuer) {
 #pragma unroll
-        for (int ks = 0; ks < kTok / 16; ++ks)
-          umma::mma_f16_ts(o_tmem[t], s_tmem[sbuf] + ks * 8, dv + ks * (2048 >> 4), kIdPv, j > 0 || ks > 0);
-        umma::commit(bar(kPvDone + t));
+          for (int ks = 0; ks < kTok / 16; ++ks)
+            umma::mma_f16_ts(o_tmem[t], s_tmem[sbuf] + ks * 8, dv + ks * (2048 >> 4), kIdPv, j > 0 || ks > 0);
+          umma::commit(bar(kPvDone + t));
+        }
+        __syncwarp();
       };
       const int nt = MT == 2 ? active : 1;
       wait(kOpFull + 0, 0);
-      if (ok)
+      if (ok) {
         for (int t = 0; t < nt; ++t) qk(t, 0, t);
-      if (ok) umma::commit(bar(kOpEmpty + 0));
+        commit(kOpEmpty + 0);
+      }
       for (int j = 0; j < cnt && ok; ++j) {
         const bool more = j + 1 < cnt;
         if (MT == 1) {
@@ -575,31 +594,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
             wait(kOpFull + ((j + 1) & 1), (j + 1) >> 1);
             if (!ok) break;
             qk(0, j + 1, (j + 1) & 1);
-            umma::commit(bar(kOpEmpty + ((j + 1) & 1)));
+            commit(kOpEmpty + ((j + 1) & 1));
           }
           wait(kPFull + 0, j);
           wait(kOpFull + 2 + (j & 1), j >> 1);
           if (!ok) break;
           pv(0, j, j & 1);
-          umma::commit(bar(kOpEmpty + 2 + (j & 1)));
+          commit(kOpEmpty + 2 + (j & 1));
         } else {
           for (int t = 0; t < nt && ok; ++t) {
             wait(kPFull + t, j);
             if (t == 0) wait(kOpFull + 2 + (j & 1), j >> 1);
             if (!ok) break;
             pv(t, j, t);
-            if (t == nt - 1) umma::commit(bar(kOpEmpty + 2 + (j & 1)));
+            if (t == nt - 1) commit(kOpEmpty + 2 + (j & 1));
             if (more) {
               if (t == 0) wait(kOpFull + ((j + 1) & 1), (j + 1) >> 1);
               if (!ok) break;
               qk(t, j + 1, t);
-              if (t == nt - 1) umma::commit(bar(kOpEmpty + ((j + 1) & 1)));
+              if (t == nt - 1) commit(kOpEmpty + ((j + 1) & 1));
             }
           }
         }
       }
-      if (!ok) record_error(OSCAR_DEVERR_TIMEOUT);
-      umma::commit(bar(kEnd));  // every product is over before TMEM is freed
+      if (!ok && lane == 0) record_error(OSCAR_DEVERR_TIMEOUT);
+      commit(kEnd);  // every product is over before TMEM is freed
       mbar_wait_bounded(bar(kEnd), 0);
     }
   }
