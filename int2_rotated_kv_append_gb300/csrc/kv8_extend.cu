@@ -6,11 +6,14 @@
 // of the tile sees go through in blocks of 8 (128 tokens).  Roles of the 16 warps:
 //   warp 13       page ids and scales of the coming blocks; K and V codes into a ring by bulk copies;
 //   warps 8..11   codes -> fp16 (exact) K and V operands in shared memory, two blocks deep, once per CTA;
-//   warp 12       one thread issues S = Q K^T and O += P V (A = P from TMEM);
+//   warps 12, 14  issue S = Q K^T and O += P V (A = P from TMEM): apart, so that neither's waits hold up the other;
 //   warps 0..7    softmax, one thread per row, one warpgroup per 128 rows: 128 logits from TMEM, weights back to
-//                 TMEM as fp16 over the logits' own columns.
-// With MT = 2 the two row tiles alternate on the tensor cores: while one tile's softmax runs the other tile's
-// products do.  With MT = 1 the logits are double-buffered over blocks instead.
+//                 TMEM as fp16.
+// TMEM (512 columns): with MT = 2 one logit buffer (128) for both row tiles, which is free again once a row tile has
+// it in registers, so that the next logits of either tile are formed while both compute weights; a weight
+// buffer (64) and an accumulator (D) per row tile.  (With the weights over a tile's own logits, its next
+// product waited for its softmax and PV: 3650 clocks a block instead of 2700.)  With MT = 1 two logit buffers
+// alternate.
 // Scales stay out of the operands.  Q is scaled per row by a power of two to below 2, where fp16 holds
 // it to 2^-25 of the row's largest element; a page's K scale multiplies its 16 logits.  V codes carry the ratio of their page's scale to the
 // block's largest, vmax (a power of two, exact down to 2^-24), and the weights carry vmax / vref, vref the largest
@@ -34,7 +37,7 @@ constexpr int kBlkPages = kTok / kPageSize;
 constexpr int kInfo = 8;          // blocks whose scales and positions are kept
 constexpr float kLazy = 8.f;      // log2: how far a logit may pass the maximum in use
 constexpr int kBoost = 7;         // weights are stored times 2^kBoost: 2^(kLazy + kBoost) < 65504
-constexpr int kFetchWarp = 13, kMmaWarp = 12;
+constexpr int kQkWarp = 12, kFetchWarp = 13, kPvWarp = 14;
 // Registers a thread: 512 x 128 at launch, divided as 2 x 128 x 184 + 128 x 80 + 128 x 64
 constexpr int kRegsLaunch = 128;
 constexpr int kRegsSoftmax = 184, kRegsExpand = 80, kRegsIssue = 64;
@@ -62,8 +65,8 @@ struct Geo {
   static constexpr uint32_t kV = kK + 2 * kOp;
   static constexpr uint32_t kRaw = kV + 2 * kOp;
   static constexpr uint32_t kBars = kRaw + kRing * kHalf;
-  // raw full, raw empty | K full, K empty, V full, V empty (2 each) | S full (2) | P full, PV done (2 each) | info | end
-  static constexpr int kNumBars = 2 * kRing + 8 + 2 + 4 + kInfo + 1;
+  // raw full, raw empty | K full, K empty, V full, V empty (2 each) | S full, S free, P full, PV done (2 each) | info | end
+  static constexpr int kNumBars = 2 * kRing + 8 + 8 + kInfo + 1;
   static constexpr uint32_t kScale = kBars + ((kNumBars * 8 + 15) & ~15);  // [kInfo] BlockInfo
   static constexpr uint32_t kQs = kScale + kInfo * sizeof(BlockInfo);
   static constexpr uint32_t kMisc = kQs + MT * 128 * 4;
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + G::kBars);
   auto bar = [&](int i) { return smem_u32(bars + i); };
   constexpr int kRawFull = 0, kRawEmpty = G::kRing, kOpFull = 2 * G::kRing, kOpEmpty = kOpFull + 4,
-                kSFull = kOpEmpty + 4, kPFull = kSFull + 2, kPvDone = kPFull + 2, kInfoFull = kPvDone + 2,
+                kSFull = kOpEmpty + 4, kSFree = kSFull + 2, kPFull = kSFree + 2, kPvDone = kPFull + 2, kInfoFull = kPvDone + 2,
                 kEnd = kInfoFull + kInfo;  // operand barriers: 2 x side + buffer
   BlockInfo* infos = reinterpret_cast<BlockInfo*>(sm + G::kScale);
   float* q_scale = reinterpret_cast<float*>(sm + G::kQs);
@@ -177,14 +180,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kSFull + i), 1);
+      mbar_init(bar(kSFree + i), 128);
       mbar_init(bar(kPFull + i), 128);
       mbar_init(bar(kPvDone + i), 1);
     }
     for (int i = 0; i < kInfo; ++i) mbar_init(bar(kInfoFull + i), 1);
-    mbar_init(bar(kEnd), 1);
+    mbar_init(bar(kEnd), 2);
     mbar_init_fence();
   }
-  if (warp == kMmaWarp) umma::tmem_alloc(smem_u32(misc), 512);
+  if (warp == kQkWarp) umma::tmem_alloc(smem_u32(misc), 512);
   // Q as fp16, K-major with the 128-byte swizzle; a warp per row, lane l channels (D / 32) l ..
   {
     constexpr int kPer = D / 32, kWords = kPer / 2, kBatch = 8;  // rows whose loads are in flight at once
@@ -232,7 +236,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
   __syncthreads();
   umma::fence_after_sync();
   const uint32_t tmem = misc[0];
-  const uint32_t s_tmem[2] = {tmem, tmem + 128};       // logits / weights
+  // logits, weights, accumulators
+  const uint32_t s_tmem[2] = {tmem, MT == 2 ? tmem : tmem + 384};
+  const uint32_t p_tmem[2] = {tmem + 128, tmem + 192};
   const uint32_t o_tmem[2] = {tmem + 256, tmem + 256 + D};
 
   const int wg = warp >> 2;
@@ -249,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       float m = -INFINITY, l = 0.f, vref = 0.f;
       bool ok = true;
       for (int j = 0; j < cnt && ok; ++j) {
-        const int sbuf = MT == 2 ? wg : j & 1;
+        const int sbuf = MT == 2 ? wg : j & 1;  // barrier and buffer of the logits
         const int info = j & (kInfo - 1);
         ok = mbar_wait_bounded(bar(kInfoFull + info), (j / kInfo) & 1) &&
              mbar_wait_bounded(bar(kSFull + sbuf), MT == 2 ? j & 1 : (j >> 1) & 1);
@@ -262,6 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) umma::tmem_ld32(s_tmem[sbuf] + t_lane + 32 * c, v[c]);
         umma::tmem_ld_wait();
+        umma::fence_before_sync();
+        mbar_arrive(bar(kSFree + sbuf));
         const BlockInfo& bi = infos[info];
         const float vmax = bi.vmax;
         float ks[8];
@@ -291,6 +299,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           y = fmaxf(y, __uint_as_float(x[15]));
           mx = fmaxf(mx, y * ks[pg]);
         }
+        // The product before is over: its weights' columns and O are free.  (Every phase of this barrier is waited
+        // for in its turn: a parity says nothing two phases ahead.)
+        if (j > 0) {
+          ok = mbar_wait_bounded(bar(kPvDone + (MT == 2 ? wg : 0)), (j - 1) & 1);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          umma::fence_after_sync();
+        }
         const bool move = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
         const bool v_move = vmax > vref;
         if (__any_sync(0xffffffffu, move) || v_move) {
@@ -304,12 +322,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
             vref = vmax;
           }
           if (j > 0) {
-            ok = mbar_wait_bounded(bar(kPvDone + (MT == 2 ? wg : 0)), (j - 1) & 1);
-            if (!__all_sync(0xffffffffu, ok)) {
-              ok = false;
-              break;
-            }
-            umma::fence_after_sync();
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               uint32_t o[16];
@@ -327,7 +339,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
                                   : 0;
         const float off = static_cast<float>(lb) - (m == -INFINITY ? 0.f : m);
         const float2 off2 = make_float2(off, off);
-        float2 sum = make_float2(0.f, 0.f);
+        float2 sum[4];  // four chains of additions
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sum[c] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t p[32];
@@ -339,17 +353,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
                                                __uint_as_float(v[col >> 5][(col & 31) + 1])),
                                    make_float2(k, k), off2);
             const float2 w = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-            sum = f2add(sum, w);
+            sum[c & 3] = f2add(sum[c & 3], w);
             p[c] = half2_bits(w.x, w.y);
           }
-          umma::tmem_st32(s_tmem[sbuf] + t_lane + 32 * half, p);
+          umma::tmem_st32(p_tmem[wg] + t_lane + 32 * half, p);
         }
         umma::tmem_st_wait();
-        // every phase of this barrier is waited for in its turn (a parity says nothing two phases ahead)
-        if (j > 0 && !mbar_wait_bounded(bar(kPvDone + (MT == 2 ? wg : 0)), (j - 1) & 1)) ok = false;
         umma::fence_before_sync();
         mbar_arrive(bar(kPFull + (MT == 2 ? wg : 0)));
-        l = fmaf(sum.x + sum.y, pow2i(-lb), l);
+        sum[0] = f2add(f2add(sum[0], sum[1]), f2add(sum[2], sum[3]));
+        l = fmaf(sum[0].x + sum[0].y, pow2i(-lb), l);
       }
       if (ok) ok = mbar_wait_bounded(bar(kPvDone + (MT == 2 ? wg : 0)), (cnt - 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
@@ -542,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
         for (int hf = max(0, issued - G::kRing); hf < issued; ++hf)
           mbar_wait_bounded(bar(kRawFull + hf % G::kRing), (hf / G::kRing) & 1);
       }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kQkWarp || warp == kPvWarp) {
       // ---- products ---------------------------------------------------------------------------------
       // The whole warp goes through this code and one elected lane issues: with uniform control flow the
       // operands stay in uniform registers (65 clocks a 128 x 128 x 16 product with A in TMEM, the pipe's rate, where a branch
@@ -550,75 +563,66 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       constexpr uint32_t kIdQk = umma::idesc_f16_f32(128, kTok, false), kIdPv = umma::idesc_f16_f32_b_mn(128, D);
       const bool issuer = umma::elect_one();
       bool ok = true;
-      auto wait = [&](int i, int parity) {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(i), parity & 1));
-        umma::fence_after_sync();
-      };
-      auto commit = [&](int i) {
-        if (issuer) umma::commit(bar(i));
-        __syncwarp();
-      };
-      auto qk = [&](int t, int j, int sbuf) {
-        const uint64_t dq = umma::desc_k_sw128(sb + G::kQ + t * G::kOp);
-        const uint64_t dk = umma::desc_k_sw128(sb + G::kK + (j & 1) * G::kOp);
-        if (issuer) {
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = ((ks >> 2) * (kTok * 128) + (ks & 3) * 32) >> 4;  // within the address field
-            umma::mma_bf16(s_tmem[sbuf], dq + off, dk + off, kIdQk, ks > 0);
-          }
-          umma::commit(bar(kSFull + sbuf));
-        }
-        __syncwarp();
-      };
-      auto pv = [&](int t, int j, int sbuf) {
-        const uint64_t dv = umma::desc_mn_sw128(sb + G::kV + (j & 1) * G::kOp, kTok * 128);
-        if (issuer) {
-#pragma unroll
-          for (int ks = 0; ks < kTok / 16; ++ks)
-            umma::mma_f16_ts(o_tmem[t], s_tmem[sbuf] + ks * 8, dv + ks * (2048 >> 4), kIdPv, j > 0 || ks > 0);
-          umma::commit(bar(kPvDone + t));
-        }
-        __syncwarp();
-      };
+      auto wait = [&](int i, int parity) { ok = ok && mbar_wait_bounded(bar(i), parity & 1); };
       const int nt = MT == 2 ? active : 1;
-      wait(kOpFull + 0, 0);
-      if (ok) {
-        for (int t = 0; t < nt; ++t) qk(t, 0, t);
-        commit(kOpEmpty + 0);
-      }
-      for (int j = 0; j < cnt && ok; ++j) {
-        const bool more = j + 1 < cnt;
-        if (MT == 1) {
-          if (more) {
-            wait(kOpFull + ((j + 1) & 1), (j + 1) >> 1);
-            if (!ok) break;
-            qk(0, j + 1, (j + 1) & 1);
-            commit(kOpEmpty + ((j + 1) & 1));
-          }
-          wait(kPFull + 0, j);
-          wait(kOpFull + 2 + (j & 1), j >> 1);
-          if (!ok) break;
-          pv(0, j, j & 1);
-          commit(kOpEmpty + 2 + (j & 1));
-        } else {
-          for (int t = 0; t < nt && ok; ++t) {
-            wait(kPFull + t, j);
-            if (t == 0) wait(kOpFull + 2 + (j & 1), j >> 1);
-            if (!ok) break;
-            pv(t, j, t);
-            if (t == nt - 1) commit(kOpEmpty + 2 + (j & 1));
-            if (more) {
-              if (t == 0) wait(kOpFull + ((j + 1) & 1), (j + 1) >> 1);
-              if (!ok) break;
-              qk(t, j + 1, t);
-              if (t == nt - 1) commit(kOpEmpty + ((j + 1) & 1));
+      if (warp == kQkWarp) {
+        for (int j = 0; j < cnt && ok; ++j) {
+          const int buf = j & 1;
+          const uint64_t dk = umma::desc_k_sw128(sb + G::kK + buf * G::kOp);
+          wait(kOpFull + buf, j >> 1);
+          for (int t = 0; t < nt; ++t) {
+            // the logit buffer has been read: by the row tile before (MT = 2), two blocks ago (MT = 1)
+            if (MT == 1) {
+              if (j >= 2) wait(kSFree + buf, (j >> 1) - 1);
+            } else if (t == 1) {
+              wait(kSFree + 0, j);
+            } else if (j > 0) {
+              wait(kSFree + (nt - 1), j - 1);
             }
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              break;
+            }
+            umma::fence_after_sync();
+            const int sbuf = MT == 2 ? t : buf;
+            const uint64_t dq = umma::desc_k_sw128(sb + G::kQ + t * G::kOp);
+            if (issuer) {
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = ((ks >> 2) * (kTok * 128) + (ks & 3) * 32) >> 4;  // within the address field
+                umma::mma_bf16(s_tmem[sbuf], dq + off, dk + off, kIdQk, ks > 0);
+              }
+              umma::commit(bar(kSFull + sbuf));
+              if (t == nt - 1) umma::commit(bar(kOpEmpty + buf));
+            }
+            __syncwarp();
+          }
+        }
+      } else {
+        for (int j = 0; j < cnt && ok; ++j) {
+          const int buf = j & 1;
+          const uint64_t dv = umma::desc_mn_sw128(sb + G::kV + buf * G::kOp, kTok * 128);
+          wait(kOpFull + 2 + buf, j >> 1);
+          for (int t = 0; t < nt; ++t) {
+            wait(kPFull + t, j);
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              break;
+            }
+            umma::fence_after_sync();
+            if (issuer) {
+#pragma unroll
+              for (int ks = 0; ks < kTok / 16; ++ks)
+                umma::mma_f16_ts(o_tmem[t], p_tmem[t] + ks * 8, dv + ks * (2048 >> 4), kIdPv, j > 0 || ks > 0);
+              umma::commit(bar(kPvDone + t));
+              if (t == nt - 1) umma::commit(bar(kOpEmpty + 2 + buf));
+            }
+            __syncwarp();
           }
         }
       }
       if (!ok && lane == 0) record_error(OSCAR_DEVERR_TIMEOUT);
-      commit(kEnd);  // every product is over before TMEM is freed
+      if (issuer) umma::commit(bar(kEnd));  // every product is over before TMEM is freed
       mbar_wait_bounded(bar(kEnd), 0);
     }
   }
@@ -626,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
-  if (warp == kMmaWarp) umma::tmem_dealloc(tmem, 512);
+  if (warp == kQkWarp) umma::tmem_dealloc(tmem, 512);
 }
 
 // One CTA per (tile, KV head, sequence): the merge of its rows' splits, a warp per row.
