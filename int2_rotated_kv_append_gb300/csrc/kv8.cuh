@@ -93,6 +93,25 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
   }
 }
 
+// The same, times a power of two f (both halves): one operation more for e4m3, none for int8.
+template <int F>
+__device__ __forceinline__ void codes_to_f16_scaled(uint32_t w, __half2 f, __half2 f1152, uint32_t& lo, uint32_t& hi) {
+  if constexpr (F == kE4M3) {
+    codes_to_f16<F>(w, lo, hi);
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&lo), f);
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&hi), f);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hfma2(*reinterpret_cast<const __half2*>(&a), f, __hneg2(f1152));
+    const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&b), f, __hneg2(f1152));
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+
 // Positions of a sequence that a row at position `row` sees: [0, sink_end) and [lo, row], as a list of
 // pages: the first nA pages, then pages first_b ... of the window (a page that holds both ends is
 // in the first part).

@@ -4,8 +4,9 @@
 // One CTA per (split, tile, KV head, sequence).  A tile is MT x 128 query rows, a row being one (position, query
 // head of the group): MT = 2 for prompts, 1 where a sequence has at most 128 rows (drafts).  The pages that any row
 // of the tile sees go through in blocks of 8 (128 tokens).  Roles of the 16 warps:
-//   warp 13       page ids and scales of the coming blocks; K and V codes into a ring by bulk copies;
-//   warps 8..11   codes -> fp16 (exact) K and V operands in shared memory, two blocks deep, once per CTA;
+//   warps 13, 15  page ids and scales of the coming blocks; K and V codes into a ring by bulk copies;
+//   warps 8..11   codes -> fp16 (exact) K and V operands in shared memory, two blocks deep, once per CTA (with MT = 1
+//                 warps 4..7 take the V side);
 //   warps 12, 14  issue S = Q K^T and O += P V (A = P from TMEM): apart, so that neither's waits hold up the other;
 //   warps 0..7    softmax, one thread per row, one warpgroup per 128 rows: 128 logits from TMEM, weights back to
 //                 TMEM as fp16.
@@ -37,11 +38,15 @@ constexpr int kBlkPages = kTok / kPageSize;
 constexpr int kInfo = 8;          // blocks whose scales and positions are kept
 constexpr float kLazy = 8.f;      // log2: how far a logit may pass the maximum in use
 constexpr int kBoost = 7;         // weights are stored times 2^kBoost: 2^(kLazy + kBoost) < 65504
-constexpr int kQkWarp = 12, kFetchWarp = 13, kPvWarp = 14;
-// Registers a thread: 512 x 128 at launch, divided as 2 x 128 x 184 + 128 x 80 + 128 x 64
+constexpr int kQkWarp = 12, kFetchK = 13, kPvWarp = 14, kFetchV = 15;
+// Registers a thread: 512 x 128 at launch, divided among the warpgroups by setmaxnreg
 constexpr int kRegsLaunch = 128;
-constexpr int kRegsSoftmax = 184, kRegsExpand = 80, kRegsIssue = 64;
-static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsIssue == 4 * kRegsLaunch, "the warpgroups share what was launched");
+template <int MT>
+struct Regs {
+  static constexpr int kSoftmax = MT == 2 ? 184 : 240, kExpand = MT == 2 ? 80 : 104, kIssue = 64;
+  static_assert((MT == 2 ? 2 * kSoftmax + kExpand : kSoftmax + 2 * kExpand) + kIssue == 4 * kRegsLaunch,
+                "the warpgroups share what was launched");
+};
 
 // What the fetching warp finds out about a block, for the warps that expand it and those that weigh it.
 struct alignas(16) BlockInfo {
@@ -52,8 +57,8 @@ struct alignas(16) BlockInfo {
   uint32_t flags;
 };
 constexpr int kNoPage = 0x7fffffff - kPageSize;
-// flags: every row of row tile 0 / 1 sees the whole block; some ratio is not 1; some row is behind the last token
-constexpr uint32_t kFull0 = 1, kScaled = 4, kTail = 8;
+// flags: every row of row tile 0 / 1 sees the whole block; some row is behind the last token
+constexpr uint32_t kFull0 = 1, kTail = 4;
 
 template <int D, int MT>
 struct Geo {
@@ -242,9 +247,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
   const uint32_t o_tmem[2] = {tmem + 256, tmem + 256 + D};
 
   const int wg = warp >> 2;
-  if (wg < 2) {
+  if (wg < MT) {
     // ---- softmax ---------------------------------------------------------------------------
-    reg_inc<kRegsSoftmax>();
+    reg_inc<Regs<MT>::kSoftmax>();
     if (wg < active) {
       const int r = wg * 128 + (tid & 127);
       const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -322,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
             vref = vmax;
           }
           if (j > 0) {
-#pragma unroll
+#pragma unroll 1  // (rare: kept small for the instruction cache)
             for (int c = 0; c < D / 16; ++c) {
               uint32_t o[16];
               umma::tmem_ld16(o_tmem[wg] + t_lane + 16 * c, o);
@@ -374,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       const float unit = ok ? vref * (1.f / (1 << kBoost)) : 0.f;
       if (!ok) l = 0.f;
       const float inv = l > 0.f ? unit / l : 0.f;
-#pragma unroll
+#pragma unroll 2
       for (int c = 0; c < D / 16; ++c) {
         uint32_t o[16];
         __syncwarp();
@@ -404,74 +409,71 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
         *reinterpret_cast<float2*>(ea.part_ml + (row * ea.ns + split) * 2) =
             make_float2(l > 0.f ? m : -INFINITY, l);
     }
-  } else if (wg == 2) {
-    // ---- codes -> fp16 operands ---------------------------------------------------------------
-    reg_dec<kRegsExpand>();
-    const int pt = tid - 256;
-    constexpr int kChunks = D / 16;                    // 16-byte chunks of a row of codes
-    constexpr int kUnits = kTok * kChunks / 128;       // per thread
+  } else if (wg < 3) {
+    // ---- codes -> fp16 operands: K and V in turn (MT = 2), V or K (MT = 1: warpgroups 1 and 2) ------------
+    reg_dec<Regs<MT>::kExpand>();
+    const int pt = tid & 127;
+    constexpr int kChunks = D / 16;               // 16-byte chunks of a row of codes
+    constexpr int kUnits = kTok * kChunks / 128;  // a thread's chunks: rows r0, r0 + kStep, ...
+    constexpr int kStep = 128 / kChunks;
+    // Lanes of the second 64 channels take the neighbouring row, so that the eight lanes of a shared-memory access meet
+    // all banks both where they read (chunk c) and where they write (chunk 2 (c % 4) ^ row % 8).
+    const int c = pt % kChunks, r0 = (pt / kChunks) ^ (c >> 2);
+    const uint32_t src0 = sb + G::kRaw + r0 * D + c * 16;
+    // channels 16 c .. + 15 of row r: chunks 2 (c % 4), + 1 of 64-channel block c / 4
+    const uint32_t dst0 = sb + G::kK + (c >> 2) * (kTok * 128) + r0 * 128 + (((2 * (c & 3)) ^ (r0 & 7)) << 4);
+    const uint32_t dst1 = sb + G::kK + (c >> 2) * (kTok * 128) + r0 * 128 + (((2 * (c & 3) + 1) ^ (r0 & 7)) << 4);
     bool ok = true;
-    for (int j = 0; j < cnt && ok; ++j) {
-      const int info = j & (kInfo - 1);
-      for (int side = 0; side < 2 && ok; ++side) {
-        const int hf = 2 * j + side, st = hf % G::kRing, op = 2 * side + (j & 1);
-        ok = mbar_wait_bounded(bar(kRawFull + st), (hf / G::kRing) & 1) &&
-             (j < 2 || mbar_wait_bounded(bar(kOpEmpty + op), ((j >> 1) - 1) & 1));
-        if (!ok) break;
-        const uint32_t src = sb + G::kRaw + st * G::kHalf;
-        const uint32_t dst = sb + (side ? G::kV : G::kK) + (j & 1) * G::kOp;
-        // every load first: the units are independent, and a load waits for nothing but itself
-        uint32_t w[kUnits][4];
+#pragma unroll 1
+    for (int x = 0; x < (MT == 2 ? 2 : 1) * cnt; ++x) {
+      const int j = MT == 2 ? x >> 1 : x, side = MT == 2 ? x & 1 : 2 - wg;
+      const int hf = 2 * j + side, st = hf % G::kRing, op = 2 * side + (j & 1);
+      ok = mbar_wait_bounded(bar(kRawFull + st), (hf / G::kRing) & 1) &&
+           (j < 2 || mbar_wait_bounded(bar(kOpEmpty + op), ((j >> 1) - 1) & 1)) &&
+           mbar_wait_bounded(bar(kInfoFull + (j & (kInfo - 1))), (j / kInfo) & 1);
+      if (!ok) break;
+      // every load first: the units are independent, and a load waits for nothing but itself
+      uint32_t w[kUnits][4];
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i)
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
-                       : "r"(src + (i * 128 + pt) * 16)
-                       : "memory");
-        const BlockInfo& bi = infos[info];
-        const uint32_t flags = side == 1 ? bi.flags : 0u;
-        if (flags & kTail) {
-#pragma unroll
-          for (int i = 0; i < kUnits; ++i) {
-            const int r = (i * 128 + pt) / kChunks;
-            if (bi.pos[r >> 4] + (r & 15) >= T.L)
-              w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;  // any bits: behind the last token, or no page
-          }
-        }
+      for (int i = 0; i < kUnits; ++i)
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                     : "r"(src0 + st * G::kHalf + i * (kStep * D))
+                     : "memory");
+      const BlockInfo& bi = infos[j & (kInfo - 1)];
+      if (side == 1 && (bi.flags & kTail)) {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
-          const int u = i * 128 + pt, r = u / kChunks, c = u % kChunks;
-          uint32_t y[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) codes_to_f16<F>(w[i][e], y[2 * e], y[2 * e + 1]);
-          if (flags & kScaled) {
-            const __half2 f = __half2half2(bi.v_ratio[r >> 4]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&y[e]), f);
-              y[e] = *reinterpret_cast<const uint32_t*>(&z);
-            }
-          }
-          // channels 16 c .. + 15 of row r: two 16-byte chunks of 64-channel block c / 4
-          const uint32_t row = dst + (c >> 2) * (kTok * 128) + r * 128;
-          const int c0 = 2 * (c & 3), sw = r & 7;
-          st_shared_v4(row + ((c0 ^ sw) << 4), y[0], y[1], y[2], y[3]);
-          st_shared_v4(row + (((c0 + 1) ^ sw) << 4), y[4], y[5], y[6], y[7]);
+          const int r = r0 + i * kStep;
+          if (bi.pos[r >> 4] + (r & 15) >= T.L)
+            w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;  // any bits: behind the last token, or no page
         }
-        fence_async();
-        mbar_arrive(bar(kOpFull + op));
-        mbar_arrive(bar(kRawEmpty + st));
       }
+      const uint32_t to = (side * 2 + (j & 1)) * G::kOp;  // the K buffers, then the V buffers
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const __half ratio = side == 1 ? bi.v_ratio[(r0 + i * kStep) >> 4] : __ushort_as_half(0x3c00);
+        const __half2 f = __half2half2(ratio), f1152 = __hmul2(f, __half2half2(__ushort_as_half(0x6480)));
+        uint32_t y[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) codes_to_f16_scaled<F>(w[i][e], f, f1152, y[2 * e], y[2 * e + 1]);
+        st_shared_v4(dst0 + to + i * (kStep * 128), y[0], y[1], y[2], y[3]);
+        st_shared_v4(dst1 + to + i * (kStep * 128), y[4], y[5], y[6], y[7]);
+      }
+      fence_async();
+      mbar_arrive(bar(kOpFull + op));
+      mbar_arrive(bar(kRawEmpty + st));
     }
     if (!ok && lane == 0) record_error(OSCAR_DEVERR_TIMEOUT);
   } else {
-    reg_dec<kRegsIssue>();
-    if (warp == kFetchWarp) {
-      // ---- page ids, scales, copies of codes -------------------------------------------------------
+    reg_dec<Regs<MT>::kIssue>();
+    if (warp == kFetchK || warp == kFetchV) {
+      // ---- page ids, scales, copies of codes: K and block infos by one warp, V by another ---------------
+      const int side = warp == kFetchV;
       const int32_t* table = a.page_table + static_cast<size_t>(b) * a.max_pages;
       // Four blocks at a time, a page a lane: the ids are loaded two groups ahead and the scales one,
       // so that neither is waited for.
-      auto look_up = [&](int g) {  // page id (-1: none)
+      auto look_up = [&](int g) {  // page id (-2: none)
         const int v = blk0 * kBlkPages + g * 32 + lane;
         return g * 32 + lane < cnt * kBlkPages && v < T.vis.n ? __ldg(table + T.vis.page(v)) : -2;
       };
@@ -480,9 +482,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
         return id >= 0 && id < a.num_pages ? id : -1;
       };
       auto scales = [&](int id) {
-        return id >= 0 ? __ldg(reinterpret_cast<const float2*>(a.scales) + static_cast<size_t>(id) * a.H + h)
-                       : make_float2(1.f, 0.f);
+        return id >= 0 && side == 0 ? __ldg(reinterpret_cast<const float2*>(a.scales) + static_cast<size_t>(id) * a.H + h)
+                                    : make_float2(1.f, 0.f);
       };
+      // every row of row tile t sees the positions up to p_lo[t] that are behind p_after[t], or in the sink
+      int p_lo[MT], p_after[MT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        p_lo[t] = T.L - T.n + (T.r0 + t * 128) / gqa;
+        p_after[t] = a.window > 0 ? T.L - T.n + (T.r0 + min(T.rows, t * 128 + 128) - 1) / gqa - a.window : -1;
+      }
+      const bool issuer = umma::elect_one();
       int pid = -1, pid1 = checked(look_up(0)), pid2 = look_up(1);
       float2 sc = make_float2(1.f, 0.f), sc1 = scales(pid1);
       bool ok = true;
@@ -497,63 +507,62 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           pid2 = look_up((j >> 2) + 2);
         }
         const bool mine = (lane >> 3) == (j & 3);  // this lane holds a page of block j
-        const bool have = mine && pid >= 0;
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, have)) * (kPageSize * D);
-        for (int side = 0; side < 2; ++side) {
-          const int hf = 2 * j + side, st = hf % G::kRing;
-          if (hf >= G::kRing) ok = mbar_wait_bounded(bar(kRawEmpty + st), (hf / G::kRing - 1) & 1);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          if (side == 0) {
-            // (block j - 8's readers are done: their weights came before the products that freed this stage)
-            const int pos = pid < 0 ? kNoPage : T.vis.page((blk0 + j) * kBlkPages + (lane & 7)) * kPageSize;
-            float vmax = sc.y;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine && pid >= 0)) * (kPageSize * D);
+        const int hf = 2 * j + side, st = hf % G::kRing;
+        if (hf >= G::kRing) ok = mbar_wait_bounded(bar(kRawEmpty + st), (hf / G::kRing - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        if (side == 0) {
+          // (block j - 8's readers are done: their weights came before the products that freed this stage)
+          const int pos = pid < 0 ? kNoPage : T.vis.page((blk0 + j) * kBlkPages + (lane & 7)) * kPageSize;
+          float vmax = sc.y;
 #pragma unroll
-            for (int o = 1; o < kBlkPages; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
-            const float ratio = pid >= 0 && vmax > 0.f ? sc.y / vmax : 1.f;  // exact: powers of two
-            auto any = [&](bool x) { return __any_sync(0xffffffffu, mine && x); };
-            uint32_t flags = 0;
+          for (int o = 1; o < kBlkPages; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+          const float ratio = pid >= 0 && vmax > 0.f ? sc.y / vmax : 1.f;  // exact: powers of two
+          auto any = [&](bool x) { return __any_sync(0xffffffffu, mine & x); };
+          uint32_t flags = 0;
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-              // every row of this row tile sees positions up to p_lo that are behind p_after, or in the sink
-              const int p_lo = T.L - T.n + (T.r0 + t * 128) / gqa;
-              const int p_hi = T.L - T.n + (T.r0 + min(T.rows, t * 128 + 128) - 1) / gqa;
-              const int p_after = a.window > 0 ? p_hi - a.window : -1;
-              if (!any(pos > p_lo - (kPageSize - 1) || (pos <= p_after && pos > a.sink - kPageSize))) flags |= kFull0 << t;
+          for (int t = 0; t < MT; ++t)
+            if (!any((pos > p_lo[t] - (kPageSize - 1)) | ((pos <= p_after[t]) & (pos > a.sink - kPageSize))))
+              flags |= kFull0 << t;
+          if (any((pid < 0) | (pos > T.L - kPageSize))) flags |= kTail;
+          if (mine) {
+            BlockInfo& bi = infos[info];
+            bi.k_scale[lane & 7] = sc.x;
+            bi.v_ratio[lane & 7] = __float2half_rn(ratio);
+            bi.pos[lane & 7] = pos;
+            if ((lane & 7) == 0) {
+              bi.vmax = vmax;
+              bi.flags = flags;
             }
-            if (any(ratio != 1.f)) flags |= kScaled;
-            if (any(pid < 0 || pos > T.L - kPageSize)) flags |= kTail;
-            if (mine) {
-              BlockInfo& bi = infos[info];
-              bi.k_scale[lane & 7] = sc.x;
-              bi.v_ratio[lane & 7] = __float2half_rn(ratio);
-              bi.pos[lane & 7] = pos;
-              if ((lane & 7) == 0) {
-                bi.vmax = vmax;
-                bi.flags = flags;
-              }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kInfoFull + info));
-          }
-          if (lane == 0) {
-            if (bytes > 0) mbar_arrive_expect_tx(bar(kRawFull + st), bytes);
-            else mbar_arrive(bar(kRawFull + st));
           }
           __syncwarp();
-          if (have)
-            bulk_g2s(sb + G::kRaw + st * G::kHalf + (lane & 7) * (kPageSize * D),
-                     a.pages + ((static_cast<size_t>(pid) * a.H + h) * 2 + side) * (kPageSize * D), kPageSize * D,
-                     bar(kRawFull + st));
-          issued = hf + 1;
+          if (lane == 0) mbar_arrive(bar(kInfoFull + info));
         }
+        int ids[kBlkPages];
+#pragma unroll
+        for (int c = 0; c < kBlkPages; ++c) ids[c] = __shfl_sync(0xffffffffu, pid, (j & 3) * kBlkPages + c);
+        if (issuer) {  // (one lane: eight lanes with a copy each take longer than one lane with eight)
+          if (bytes > 0) mbar_arrive_expect_tx(bar(kRawFull + st), bytes);
+          else mbar_arrive(bar(kRawFull + st));
+#pragma unroll
+          for (int c = 0; c < kBlkPages; ++c)
+            if (ids[c] >= 0)
+              bulk_g2s(sb + G::kRaw + st * G::kHalf + c * (kPageSize * D),
+                       a.pages + ((static_cast<size_t>(ids[c]) * a.H + h) * 2 + side) * (kPageSize * D), kPageSize * D,
+                       bar(kRawFull + st));
+        }
+        __syncwarp();
+        issued = j + 1;
       }
       if (!ok) {  // wait for the copies in flight
         if (lane == 0) record_error(OSCAR_DEVERR_TIMEOUT);
-        for (int hf = max(0, issued - G::kRing); hf < issued; ++hf)
+        for (int j = max(0, issued - G::kRing / 2); j < issued; ++j) {
+          const int hf = 2 * j + side;
           mbar_wait_bounded(bar(kRawFull + hf % G::kRing), (hf / G::kRing) & 1);
+        }
       }
     } else if (warp == kQkWarp || warp == kPvWarp) {
       // ---- products ---------------------------------------------------------------------------------
