@@ -145,20 +145,20 @@ def _dims(d) -> oscar_dims_t:
     return make_dims(**d)
 
 
-def _ptr(t) -> ctypes.c_void_p | None:
+def _ptr(t) -> int | None:
     if t is None:
         return None
     if not t.is_contiguous():
         raise ValueError("OSCAR tensors must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+def _stream(stream) -> int:
+    if stream is None:  # the current stream of the current device, without a Stream object (0.3 against 3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
-    return ctypes.c_void_p(int(stream))
+    return int(stream)
 
 
 def _check(status: int, where: str):

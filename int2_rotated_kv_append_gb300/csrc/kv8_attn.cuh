@@ -73,26 +73,35 @@ __device__ __forceinline__ void store_out4(__nv_bfloat16* out, float4 o, float l
       make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
-// One warp: the log-sum-exp merge of n partials (o [n][D] unnormalised, ml [n][2] = maximum in log2
-// units, sum) into a row of the output.
+// One warp: partials first, first + step, ... of n (o [n][D] unnormalised, ml [n][2] = maximum in log2 units,
+// sum): l and four channels r of lane's c4 = lane % (D / 4), relative to the maximum `base`.  Eight partials are in flight
+// at once.
 template <int D>
-__device__ __forceinline__ void merge_row(const float* o, const float* ml, int n, __nv_bfloat16* out, int lane) {
-  constexpr int kSub = 128 / D;        // partials read at once (D = 64: two half warps)
+__device__ __forceinline__ void merge_part(const float* o, const float* ml, int n, int first, int step, float base,
+                                           int lane, float& l, float4& r) {
+  constexpr int kSub = 128 / D, kFly = 8;  // D = 64: two half warps take every second partial
   const int sub = lane / (D / 4), c4 = lane % (D / 4);
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, ml[2 * i]);
+  l = 0.f;
+  r = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = first * kSub + sub; i0 < n; i0 += step * kSub * kFly) {
+    float4 x[kFly];
+    float2 p[kFly];
 #pragma unroll
-  for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  const float base = M == -INFINITY ? 0.f : M;
-  float l = 0.f;
-  float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = sub; i < n; i += kSub) {
-    const float2 p = *reinterpret_cast<const float2*>(ml + 2 * i);
-    const float4 x = *reinterpret_cast<const float4*>(o + static_cast<size_t>(i) * D + 4 * c4);
-    const float w = fast_exp2(p.x - base);  // 0 for a partial of nothing (-inf)
-    l = fmaf(w, p.y, l);
-    r.x = fmaf(w, x.x, r.x); r.y = fmaf(w, x.y, r.y); r.z = fmaf(w, x.z, r.z); r.w = fmaf(w, x.w, r.w);
+    for (int k = 0; k < kFly; ++k) {
+      const int i = i0 + k * step * kSub;
+      p[k] = make_float2(-INFINITY, 0.f);
+      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        p[k] = *reinterpret_cast<const float2*>(ml + 2 * i);
+        x[k] = *reinterpret_cast<const float4*>(o + static_cast<size_t>(i) * D + 4 * c4);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kFly; ++k) {
+      const float w = fast_exp2(p[k].x - base);  // 0 for a partial of nothing (-inf)
+      l = fmaf(w, p[k].y, l);
+      r.x = fmaf(w, x[k].x, r.x); r.y = fmaf(w, x[k].y, r.y); r.z = fmaf(w, x[k].z, r.z); r.w = fmaf(w, x[k].w, r.w);
+    }
   }
   if (kSub == 2) {
     l += __shfl_xor_sync(0xffffffffu, l, 16);
@@ -101,7 +110,24 @@ __device__ __forceinline__ void merge_row(const float* o, const float* ml, int n
     r.z += __shfl_xor_sync(0xffffffffu, r.z, 16);
     r.w += __shfl_xor_sync(0xffffffffu, r.w, 16);
   }
-  if (sub == 0) store_out4(out + 4 * c4, r, l);
+}
+
+// One warp: the largest of n partials' maxima (0 where there is none).
+__device__ __forceinline__ float merge_max(const float* ml, int n, int lane) {
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, ml[2 * i]);
+#pragma unroll
+  for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  return M == -INFINITY ? 0.f : M;
+}
+
+// One warp: the merge of n partials into a row of the output.
+template <int D>
+__device__ __forceinline__ void merge_row(const float* o, const float* ml, int n, __nv_bfloat16* out, int lane) {
+  float l;
+  float4 r;
+  merge_part<D>(o, ml, n, 0, 1, merge_max(ml, n, lane), lane, l, r);
+  if (lane < D / 4) store_out4(out + 4 * lane, r, l);
 }
 
 }  // namespace kv8

@@ -316,20 +316,37 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
   }
 }
 
-// One warp per (sequence, query head): the log-sum-exp merge of its splits.
+// One CTA per (sequence, query head): the log-sum-exp merge of its splits, dealt out to four warps.
+constexpr int kMergeWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(128) kv8_merge_kernel(SplitArgs sa) {
+__global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(SplitArgs sa) {
+  __shared__ float4 part[kMergeWarps][D / 4];
+  __shared__ float sums[kMergeWarps];
   const AttnArgs& a = sa.a;
-  const int lane = threadIdx.x & 31;
-  const size_t row = static_cast<size_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  grid_dep_wait();
-  if (row >= static_cast<size_t>(a.batch) * a.Hq) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const size_t row = blockIdx.x;
   const int b = static_cast<int>(row / a.Hq);
+  grid_dep_wait();
   const int L = min(max(__ldg(a.seq_lens + b), 0), a.max_seq_len);
   const Visible vis = visible(L - 1, L - 1, a.sink, a.window);
   const int n = (vis.n + sa.pps - 1) / sa.pps;
   if (n <= 1) return;  // the split kernel wrote the output
-  merge_row<D>(sa.part_o + row * sa.ns * D, sa.part_ml + row * sa.ns * 2, n, a.out + row * D, lane);
+  const float* o = sa.part_o + row * sa.ns * D;
+  const float* ml = sa.part_ml + row * sa.ns * 2;
+  float l;
+  float4 r;
+  merge_part<D>(o, ml, n, warp, kMergeWarps, merge_max(ml, n, lane), lane, l, r);
+  if (lane < D / 4) part[warp][lane] = r;
+  if (lane == 0) sums[warp] = l;
+  __syncthreads();
+  if (threadIdx.x < D / 4) {
+    for (int w = 1; w < kMergeWarps; ++w) {
+      const float4 x = part[w][threadIdx.x];
+      l += sums[w];
+      r.x += x.x; r.y += x.y; r.z += x.z; r.w += x.w;
+    }
+    store_out4(a.out + row * D + 4 * threadIdx.x, r, l);
+  }
 }
 
 struct Plan {
@@ -341,7 +358,7 @@ bool make_plan(const oscar_dims_t* d, int batch, int max_seq_len, int pps, int s
   if (check_dims(d) != OSCAR_OK || batch < 0 || batch > 65535 || max_seq_len < 0 || pps < 0 || sink < 0 || window < 0)
     return false;
   if (max_seq_len > static_cast<long long>(d->max_pages_per_seq) * kPageSize) return false;
-  if (d->num_kv_heads > 65535) return false;
+  if (d->num_kv_heads > 65535 || static_cast<long long>(batch) * d->num_q_heads > 0x7fffffffLL) return false;
   const long long pages = max_visible_pages(max_seq_len, sink, window, 1);
   if (pps == 0) {
     const long long units = static_cast<long long>(batch > 0 ? batch : 1) * d->num_kv_heads;
@@ -369,8 +386,8 @@ cudaError_t launch(const SplitArgs& sa, const CUtensorMap& map, cudaStream_t str
   if (e != cudaSuccess) return e;
   e = launch_pdl(k, dim3(sa.ns, sa.a.H, sa.a.batch), dim3(kWarps * 32), Geo<D>::kSmem, stream, map, sa);
   if (e != cudaSuccess || sa.ns == 1) return e;
-  const size_t rows = static_cast<size_t>(sa.a.batch) * sa.a.Hq;
-  return launch_pdl(kv8_merge_kernel<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, stream, sa);
+  return launch_pdl(kv8_merge_kernel<D>, dim3(static_cast<unsigned>(sa.a.batch) * sa.a.Hq), dim3(kMergeWarps * 32), 0,
+                    stream, sa);
 }
 
 }  // namespace

@@ -137,6 +137,9 @@ __device__ __forceinline__ uint32_t half2_bits(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// The lowest n of 16 bits (n < 0: none).
+__device__ __forceinline__ uint32_t low_bits(int n) { return (1u << min(max(n, 0), 16)) - 1u; }
+
 template <int F, int D, int MT>
 __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
   using G = Geo<D, MT>;
@@ -193,15 +196,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
     mbar_init(bar(kEnd), 2);
     mbar_init_fence();
   }
+  __syncthreads();
+  const int wg = warp >> 2;
+  const bool fetches = warp == kFetchK || warp == kFetchV;  // these start at once; the others get Q and TMEM ready
   if (warp == kQkWarp) umma::tmem_alloc(smem_u32(misc), 512);
   // Q as fp16, K-major with the 128-byte swizzle; a warp per row, lane l channels (D / 32) l ..
-  {
-    constexpr int kPer = D / 32, kWords = kPer / 2, kBatch = 8;  // rows whose loads are in flight at once
-    for (int r0 = warp; r0 < active * 128; r0 += kBatch * (kThreads / 32)) {
+  if (wg < 3) {
+    constexpr int kPer = D / 32, kWords = kPer / 2, kBatch = 6, kLoaders = 12;  // six rows' loads in flight a warp
+    for (int r0 = warp; r0 < active * 128; r0 += kBatch * kLoaders) {
       uint32_t x[kBatch][kWords];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int r = r0 + i * (kThreads / 32);
+        const int r = r0 + i * kLoaders;
 #pragma unroll
         for (int c = 0; c < kWords; ++c) x[i][c] = 0u;
         if (r < T.rows) {
@@ -217,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int r = r0 + i * (kThreads / 32);
+        const int r = r0 + i * kLoaders;
         uint32_t mx = x[i][0] & 0x7fff7fffu;
         if constexpr (kWords == 2) mx = __vmaxu2(mx, x[i][1] & 0x7fff7fffu);
         mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
@@ -227,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
 #pragma unroll
         for (int c = 0; c < kWords; ++c)
           y[c] = half2_bits(__uint_as_float(x[i][c] << 16) * inv, __uint_as_float(x[i][c] & 0xffff0000u) * inv);
+        if (r >= active * 128) break;
         const uint32_t dst = sb + G::kQ + (r >> 7) * G::kOp + umma::sw128_offset(r & 127, lane * kPer, 128);
         if constexpr (kWords == 2)
           asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(y[0]), "r"(y[1]) : "memory");
@@ -236,17 +243,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       }
     }
   }
-  fence_async();
-  umma::fence_before_sync();
-  __syncthreads();
-  umma::fence_after_sync();
-  const uint32_t tmem = misc[0];
+  if (!fetches) {
+    fence_async();
+    umma::fence_before_sync();
+    asm volatile("bar.sync 1, %0;" ::"n"(kThreads - 64) : "memory");
+    umma::fence_after_sync();
+  }
+  const uint32_t tmem = fetches ? 0u : misc[0];
   // logits, weights, accumulators
   const uint32_t s_tmem[2] = {tmem, MT == 2 ? tmem : tmem + 384};
   const uint32_t p_tmem[2] = {tmem + 128, tmem + 192};
   const uint32_t o_tmem[2] = {tmem + 256, tmem + 256 + D};
 
-  const int wg = warp >> 2;
   if (wg < MT) {
     // ---- softmax ---------------------------------------------------------------------------
     reg_inc<Regs<MT>::kSoftmax>();
@@ -287,11 +295,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
         if ((bi.flags & (kFull0 << wg)) == 0) {
 #pragma unroll
           for (int pg = 0; pg < 8; ++pg) {
+            // bit c: the row sees position pp + c (a page that all rows of the warp see costs no selects)
             const int pp = bi.pos[pg];
-            const int c_hi = pos - pp, c_lo = after - pp, c_sink = a.sink - pp;
+            const uint32_t upto = low_bits(pos - pp + 1), behind = ~low_bits(after - pp + 1), sinks = low_bits(a.sink - pp);
+            const uint32_t see = upto & (behind | sinks);
+            if (__any_sync(0xffffffffu, see != 0xffffu)) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-              if ((c > c_hi) | ((c <= c_lo) & (c >= c_sink))) v[pg >> 1][(pg & 1) * 16 + c] = 0xff800000u;
+              for (int c = 0; c < 16; ++c)
+                if ((see >> c & 1u) == 0) v[pg >> 1][(pg & 1) * 16 + c] = 0xff800000u;
+            }
           }
         }
         float mx = -INFINITY;
@@ -639,26 +651,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
-  if (warp == kQkWarp) umma::tmem_dealloc(tmem, 512);
+  if (warp == kQkWarp) umma::tmem_dealloc(misc[0], 512);
 }
 
-// One CTA per (tile, KV head, sequence): the merge of its rows' splits, a warp per row.
+// The merge of the splits, one warp per output row: kMergeRows rows of a tile per CTA.
+constexpr int kMergeRows = 4;
 template <int D, int TM>
-__global__ void __launch_bounds__(256) kv8_extend_merge_kernel(ExtArgs ea) {
+__global__ void __launch_bounds__(kMergeRows * 32) kv8_extend_merge_kernel(ExtArgs ea) {
   const AttnArgs& a = ea.a;
   grid_dep_wait();
-  const Tile T = tile_of<TM>(a, blockIdx.z, blockIdx.x);
+  constexpr int kParts = TM / kMergeRows;
+  const Tile T = tile_of<TM>(a, blockIdx.z, blockIdx.x / kParts);
   if (!T.ok) return;
   const int n = (T.blocks + ea.bps - 1) / ea.bps;
-  if (n <= 1) return;  // written by the attention kernel
-  const int gqa = a.Hq / a.H, lane = threadIdx.x & 31;
-  for (int r = threadIdx.x >> 5; r < T.rows; r += 8) {
-    const int x = T.r0 + r;
-    const size_t row = static_cast<size_t>(T.q0 + x / gqa) * a.Hq + blockIdx.y * gqa + x % gqa;
-    merge_row<D>(ea.part_o + row * ea.ns * D, ea.part_ml + row * ea.ns * 2, n, a.out + row * D, lane);
-  }
+  const int r = blockIdx.x % kParts * kMergeRows + (threadIdx.x >> 5);
+  if (n <= 1 || r >= T.rows) return;  // (one split: written by the attention kernel)
+  const int gqa = a.Hq / a.H, x = T.r0 + r;
+  const size_t row = static_cast<size_t>(T.q0 + x / gqa) * a.Hq + blockIdx.y * gqa + x % gqa;
+  merge_row<D>(ea.part_o + row * ea.ns * D, ea.part_ml + row * ea.ns * 2, n, a.out + row * D, threadIdx.x & 31);
 }
 
+#ifndef WANT
+#define WANT 4
+#endif
+constexpr long long kWantShort = WANT;
 struct Plan {
   int mt, tiles, ns, bps;
   size_t off_ml, total;
@@ -686,14 +702,14 @@ bool make_plan(const oscar_dims_t* d, int batch, int rows, int max_seq_len, int 
     long long units = static_cast<long long>(rows) * gqa / tm + batch;
     if (units > tiles * batch) units = tiles * batch;
     units *= d->num_kv_heads;
-    const long long want = (p->mt == 1 ? 4LL : 2LL) * num_sms();
+    const long long want = (p->mt == 1 ? kWantShort : 2LL) * num_sms();
     const long long splits = units > 0 && units < want ? want / units : 1;
     bps = (blocks + splits - 1) / splits;
     if (bps < 4) bps = 4;
   }
   if (bps < 1) bps = 1;
   const long long ns = blocks > 0 ? (blocks + bps - 1) / bps : 1;
-  if (ns > 65535 || tiles * ns > 0x7fffffffLL || bps > 0x7fffffffLL / kBlkPages) return false;
+  if (ns > 65535 || tiles * ns > 0x7fffffffLL || tiles * 64 > 0x7fffffffLL || bps > 0x7fffffffLL / kBlkPages) return false;
   p->tiles = static_cast<int>(tiles > 0 ? tiles : 1);
   p->ns = static_cast<int>(ns);
   p->bps = static_cast<int>(bps);
@@ -720,7 +736,8 @@ cudaError_t launch(const ExtArgs& ea, cudaStream_t stream) {
   e = launch_pdl(k, dim3(static_cast<unsigned>(ea.tiles * ea.ns), ea.a.H, ea.a.batch), dim3(kThreads),
                  Geo<D, MT>::kSmem, stream, ea);
   if (e != cudaSuccess || ea.ns == 1) return e;
-  return launch_pdl(kv8_extend_merge_kernel<D, MT * 128>, dim3(ea.tiles, ea.a.H, ea.a.batch), dim3(256), 0, stream, ea);
+  return launch_pdl(kv8_extend_merge_kernel<D, MT * 128>, dim3(ea.tiles * (MT * 128 / kMergeRows), ea.a.H, ea.a.batch),
+                    dim3(kMergeRows * 32), 0, stream, ea);
 }
 
 template <int F, int D>
