@@ -35,7 +35,7 @@ using namespace oscar::kv8;
 constexpr int kThreads = 512;
 constexpr int kTok = 128;
 constexpr int kBlkPages = kTok / kPageSize;
-constexpr int kInfo = 8;          // blocks whose scales and positions are kept
+constexpr int kInfo = 6;          // blocks whose scales and positions are kept
 constexpr float kLazy = 8.f;      // log2: how far a logit may pass the maximum in use
 constexpr int kBoost = 7;         // weights are stored times 2^kBoost: 2^(kLazy + kBoost) < 65504
 constexpr int kQkWarp = 12, kFetchK = 13, kPvWarp = 14, kFetchV = 15;
@@ -63,15 +63,16 @@ constexpr uint32_t kFull0 = 1, kTail = 4;
 template <int D, int MT>
 struct Geo {
   static constexpr uint32_t kOp = kTok * D * 2;   // one fp16 operand: D / 64 blocks of 128 rows x 128 bytes
-  static constexpr uint32_t kHalf = kTok * D;     // K or V codes of a block
-  static constexpr int kRing = D == 128 ? (MT == 2 ? 2 : 4) : 8;
+  // Stages of codes: K or V of a block (MT = 2), or whole pages of a block (MT = 1: half as many copies to issue)
+  static constexpr uint32_t kStage = (MT == 2 ? 1 : 2) * kTok * D;
+  static constexpr int kRing = D == 128 ? 2 : (MT == 2 ? 8 : 4);
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kK = MT * kOp;
   static constexpr uint32_t kV = kK + 2 * kOp;
   static constexpr uint32_t kRaw = kV + 2 * kOp;
-  static constexpr uint32_t kBars = kRaw + kRing * kHalf;
-  // raw full, raw empty | K full, K empty, V full, V empty (2 each) | S full, S free, P full, PV done (2 each) | info | end
-  static constexpr int kNumBars = 2 * kRing + 8 + 8 + kInfo + 1;
+  static constexpr uint32_t kBars = kRaw + kRing * kStage;
+  // raw full, raw empty | K full, K empty, V full, V empty (2 each) | S full, S free, P full, PV done (2 each) | info full, info free | end
+  static constexpr int kNumBars = 2 * kRing + 8 + 8 + 2 * kInfo + 1;
   static constexpr uint32_t kScale = kBars + ((kNumBars * 8 + 15) & ~15);  // [kInfo] BlockInfo
   static constexpr uint32_t kQs = kScale + kInfo * sizeof(BlockInfo);
   static constexpr uint32_t kMisc = kQs + MT * 128 * 4;
@@ -128,7 +129,7 @@ __device__ __forceinline__ void reg_dec() {
 }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w));
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -172,15 +173,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
   auto bar = [&](int i) { return smem_u32(bars + i); };
   constexpr int kRawFull = 0, kRawEmpty = G::kRing, kOpFull = 2 * G::kRing, kOpEmpty = kOpFull + 4,
                 kSFull = kOpEmpty + 4, kSFree = kSFull + 2, kPFull = kSFree + 2, kPvDone = kPFull + 2, kInfoFull = kPvDone + 2,
-                kEnd = kInfoFull + kInfo;  // operand barriers: 2 x side + buffer
+                kInfoFree = kInfoFull + kInfo, kEnd = kInfoFree + kInfo;  // operand barriers: 2 x side + buffer
   BlockInfo* infos = reinterpret_cast<BlockInfo*>(sm + G::kScale);
   float* q_scale = reinterpret_cast<float*>(sm + G::kQs);
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + G::kMisc);  // TMEM base
   const int active = (T.rows + 127) / 128;
   if (tid == 0) {
     for (int i = 0; i < G::kRing; ++i) {
-      mbar_init(bar(kRawFull + i), 1);
-      mbar_init(bar(kRawEmpty + i), 128);
+      mbar_init(bar(kRawFull + i), MT == 2 ? 1 : 2);
+      mbar_init(bar(kRawEmpty + i), MT == 2 ? 128 : 256);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(bar(kOpFull + i), 128);
@@ -192,7 +193,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       mbar_init(bar(kPFull + i), 128);
       mbar_init(bar(kPvDone + i), 1);
     }
-    for (int i = 0; i < kInfo; ++i) mbar_init(bar(kInfoFull + i), 1);
+    for (int i = 0; i < kInfo; ++i) {
+      mbar_init(bar(kInfoFull + i), 1);
+      mbar_init(bar(kInfoFree + i), 4 * active + 4);  // the warps that weigh, and those that expand V
+    }
     mbar_init(bar(kEnd), 2);
     mbar_init_fence();
   }
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       bool ok = true;
       for (int j = 0; j < cnt && ok; ++j) {
         const int sbuf = MT == 2 ? wg : j & 1;  // barrier and buffer of the logits
-        const int info = j & (kInfo - 1);
+        const int info = j % kInfo;
         ok = mbar_wait_bounded(bar(kInfoFull + info), (j / kInfo) & 1) &&
              mbar_wait_bounded(bar(kSFull + sbuf), MT == 2 ? j & 1 : (j >> 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -295,17 +299,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
         if ((bi.flags & (kFull0 << wg)) == 0) {
 #pragma unroll
           for (int pg = 0; pg < 8; ++pg) {
-            // bit c: the row sees position pp + c (a page that all rows of the warp see costs no selects)
             const int pp = bi.pos[pg];
-            const uint32_t upto = low_bits(pos - pp + 1), behind = ~low_bits(after - pp + 1), sinks = low_bits(a.sink - pp);
-            const uint32_t see = upto & (behind | sinks);
-            if (__any_sync(0xffffffffu, see != 0xffffu)) {
+            const int c_hi = pos - pp, c_lo = after - pp, c_sink = a.sink - pp;
 #pragma unroll
-              for (int c = 0; c < 16; ++c)
-                if ((see >> c & 1u) == 0) v[pg >> 1][(pg & 1) * 16 + c] = 0xff800000u;
-            }
+            for (int c = 0; c < 16; ++c)
+              if ((c > c_hi) | ((c <= c_lo) & (c >= c_sink))) v[pg >> 1][(pg & 1) * 16 + c] = 0xff800000u;
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kInfoFree + info));
         float mx = -INFINITY;
 #pragma unroll
         for (int pg = 0; pg < 8; ++pg) {
@@ -431,7 +433,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
     // Lanes of the second 64 channels take the neighbouring row, so that the eight lanes of a shared-memory access meet
     // all banks both where they read (chunk c) and where they write (chunk 2 (c % 4) ^ row % 8).
     const int c = pt % kChunks, r0 = (pt / kChunks) ^ (c >> 2);
-    const uint32_t src0 = sb + G::kRaw + r0 * D + c * 16;
+    // MT = 1: a page's K rows, then its V rows
+    const uint32_t src0 = sb + G::kRaw + c * 16 + (MT == 2 ? r0 * D : (r0 >> 4) * (2 * kPageSize * D) + (r0 & 15) * D);
+    constexpr uint32_t kSrcStep = (MT == 2 ? 1 : 2) * kStep * D;
     // channels 16 c .. + 15 of row r: chunks 2 (c % 4), + 1 of 64-channel block c / 4
     const uint32_t dst0 = sb + G::kK + (c >> 2) * (kTok * 128) + r0 * 128 + (((2 * (c & 3)) ^ (r0 & 7)) << 4);
     const uint32_t dst1 = sb + G::kK + (c >> 2) * (kTok * 128) + r0 * 128 + (((2 * (c & 3) + 1) ^ (r0 & 7)) << 4);
@@ -439,10 +443,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
 #pragma unroll 1
     for (int x = 0; x < (MT == 2 ? 2 : 1) * cnt; ++x) {
       const int j = MT == 2 ? x >> 1 : x, side = MT == 2 ? x & 1 : 2 - wg;
-      const int hf = 2 * j + side, st = hf % G::kRing, op = 2 * side + (j & 1);
-      ok = mbar_wait_bounded(bar(kRawFull + st), (hf / G::kRing) & 1) &&
-           (j < 2 || mbar_wait_bounded(bar(kOpEmpty + op), ((j >> 1) - 1) & 1)) &&
-           mbar_wait_bounded(bar(kInfoFull + (j & (kInfo - 1))), (j / kInfo) & 1);
+      const int op = 2 * side + (j & 1), st = x % G::kRing;
+      ok = mbar_wait_bounded(bar(kRawFull + st), (x / G::kRing) & 1) &&
+           mbar_wait_bounded(bar(kInfoFull + (j % kInfo)), (j / kInfo) & 1);
       if (!ok) break;
       // every load first: the units are independent, and a load waits for nothing but itself
       uint32_t w[kUnits][4];
@@ -450,9 +453,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       for (int i = 0; i < kUnits; ++i)
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
-                     : "r"(src0 + st * G::kHalf + i * (kStep * D))
+                     : "r"(src0 + st * G::kStage + (MT == 1 ? side * (kPageSize * D) : 0) + i * kSrcStep)
                      : "memory");
-      const BlockInfo& bi = infos[j & (kInfo - 1)];
+      mbar_arrive(bar(kRawEmpty + st));  // read: the next codes may come
+      ok = j < 2 || mbar_wait_bounded(bar(kOpEmpty + op), ((j >> 1) - 1) & 1);
+      if (!ok) break;
+      const BlockInfo& bi = infos[j % kInfo];
       if (side == 1 && (bi.flags & kTail)) {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
@@ -474,13 +480,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       }
       fence_async();
       mbar_arrive(bar(kOpFull + op));
-      mbar_arrive(bar(kRawEmpty + st));
+      if (side == 1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kInfoFree + j % kInfo));
+      }
     }
     if (!ok && lane == 0) record_error(OSCAR_DEVERR_TIMEOUT);
   } else {
     reg_dec<Regs<MT>::kIssue>();
     if (warp == kFetchK || warp == kFetchV) {
-      // ---- page ids, scales, copies of codes: K and block infos by one warp, V by another ---------------
+      // ---- page ids, scales, copies of codes: K by one warp, V by another (MT = 1: four pages each) -------------
       const int side = warp == kFetchV;
       const int32_t* table = a.page_table + static_cast<size_t>(b) * a.max_pages;
       // Four blocks at a time, a page a lane: the ids are loaded two groups ahead and the scales one,
@@ -510,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       bool ok = true;
       int issued = 0;
       for (int j = 0; j < cnt && ok; ++j) {
-        const int info = j & (kInfo - 1);
+        const int info = j % kInfo;
         if ((j & 3) == 0) {
           pid = pid1;
           sc = sc1;
@@ -519,15 +528,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           pid2 = look_up((j >> 2) + 2);
         }
         const bool mine = (lane >> 3) == (j & 3);  // this lane holds a page of block j
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine && pid >= 0)) * (kPageSize * D);
-        const int hf = 2 * j + side, st = hf % G::kRing;
-        if (hf >= G::kRing) ok = mbar_wait_bounded(bar(kRawEmpty + st), (hf / G::kRing - 1) & 1);
+        const bool copies = mine && pid >= 0 && (MT == 2 || ((lane >> 2) & 1) == side);
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, copies)) * ((MT == 2 ? 1 : 2) * kPageSize * D);
+        const int x = MT == 2 ? 2 * j + side : j, st = x % G::kRing;
+        if (x >= G::kRing) ok = mbar_wait_bounded(bar(kRawEmpty + st), (x / G::kRing - 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
         if (side == 0) {
-          // (block j - 8's readers are done: their weights came before the products that freed this stage)
+          if (j >= kInfo) ok = mbar_wait_bounded(bar(kInfoFree + info), (j / kInfo - 1) & 1);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
           const int pos = pid < 0 ? kNoPage : T.vis.page((blk0 + j) * kBlkPages + (lane & 7)) * kPageSize;
           float vmax = sc.y;
 #pragma unroll
@@ -553,27 +567,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kInfoFull + info));
         }
-        int ids[kBlkPages];
+        constexpr int kCopies = MT == 2 ? kBlkPages : kBlkPages / 2;
+        int ids[kCopies];
 #pragma unroll
-        for (int c = 0; c < kBlkPages; ++c) ids[c] = __shfl_sync(0xffffffffu, pid, (j & 3) * kBlkPages + c);
+        for (int c = 0; c < kCopies; ++c)
+          ids[c] = __shfl_sync(0xffffffffu, pid, (j & 3) * kBlkPages + c + (MT == 2 ? 0 : side * kCopies));
         if (issuer) {  // (one lane: eight lanes with a copy each take longer than one lane with eight)
           if (bytes > 0) mbar_arrive_expect_tx(bar(kRawFull + st), bytes);
           else mbar_arrive(bar(kRawFull + st));
+          const uint32_t dst = sb + G::kRaw + st * G::kStage;
 #pragma unroll
-          for (int c = 0; c < kBlkPages; ++c)
-            if (ids[c] >= 0)
-              bulk_g2s(sb + G::kRaw + st * G::kHalf + c * (kPageSize * D),
-                       a.pages + ((static_cast<size_t>(ids[c]) * a.H + h) * 2 + side) * (kPageSize * D), kPageSize * D,
-                       bar(kRawFull + st));
+          for (int c = 0; c < kCopies; ++c) {
+            if (ids[c] < 0) continue;
+            const uint8_t* src = a.pages + (static_cast<size_t>(ids[c]) * a.H + h) * (2 * kPageSize * D);
+            if (MT == 2) bulk_g2s(dst + c * (kPageSize * D), src + side * (kPageSize * D), kPageSize * D, bar(kRawFull + st));
+            else bulk_g2s(dst + (side * kCopies + c) * (2 * kPageSize * D), src, 2 * kPageSize * D, bar(kRawFull + st));
+          }
         }
         __syncwarp();
         issued = j + 1;
       }
       if (!ok) {  // wait for the copies in flight
         if (lane == 0) record_error(OSCAR_DEVERR_TIMEOUT);
-        for (int j = max(0, issued - G::kRing / 2); j < issued; ++j) {
-          const int hf = 2 * j + side;
-          mbar_wait_bounded(bar(kRawFull + hf % G::kRing), (hf / G::kRing) & 1);
+        constexpr int kBack = MT == 2 ? G::kRing / 2 : G::kRing;
+        for (int j = max(0, issued - kBack); j < issued; ++j) {
+          const int x = MT == 2 ? 2 * j + side : j;
+          mbar_wait_bounded(bar(kRawFull + x % G::kRing), (x / G::kRing) & 1);
         }
       }
     } else if (warp == kQkWarp || warp == kPvWarp) {
@@ -671,10 +690,6 @@ __global__ void __launch_bounds__(kMergeRows * 32) kv8_extend_merge_kernel(ExtAr
   merge_row<D>(ea.part_o + row * ea.ns * D, ea.part_ml + row * ea.ns * 2, n, a.out + row * D, threadIdx.x & 31);
 }
 
-#ifndef WANT
-#define WANT 4
-#endif
-constexpr long long kWantShort = WANT;
 struct Plan {
   int mt, tiles, ns, bps;
   size_t off_ml, total;
@@ -702,7 +717,9 @@ bool make_plan(const oscar_dims_t* d, int batch, int rows, int max_seq_len, int 
     long long units = static_cast<long long>(rows) * gqa / tm + batch;
     if (units > tiles * batch) units = tiles * batch;
     units *= d->num_kv_heads;
-    const long long want = (p->mt == 1 ? kWantShort : 2LL) * num_sms();
+    // CTAs per SM aimed at: short runs (bound by the pages' bytes) 3 -- with lengths of 1000 to 32768 and 8 sequences, 1: 160 us,
+    // 2: 139, 3: 114, 4: 128, 6: 135, 8: 149 -- and long runs 2.
+    const long long want = (p->mt == 1 ? 3LL : 2LL) * num_sms();
     const long long splits = units > 0 && units < want ? want / units : 1;
     bps = (blocks + splits - 1) / splits;
     if (bps < 4) bps = 4;
