@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
     mbar_arrive_expect_tx(bar, kPage);
     umma::tma_load_3d(my_ring + (i % kStages) * kPage, &map, 0, 0, pid * a.H + h, bar);
   };
-  if (lane == 0)
+  const bool issuer = umma::elect_one();
+  if (issuer)
     for (int i = 0; i < min(n_my, kStages); ++i) issue(i);
 
   // Q: lane (g, t) holds query g, channels 16 ks + 4 t .. + 3 (k = 2t, 2t+1, 2t+8, 2t+9 of k-step ks)
@@ -169,11 +170,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
       const uint32_t st = my_ring + (i % kStages) * kPage;
       const float2 sc = scale_s[k];
       const int pos0 = vis.page(v0 + k) * kPageSize;
-      float acc[2][4];
+      float acc[2][2][4];  // two chains of products per eight tokens
 #pragma unroll
       for (int th = 0; th < 2; ++th) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[th][c] = 0.f;
+        for (int c = 0; c < 4; ++c) acc[th][0][c] = acc[th][1][c] = 0.f;
 #pragma unroll
         for (int c4 = 0; c4 < kKs; c4 += 4) {
           uint32_t w[4];
@@ -182,12 +183,13 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
           for (int c = 0; c < 4; ++c) {
             uint32_t b0, b1;
             codes_to_f16<F>(w[c], b0, b1);
-            mma_f16(acc[th], qa[c4 + c][0], 0u, qa[c4 + c][1], 0u, b0, b1);
+            mma_f16(acc[th][c & 1], qa[c4 + c][0], 0u, qa[c4 + c][1], 0u, b0, b1);
           }
         }
       }
       // this lane's tokens: 2t, 2t+1, 2t+8, 2t+9
-      float sx[4] = {acc[0][0], acc[0][1], acc[1][0], acc[1][1]};
+      float sx[4] = {acc[0][0][0] + acc[0][1][0], acc[0][0][1] + acc[0][1][1], acc[1][0][0] + acc[1][1][0],
+                     acc[1][0][1] + acc[1][1][1]};
       const bool full = pos0 + kPageSize <= vis.end && (pos0 + kPageSize <= vis.sink_end || pos0 >= vis.lo);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
       }
     }
     __syncwarp();
-    if (lane == 0 && i + kStages < n_my) issue(i + kStages);
+    if (issuer && i + kStages < n_my) issue(i + kStages);
   }
   if (aborted) {  // a copy did not land: drop this warp's pages, once the copies in flight are over
     if (lane == 0) record_error(OSCAR_DEVERR_TIMEOUT);

@@ -63,9 +63,10 @@ constexpr uint32_t kFull0 = 1, kTail = 4;
 template <int D, int MT>
 struct Geo {
   static constexpr uint32_t kOp = kTok * D * 2;   // one fp16 operand: D / 64 blocks of 128 rows x 128 bytes
-  // Stages of codes: K or V of a block (MT = 2), or whole pages of a block (MT = 1: half as many copies to issue)
-  static constexpr uint32_t kStage = (MT == 2 ? 1 : 2) * kTok * D;
-  static constexpr int kRing = D == 128 ? 2 : (MT == 2 ? 8 : 4);
+  // Stages of codes: whole pages of a block where two of them fit (half as many copies to issue), else K or V of a block
+  static constexpr bool kWhole = MT == 1 || D == 64;
+  static constexpr uint32_t kStage = (kWhole ? 2 : 1) * kTok * D;
+  static constexpr int kRing = D == 128 ? 2 : 4;
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kK = MT * kOp;
   static constexpr uint32_t kV = kK + 2 * kOp;
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
   const int active = (T.rows + 127) / 128;
   if (tid == 0) {
     for (int i = 0; i < G::kRing; ++i) {
-      mbar_init(bar(kRawFull + i), MT == 2 ? 1 : 2);
+      mbar_init(bar(kRawFull + i), G::kWhole ? 2 : 1);
       mbar_init(bar(kRawEmpty + i), MT == 2 ? 128 : 256);
     }
     for (int i = 0; i < 4; ++i) {
@@ -433,9 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
     // Lanes of the second 64 channels take the neighbouring row, so that the eight lanes of a shared-memory access meet
     // all banks both where they read (chunk c) and where they write (chunk 2 (c % 4) ^ row % 8).
     const int c = pt % kChunks, r0 = (pt / kChunks) ^ (c >> 2);
-    // MT = 1: a page's K rows, then its V rows
-    const uint32_t src0 = sb + G::kRaw + c * 16 + (MT == 2 ? r0 * D : (r0 >> 4) * (2 * kPageSize * D) + (r0 & 15) * D);
-    constexpr uint32_t kSrcStep = (MT == 2 ? 1 : 2) * kStep * D;
+    // whole pages: a page's K rows, then its V rows
+    const uint32_t src0 = sb + G::kRaw + c * 16 + (G::kWhole ? (r0 >> 4) * (2 * kPageSize * D) + (r0 & 15) * D : r0 * D);
+    constexpr uint32_t kSrcStep = (G::kWhole ? 2 : 1) * kStep * D;
     // channels 16 c .. + 15 of row r: chunks 2 (c % 4), + 1 of 64-channel block c / 4
     const uint32_t dst0 = sb + G::kK + (c >> 2) * (kTok * 128) + r0 * 128 + (((2 * (c & 3)) ^ (r0 & 7)) << 4);
     const uint32_t dst1 = sb + G::kK + (c >> 2) * (kTok * 128) + r0 * 128 + (((2 * (c & 3) + 1) ^ (r0 & 7)) << 4);
@@ -443,8 +444,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
 #pragma unroll 1
     for (int x = 0; x < (MT == 2 ? 2 : 1) * cnt; ++x) {
       const int j = MT == 2 ? x >> 1 : x, side = MT == 2 ? x & 1 : 2 - wg;
-      const int op = 2 * side + (j & 1), st = x % G::kRing;
-      ok = mbar_wait_bounded(bar(kRawFull + st), (x / G::kRing) & 1) &&
+      const int op = 2 * side + (j & 1), rx = G::kWhole ? j : x, st = rx % G::kRing;
+      ok = mbar_wait_bounded(bar(kRawFull + st), (rx / G::kRing) & 1) &&
            mbar_wait_bounded(bar(kInfoFull + (j % kInfo)), (j / kInfo) & 1);
       if (!ok) break;
       // every load first: the units are independent, and a load waits for nothing but itself
@@ -453,9 +454,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       for (int i = 0; i < kUnits; ++i)
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
-                     : "r"(src0 + st * G::kStage + (MT == 1 ? side * (kPageSize * D) : 0) + i * kSrcStep)
+                     : "r"(src0 + st * G::kStage + (G::kWhole ? side * (kPageSize * D) : 0) + i * kSrcStep)
                      : "memory");
-      mbar_arrive(bar(kRawEmpty + st));  // read: the next codes may come
+      if (MT == 1 || !G::kWhole || side == 1) mbar_arrive(bar(kRawEmpty + st));  // read: the next codes may come
       ok = j < 2 || mbar_wait_bounded(bar(kOpEmpty + op), ((j >> 1) - 1) & 1);
       if (!ok) break;
       const BlockInfo& bi = infos[j % kInfo];
@@ -489,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
   } else {
     reg_dec<Regs<MT>::kIssue>();
     if (warp == kFetchK || warp == kFetchV) {
-      // ---- page ids, scales, copies of codes: K by one warp, V by another (MT = 1: four pages each) -------------
+      // ---- page ids, scales, copies of codes: K by one warp, V by another (whole pages: four each) --------------
       const int side = warp == kFetchV;
       const int32_t* table = a.page_table + static_cast<size_t>(b) * a.max_pages;
       // Four blocks at a time, a page a lane: the ids are loaded two groups ahead and the scales one,
@@ -528,9 +529,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           pid2 = look_up((j >> 2) + 2);
         }
         const bool mine = (lane >> 3) == (j & 3);  // this lane holds a page of block j
-        const bool copies = mine && pid >= 0 && (MT == 2 || ((lane >> 2) & 1) == side);
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, copies)) * ((MT == 2 ? 1 : 2) * kPageSize * D);
-        const int x = MT == 2 ? 2 * j + side : j, st = x % G::kRing;
+        const bool copies = mine && pid >= 0 && (!G::kWhole || ((lane >> 2) & 1) == side);
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, copies)) * ((G::kWhole ? 2 : 1) * kPageSize * D);
+        const int x = G::kWhole ? j : 2 * j + side, st = x % G::kRing;
         if (x >= G::kRing) ok = mbar_wait_bounded(bar(kRawEmpty + st), (x / G::kRing - 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
@@ -567,11 +568,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kInfoFull + info));
         }
-        constexpr int kCopies = MT == 2 ? kBlkPages : kBlkPages / 2;
+        constexpr int kCopies = G::kWhole ? kBlkPages / 2 : kBlkPages;
         int ids[kCopies];
 #pragma unroll
         for (int c = 0; c < kCopies; ++c)
-          ids[c] = __shfl_sync(0xffffffffu, pid, (j & 3) * kBlkPages + c + (MT == 2 ? 0 : side * kCopies));
+          ids[c] = __shfl_sync(0xffffffffu, pid, (j & 3) * kBlkPages + c + (G::kWhole ? side * kCopies : 0));
         if (issuer) {  // (one lane: eight lanes with a copy each take longer than one lane with eight)
           if (bytes > 0) mbar_arrive_expect_tx(bar(kRawFull + st), bytes);
           else mbar_arrive(bar(kRawFull + st));
@@ -580,8 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           for (int c = 0; c < kCopies; ++c) {
             if (ids[c] < 0) continue;
             const uint8_t* src = a.pages + (static_cast<size_t>(ids[c]) * a.H + h) * (2 * kPageSize * D);
-            if (MT == 2) bulk_g2s(dst + c * (kPageSize * D), src + side * (kPageSize * D), kPageSize * D, bar(kRawFull + st));
-            else bulk_g2s(dst + (side * kCopies + c) * (2 * kPageSize * D), src, 2 * kPageSize * D, bar(kRawFull + st));
+            if (G::kWhole) bulk_g2s(dst + (side * kCopies + c) * (2 * kPageSize * D), src, 2 * kPageSize * D, bar(kRawFull + st));
+            else bulk_g2s(dst + c * (kPageSize * D), src + side * (kPageSize * D), kPageSize * D, bar(kRawFull + st));
           }
         }
         __syncwarp();
@@ -589,9 +590,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       }
       if (!ok) {  // wait for the copies in flight
         if (lane == 0) record_error(OSCAR_DEVERR_TIMEOUT);
-        constexpr int kBack = MT == 2 ? G::kRing / 2 : G::kRing;
+        constexpr int kBack = G::kWhole ? G::kRing : G::kRing / 2;
         for (int j = max(0, issued - kBack); j < issued; ++j) {
-          const int x = MT == 2 ? 2 * j + side : j;
+          const int x = G::kWhole ? j : 2 * j + side;
           mbar_wait_bounded(bar(kRawFull + x % G::kRing), (x / G::kRing) & 1);
         }
       }
