@@ -504,15 +504,16 @@ oscar_status_t oscar_kv8_append(const oscar_dims_t* dims, int32_t kv_format, int
  * Arguments
  *   max_seq_len   host bound on every seq_lens[b] (<= max_pages_per_seq * P); larger or negative
  *                 device values are clamped and flagged (OSCAR_DEVERR_SEQ_LEN)
- *   pages_per_split  0 = chosen from the grid size; else >= 1 pages of one split (at most
- *                 65535 splits per sequence; batch <= 65535)
+ *   pages_per_split  0 = chosen from the grid size; else >= 1 pages of one split (no more than 512
+ *                 are taken; at most 65535 splits per sequence; batch <= 65535)
  *   q, out        device bf16 [batch][Hq][D], q 16-byte aligned, out 16-byte aligned.  The output has the
  *                 type of q (the projection that follows reads it); sums and softmax statistics are fp32
  *   kv8_pages, kv8_scales, page_table  as oscar_kv8_append
  *   sm_scale      softmax scale; <= 0 selects 1/sqrt(D)
  *   workspace     at least oscar_kv8_decode_workspace_bytes(...) bytes, 256-byte aligned; needs no
  *                 initialisation
- * A page id out of range attends nothing of that page and flags OSCAR_DEVERR_PAGE_ID.
+ * A page id out of range attends nothing of that page and flags OSCAR_DEVERR_PAGE_ID.  A NaN in a query row
+ * makes that row NaN.  What lies in pages or rows that hold no token of a sequence is never seen.
  */
 size_t oscar_kv8_decode_workspace_bytes(const oscar_dims_t* dims, int32_t batch, int32_t max_seq_len,
                                         int32_t pages_per_split, int32_t sink_len, int32_t window_len);
@@ -530,7 +531,7 @@ oscar_status_t oscar_kv8_decode(const oscar_dims_t* dims, int32_t kv_format, int
  * oscar_kv8_decode.  Arguments as oscar_extend_varlen and oscar_kv8_decode:
  *   num_rows          q_start[batch]; q and out are bf16 [num_rows][Hq][D]
  *   max_rows_per_seq  host bound on every n_b (sizes the grid)
- *   pages_per_split   0 = chosen from the grid size; else >= 1
+ *   pages_per_split   0 = chosen from the grid size; else >= 1 (rounded up to blocks of 8 pages)
  *   q_start           device int32 [batch + 1], non-decreasing, q_start[0] = 0
  * Rows that outnumber their sequence's tokens (n_b > L) have no position: they give zeros and
  * flag OSCAR_DEVERR_POSITION.  A q_start that decreases, leaves [0, num_rows] or makes n_b larger
@@ -558,8 +559,8 @@ oscar_status_t oscar_kv8_extend_varlen(const oscar_dims_t* dims, int32_t kv_form
  *               j < ceil(seq_lens[b] / P) that are >= 0; other entries are neither read nor
  *               counted
  *   seq_lens    device int32 [batch]
- *   page_refs   device int32 [num_pages]: the number of page table entries that hold the page;
- *               0 is free.  This is the allocator's whole state (all zeros at the start)
+ *   page_refs   device int32 [num_pages], 16-byte aligned: the number of page table entries that hold
+ *               the page; 0 is free.  This is the allocator's whole state (all zeros at the start)
  *   pools       host array of num_pools (0 .. OSCAR_MAX_POOLS) pools; base is 16-byte aligned, page i is
  *               the page_bytes bytes at base + i * page_bytes, page_bytes a multiple of 4
  * Free pages are handed out lowest id first, in the order of the requests, so results do not

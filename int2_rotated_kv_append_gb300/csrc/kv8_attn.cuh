@@ -35,6 +35,7 @@ static inline oscar_status_t make_args(const oscar_dims_t* dims, int batch, int 
   if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return OSCAR_ERR_INVALID_ARG;
   if (workspace_bytes < need) return OSCAR_ERR_WORKSPACE;
   if (static_cast<long long>(dims->num_pages) * dims->num_kv_heads > 0x7fffffffLL) return OSCAR_ERR_UNSUPPORTED;
+  if (window >= max_seq_len) window = 0;  // hides nothing
   const float scale = sm_scale > 0.f ? sm_scale : 1.0f / sqrtf(static_cast<float>(dims->head_dim));
   *a = AttnArgs{static_cast<const __nv_bfloat16*>(q), pages, scales, page_table, seq_lens, q_start,
                 static_cast<__nv_bfloat16*>(out), batch, rows, max_rows, dims->num_q_heads, dims->num_kv_heads,
@@ -65,9 +66,9 @@ __device__ __forceinline__ int clamped_len(const AttnArgs& a, int b) {
   return L;
 }
 
-// Four channels of an output row: o / l, 0 where nothing was attended.
+// Four channels of an output row: o / l, 0 where nothing was attended (a NaN of the query stays one).
 __device__ __forceinline__ void store_out4(__nv_bfloat16* out, float4 o, float l) {
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv), y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
   *reinterpret_cast<uint2*>(out) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));

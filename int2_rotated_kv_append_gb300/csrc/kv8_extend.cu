@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       const size_t row = store ? out_row(r) : 0;
       const float unit = ok ? vref * (1.f / (1 << kBoost)) : 0.f;
       if (!ok) l = 0.f;
-      const float inv = l > 0.f ? unit / l : 0.f;
+      const float inv = l == 0.f ? 0.f : unit / l;
 #pragma unroll 2
       for (int c = 0; c < D / 16; ++c) {
         uint32_t o[16];
@@ -404,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           uint32_t y[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const __nv_bfloat162 z = __floats2bfloat162_rn(l > 0.f ? __uint_as_float(o[2 * e]) * inv : 0.f,
-                                                           l > 0.f ? __uint_as_float(o[2 * e + 1]) * inv : 0.f);
+            const __nv_bfloat162 z = __floats2bfloat162_rn(l == 0.f ? 0.f : __uint_as_float(o[2 * e]) * inv,
+                                                           l == 0.f ? 0.f : __uint_as_float(o[2 * e + 1]) * inv);
             y[e] = *reinterpret_cast<const uint32_t*>(&z);
           }
           uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + 16 * c);
@@ -415,14 +415,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           float4* dst = reinterpret_cast<float4*>(ea.part_o + (row * ea.ns + split) * D + 16 * c);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            dst[e] = l > 0.f ? make_float4(__uint_as_float(o[4 * e]) * unit, __uint_as_float(o[4 * e + 1]) * unit,
-                                           __uint_as_float(o[4 * e + 2]) * unit, __uint_as_float(o[4 * e + 3]) * unit)
-                             : make_float4(0.f, 0.f, 0.f, 0.f);
+            dst[e] = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                              : make_float4(__uint_as_float(o[4 * e]) * unit, __uint_as_float(o[4 * e + 1]) * unit,
+                                            __uint_as_float(o[4 * e + 2]) * unit, __uint_as_float(o[4 * e + 3]) * unit);
         }
       }
       if (store && !single)
         *reinterpret_cast<float2*>(ea.part_ml + (row * ea.ns + split) * 2) =
-            make_float2(l > 0.f ? m : -INFINITY, l);
+            make_float2(l == 0.f ? -INFINITY : m, l);
     }
   } else if (wg < 3) {
     // ---- codes -> fp16 operands: K and V in turn (MT = 2), V or K (MT = 1: warpgroups 1 and 2) ------------

@@ -263,3 +263,98 @@ def test_captured_and_replayed_with_growing_lengths():
         c.lens_d.copy_(torch.tensor(lens))
         graph.replay()
         c.check(out, q, [0, 1], [n - 1 for n in lens], sink=8, window=500)
+
+
+@pytest.mark.parametrize("D,rows", [(128, [1, 8, 3, 0]), (64, [1, 8, 3, 0]), (128, [300, 200, 100, 77])])
+def test_extend_is_the_same_on_cold_caches(D, rows):
+    # the first pass after other data went through L2 meets every copy late: results have to be the same bits
+    import time
+    lens = [9000, 333, 5000, 12000]
+    c = Cache(2, D, R.INT8, lens, seed=17)
+    q = c.q(sum(rows), 16)
+    big = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    for pps in (8, 16, 64):
+        want = c.extend(q, rows, pps=pps)
+        for i in range(25):
+            big.fill_(i)
+            torch.cuda.synchronize()
+            time.sleep(0.001)
+            assert torch.equal(c.extend(q, rows, pps=pps), want), (pps, i)
+
+
+def test_pages_far_into_a_large_pool():
+    # byte offsets beyond 32 bits: 150000 pages of 32 KB, the cache in the last ones
+    n, H, D, L = 150000, 8, 128, 300
+    small = Cache(H, D, R.E4M3, [L], seed=18)
+    ids = torch.tensor([n - 1 - 3 * i for i in range(19)], dtype=torch.int32)
+    codes = torch.empty(n, H, 2, 16, D, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(n, H, 2, device="cuda")
+    codes[ids.cuda().long()] = small.codes[small.table_d[0].long()]
+    scales[ids.cuda().long()] = small.scales[small.table_d[0].long()]
+    big = Cache(H, D, R.E4M3, [L], seed=18)
+    big.codes, big.scales, big.table_d = codes, scales, ids.cuda()[None].contiguous()
+    big.dims = lambda hq: ok.make_dims(hq, H, D, 16, D, n, 19)
+    q, qx = small.q(1, 32), small.q(150, 32)
+    assert torch.equal(big.decode(q), small.decode(q))
+    assert torch.equal(big.extend(qx, [150]), small.extend(qx, [150]))
+    assert torch.equal(big.extend(qx[:20], [20]), small.extend(qx[:20], [20]))
+    k, v = (torch.randn(1, H, D, device="cuda").bfloat16() for _ in range(2))
+    lens = torch.tensor([L + 1], dtype=torch.int32, device="cuda")
+    for c in (big, small):
+        ok.oscar_kv8_append(c.dims(32), R.E4M3, 1, 1, k, v, torch.tensor([0, 1], dtype=torch.int32, device="cuda"), c.table_d, lens,
+                            c.codes, c.scales)
+    assert torch.equal(codes[ids[-1].item()], small.codes[small.table[0, -1].item()])
+
+
+def test_nan_queries_stay_in_their_rows():
+    c = Cache(2, 128, R.E4M3, [700, 90], seed=19)
+    q = c.q(2, 8)
+    want = c.decode(q)
+    bad = q.clone()
+    bad[0, 3, 5] = float("nan")
+    out = c.decode(bad)
+    assert out[0, 3].isnan().all()
+    out[0, 3] = want[0, 3]
+    assert torch.equal(out, want)
+    for rows, pps in (([40, 2], 0), ([300, 90], 0), ([3, 1], 8)):
+        q = c.q(sum(rows), 8)
+        want = c.extend(q, rows, pps=pps)
+        bad = q.clone()
+        bad[1, 6, 100] = float("nan")
+        out = c.extend(bad, rows, pps=pps)
+        assert out[1, 6].isnan().all()
+        out[1, 6] = want[1, 6]
+        assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("window", [700, 10 ** 6, 2 ** 31 - 1])
+def test_a_window_over_the_whole_cache_is_no_window(window):
+    c = Cache(2, 64, R.INT8, [700, 90], seed=20)
+    q, qx = c.q(2, 8), c.q(200, 8)
+    assert torch.equal(c.decode(q, 2 ** 31 - 1, window), c.decode(q))
+    assert torch.equal(c.extend(qx, [150, 50], 3, window), c.extend(qx, [150, 50]))
+
+
+def test_calls_on_two_streams_at_once():
+    c = Cache(2, 128, R.INT8, [3000, 1500], seed=21)
+    q, qx = c.q(2, 8), c.q(300, 8)
+    want, wantx = c.decode(q), c.extend(qx, [200, 100])
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(20):
+        with torch.cuda.stream(a):
+            got.append((c.decode(q), want))
+        with torch.cuda.stream(b):
+            got.append((c.extend(qx, [200, 100]), wantx))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in got)
+
+
+def test_a_reserved_token_without_an_append_is_zero():
+    # zeroed pools: code 0 and scale 0
+    c = Cache(1, 128, R.E4M3, [40], seed=22)
+    c.codes.zero_()
+    c.scales.zero_()
+    assert (c.decode(c.q(1, 4)) == 0).all() and (c.extend(c.q(40, 4), [40]) == 0).all()
+    assert (c.extend(c.q(3, 4), [3]) == 0).all()
