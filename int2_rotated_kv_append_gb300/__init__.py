@@ -142,7 +142,10 @@ def make_dims(num_q_heads, num_kv_heads, head_dim, page_size, group_size, num_pa
 def _dims(d) -> oscar_dims_t:
     if isinstance(d, oscar_dims_t):
         return d
-    return make_dims(**d)
+    try:
+        return oscar_dims_t(**d)
+    except TypeError:  # numbers of other types
+        return make_dims(**d)
 
 
 def _ptr(t) -> int | None:

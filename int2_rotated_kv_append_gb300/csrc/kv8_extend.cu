@@ -100,6 +100,7 @@ __device__ __forceinline__ Tile tile_of(const AttnArgs& a, int b, int tile) {
   Tile t;
   t.q0 = __ldg(a.q_start + b);
   const int q1 = __ldg(a.q_start + b + 1);
+  t.L = clamped_len(a, b);
   t.n = q1 - t.q0;
   t.ok = t.n >= 0 && t.n <= a.max_rows && t.q0 >= 0 && q1 <= a.rows;
   if (!t.ok) {
@@ -111,7 +112,6 @@ __device__ __forceinline__ Tile tile_of(const AttnArgs& a, int b, int tile) {
   t.rows = min(TM, t.n * gqa - t.r0);
   t.ok = t.rows > 0;
   if (!t.ok) return t;
-  t.L = clamped_len(a, b);
   const int first = t.L - t.n + t.r0 / gqa, last = t.L - t.n + (t.r0 + t.rows - 1) / gqa;
   if (first < 0) record_error(OSCAR_DEVERR_POSITION);
   t.vis = visible(max(first, 0), last, a.sink, a.window);
@@ -205,46 +205,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
   const int wg = warp >> 2;
   const bool fetches = warp == kFetchK || warp == kFetchV;  // these start at once; the others get Q and TMEM ready
   if (warp == kQkWarp) umma::tmem_alloc(smem_u32(misc), 512);
-  // Q as fp16, K-major with the 128-byte swizzle; a warp per row, lane l channels (D / 32) l ..
+  // Q as fp16, K-major with the 128-byte swizzle: a lane takes 8 channels of a row, and every load is in flight at once
   if (wg < 3) {
-    constexpr int kPer = D / 32, kWords = kPer / 2, kBatch = 6, kLoaders = 12;  // six rows' loads in flight a warp
-    for (int r0 = warp; r0 < active * 128; r0 += kBatch * kLoaders) {
-      uint32_t x[kBatch][kWords];
+    constexpr int kLanes = D / 8, kAtOnce = 12 * 32 / kLanes;  // lanes of a row; rows of one round of the 12 warps
+    constexpr int kRounds = (MT * 128 + kAtOnce - 1) / kAtOnce;
+    const int c = lane % kLanes, r0 = tid / kLanes;
+    int x = T.r0 + r0, i = x / gqa, hd = x - i * gqa;
+    const __nv_bfloat16* src = a.q + (static_cast<size_t>(T.q0) * a.Hq + h * gqa) * D + 8 * c;
+    uint4 v[kRounds];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = r0 + i * kLoaders;
-#pragma unroll
-        for (int c = 0; c < kWords; ++c) x[i][c] = 0u;
-        if (r < T.rows) {
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + out_row(r) * D) + lane * kWords;
-          if constexpr (kWords == 2) {
-            const uint2 y = __ldg(reinterpret_cast<const uint2*>(src));
-            x[i][0] = y.x;
-            x[i][1] = y.y;
-          } else {
-            x[i][0] = __ldg(src);
-          }
-        }
+    for (int k = 0; k < kRounds; ++k) {
+      v[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (r0 + k * kAtOnce < T.rows)
+        v[k] = __ldg(reinterpret_cast<const uint4*>(src + (static_cast<size_t>(i) * a.Hq + hd) * D));
+      i += kAtOnce / gqa;
+      hd += kAtOnce % gqa;
+      if (hd >= gqa) {
+        hd -= gqa;
+        ++i;
       }
+    }
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = r0 + i * kLoaders;
-        uint32_t mx = x[i][0] & 0x7fff7fffu;
-        if constexpr (kWords == 2) mx = __vmaxu2(mx, x[i][1] & 0x7fff7fffu);
-        mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
-        const int e = min(max(static_cast<int>(mx >> 7) - 127, -126), 126);
-        const float inv = pow2i(-e);
-        uint32_t y[kWords];
+    for (int k = 0; k < kRounds; ++k) {
+      const int r = r0 + k * kAtOnce;
+      uint32_t mx = __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
+                             __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu));
 #pragma unroll
-        for (int c = 0; c < kWords; ++c)
-          y[c] = half2_bits(__uint_as_float(x[i][c] << 16) * inv, __uint_as_float(x[i][c] & 0xffff0000u) * inv);
-        if (r >= active * 128) break;
-        const uint32_t dst = sb + G::kQ + (r >> 7) * G::kOp + umma::sw128_offset(r & 127, lane * kPer, 128);
-        if constexpr (kWords == 2)
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(y[0]), "r"(y[1]) : "memory");
-        else
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(y[0]) : "memory");
-        if (lane == 0) q_scale[r] = pow2i(e) * a.scale_log2;
+      for (int o = 1; o < kLanes; o <<= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      mx = max(mx & 0xffffu, mx >> 16);
+      const int e = min(max(static_cast<int>(mx >> 7) - 127, -126), 126);
+      const float inv = pow2i(-e);
+      const uint32_t in[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      uint32_t y[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        y[q] = half2_bits(__uint_as_float(in[q] << 16) * inv, __uint_as_float(in[q] & 0xffff0000u) * inv);
+      if (r < active * 128) {
+        st_shared_v4(sb + G::kQ + (r >> 7) * G::kOp + umma::sw128_offset(r & 127, 8 * c, 128), y[0], y[1], y[2], y[3]);
+        if (c == 0) q_scale[r] = pow2i(e) * a.scale_log2;
       }
     }
   }
@@ -446,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       const int j = MT == 2 ? x >> 1 : x, side = MT == 2 ? x & 1 : 2 - wg;
       const int op = 2 * side + (j & 1), rx = G::kWhole ? j : x, st = rx % G::kRing;
       ok = mbar_wait_bounded(bar(kRawFull + st), (rx / G::kRing) & 1) &&
-           mbar_wait_bounded(bar(kInfoFull + (j % kInfo)), (j / kInfo) & 1);
+           (side == 0 || mbar_wait_bounded(bar(kInfoFull + j % kInfo), (j / kInfo) & 1));
       if (!ok) break;
       // every load first: the units are independent, and a load waits for nothing but itself
       uint32_t w[kUnits][4];
@@ -537,6 +535,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           ok = false;
           break;
         }
+        constexpr int kCopies = G::kWhole ? kBlkPages / 2 : kBlkPages;
+        int ids[kCopies];
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c)
+          ids[c] = __shfl_sync(0xffffffffu, pid, (j & 3) * kBlkPages + c + (G::kWhole ? side * kCopies : 0));
+        if (issuer) {  // (one lane: eight lanes with a copy each take longer than one lane with eight)
+          if (bytes > 0) mbar_arrive_expect_tx(bar(kRawFull + st), bytes);
+          else mbar_arrive(bar(kRawFull + st));
+          const uint32_t dst = sb + G::kRaw + st * G::kStage;
+#pragma unroll
+          for (int c = 0; c < kCopies; ++c) {
+            if (ids[c] < 0) continue;
+            const uint8_t* src = a.pages + (static_cast<size_t>(ids[c]) * a.H + h) * (2 * kPageSize * D);
+            if (G::kWhole) bulk_g2s(dst + (side * kCopies + c) * (2 * kPageSize * D), src, 2 * kPageSize * D, bar(kRawFull + st));
+            else bulk_g2s(dst + c * (kPageSize * D), src + side * (kPageSize * D), kPageSize * D, bar(kRawFull + st));
+          }
+        }
+        __syncwarp();
+        issued = j + 1;
         if (side == 0) {
           if (j >= kInfo) ok = mbar_wait_bounded(bar(kInfoFree + info), (j / kInfo - 1) & 1);
           if (!__all_sync(0xffffffffu, ok)) {
@@ -568,25 +585,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kInfoFull + info));
         }
-        constexpr int kCopies = G::kWhole ? kBlkPages / 2 : kBlkPages;
-        int ids[kCopies];
-#pragma unroll
-        for (int c = 0; c < kCopies; ++c)
-          ids[c] = __shfl_sync(0xffffffffu, pid, (j & 3) * kBlkPages + c + (G::kWhole ? side * kCopies : 0));
-        if (issuer) {  // (one lane: eight lanes with a copy each take longer than one lane with eight)
-          if (bytes > 0) mbar_arrive_expect_tx(bar(kRawFull + st), bytes);
-          else mbar_arrive(bar(kRawFull + st));
-          const uint32_t dst = sb + G::kRaw + st * G::kStage;
-#pragma unroll
-          for (int c = 0; c < kCopies; ++c) {
-            if (ids[c] < 0) continue;
-            const uint8_t* src = a.pages + (static_cast<size_t>(ids[c]) * a.H + h) * (2 * kPageSize * D);
-            if (G::kWhole) bulk_g2s(dst + (side * kCopies + c) * (2 * kPageSize * D), src, 2 * kPageSize * D, bar(kRawFull + st));
-            else bulk_g2s(dst + c * (kPageSize * D), src + side * (kPageSize * D), kPageSize * D, bar(kRawFull + st));
-          }
-        }
-        __syncwarp();
-        issued = j + 1;
       }
       if (!ok) {  // wait for the copies in flight
         if (lane == 0) record_error(OSCAR_DEVERR_TIMEOUT);
