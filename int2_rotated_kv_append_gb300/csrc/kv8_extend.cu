@@ -18,9 +18,9 @@
 // Scales stay out of the operands.  Q is scaled per row by a power of two to below 2, where fp16 holds
 // it to 2^-25 of the row's largest element; a page's K scale multiplies its 16 logits.  V codes carry the ratio of their page's scale to the
 // block's largest, vmax (a power of two, exact down to 2^-24), and the weights carry vmax / vref, vref the largest
-// scale so far.  Weights are p 2^7 vmax / vref, rounded to fp16 (11 bits: a tenth of the output's own
-// rounding), where p = 2^(s - m) <= 2^8 as the running maximum m is only moved when a logit passes it
-// by 8.  O is rescaled in TMEM when m or vref moves.  Sums are fp32 over the unrounded weights.
+// scale so far.  Weights are p 2^3 vmax / vref, rounded to fp16 (11 bits: a tenth of the output's own
+// rounding), where p = 2^(s - m) <= 2^12 as the running maximum m is only moved when a logit passes it
+// by 12.  O is rescaled in TMEM when m or vref moves.  Sums are fp32 over the unrounded weights.
 // Bound by the tensor cores for long runs of rows, by the pages' bytes for short ones.
 #include <math.h>
 
@@ -36,8 +36,9 @@ constexpr int kThreads = 512;
 constexpr int kTok = 128;
 constexpr int kBlkPages = kTok / kPageSize;
 constexpr int kInfo = 6;          // blocks whose scales and positions are kept
-constexpr float kLazy = 8.f;      // log2: how far a logit may pass the maximum in use
-constexpr int kBoost = 7;         // weights are stored times 2^kBoost: 2^(kLazy + kBoost) < 65504
+constexpr float kLazy = 12.f;     // log2: how far a logit may pass the maximum in use (with 8, some row of a warp passed it
+                                  // in most blocks, and the rescale took 550 of 3400 clocks)
+constexpr int kBoost = 3;         // weights are stored times 2^kBoost: 2^(kLazy + kBoost) < 65504
 constexpr int kQkWarp = 12, kFetchK = 13, kPvWarp = 14, kFetchV = 15;
 // Registers a thread: 512 x 128 at launch, divided among the warpgroups by setmaxnreg
 constexpr int kRegsLaunch = 128;
@@ -298,11 +299,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
         if ((bi.flags & (kFull0 << wg)) == 0) {
 #pragma unroll
           for (int pg = 0; pg < 8; ++pg) {
+            // bit c: the row sees position pp + c
             const int pp = bi.pos[pg];
-            const int c_hi = pos - pp, c_lo = after - pp, c_sink = a.sink - pp;
+            const uint32_t see = low_bits(pos - pp + 1) & (~low_bits(after - pp + 1) | low_bits(a.sink - pp));
 #pragma unroll
             for (int c = 0; c < 16; ++c)
-              if ((c > c_hi) | ((c <= c_lo) & (c >= c_sink))) v[pg >> 1][(pg & 1) * 16 + c] = 0xff800000u;
+              if ((see & (1u << c)) == 0) v[pg >> 1][(pg & 1) * 16 + c] = 0xff800000u;
           }
         }
         __syncwarp();

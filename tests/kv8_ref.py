@@ -82,9 +82,9 @@ def attention(codes, scales, q, row_seq, row_pos, table, fmt, sink, window, sm_s
     (an error of d in a logit changes weights by a factor 1 + d, numerator and denominator).
 
     Weights held in fp16 have a smallest step.  Decode: two parts, a step of 2^-14 2^-12 2^-24 = 2^-50 of the largest
-    weight beside them.  Extend: w 2^7 s / r, s the block's and r the largest V scale, has a step of 2^-24, so a
-    weight is off by at most 2^-25 2^-7 r / s of one whose exponential is 1 (the sum has at least that); it
-    meets |v| <= M s with M r < 2 max |v|, as a block's largest code is over M / 2: 2^-31 max |v| for each of n
+    weight beside them.  Extend: w 2^3 s / r, s the block's and r the largest V scale, has a step of 2^-24, so a
+    weight is off by at most 2^-25 2^-3 r / s of one whose exponential is 1 (the sum has at least that); it
+    meets |v| <= M s with M r < 2 max |v|, as a block's largest code is over M / 2: 2^-27 max |v| for each of n
     visible tokens.  There a V code c s' / s is held to a step of 2^-24 as well: 2^-25 r < 2^-31 max |v| once more
     (M / 2 > 2^5).  Both matter only where every larger weight meets a value of 0."""
     R, hq, D = q.shape
@@ -119,7 +119,7 @@ def attention(codes, scales, q, row_seq, row_pos, table, fmt, sink, window, sm_s
             o, a = w @ vv / total, w @ vv.abs() / total
             dlog = (D + 16) * 2.0 ** -24 * (qq.abs() @ kk.abs().T * scale).amax(1, keepdim=True)
             out[rows, h] = o
-            tol[rows, h] = 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.0 ** -12) * a + 2 * dlog * a + (see.sum(1, keepdim=True) + 1) * 2.0 ** -31 * vv.abs().max()
+            tol[rows, h] = 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.0 ** -12) * a + 2 * dlog * a + (see.sum(1, keepdim=True) + 1) * 2.0 ** -27 * vv.abs().max()
     return out, tol
 
 
