@@ -271,11 +271,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       const int after = a.window > 0 ? max(pos - a.window, -1) : -1;  // visible: behind it, or a sink
       float m = -INFINITY, l = 0.f, vref = 0.f;
       bool ok = true;
-      for (int j = 0; j < cnt && ok; ++j) {
+      for (int j = 0; j < cnt; ++j) {
         const int sbuf = MT == 2 ? wg : j & 1;  // barrier and buffer of the logits
         const int info = j % kInfo;
-        ok = mbar_wait_bounded(bar(kInfoFull + info), (j / kInfo) & 1) &&
-             mbar_wait_bounded(bar(kSFull + sbuf), MT == 2 ? j & 1 : (j >> 1) & 1);
+        // (the block's info was there before its K was expanded, so before these logits)
+        ok = ok && mbar_wait_bounded(bar(kSFull + sbuf), MT == 2 ? j & 1 : (j >> 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -323,10 +323,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
         // for in its turn: a parity says nothing two phases ahead.)
         if (j > 0) {
           ok = mbar_wait_bounded(bar(kPvDone + (MT == 2 ? wg : 0)), (j - 1) & 1);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
           umma::fence_after_sync();
         }
         const bool move = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
@@ -446,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       const int j = MT == 2 ? x >> 1 : x, side = MT == 2 ? x & 1 : 2 - wg;
       const int op = 2 * side + (j & 1), rx = G::kWhole ? j : x, st = rx % G::kRing;
       ok = mbar_wait_bounded(bar(kRawFull + st), (rx / G::kRing) & 1) &&
-           (side == 0 || mbar_wait_bounded(bar(kInfoFull + j % kInfo), (j / kInfo) & 1));
+           mbar_wait_bounded(bar(kInfoFull + j % kInfo), (j / kInfo) & 1);
       if (!ok) break;
       // every load first: the units are independent, and a load waits for nothing but itself
       uint32_t w[kUnits][4];
