@@ -12,16 +12,20 @@
 //                 TMEM as fp16.
 // TMEM (512 columns): with MT = 2 one logit buffer (128) for both row tiles, which is free again once a row tile has
 // it in registers, so that the next logits of either tile are formed while both compute weights; a weight
-// buffer (64) and an accumulator (D) per row tile.  (With the weights over a tile's own logits, its next
-// product waited for its softmax and PV: 3650 clocks a block instead of 2700.)  With MT = 1 two logit buffers
-// alternate.
-// Scales stay out of the operands.  Q is scaled per row by a power of two to below 2, where fp16 holds
-// it to 2^-25 of the row's largest element; a page's K scale multiplies its 16 logits.  V codes carry the ratio of their page's scale to the
-// block's largest, vmax (a power of two, exact down to 2^-24), and the weights carry vmax / vref, vref the largest
-// scale so far.  Weights are p 2^3 vmax / vref, rounded to fp16 (11 bits: a tenth of the output's own
-// rounding), where p = 2^(s - m) <= 2^12 as the running maximum m is only moved when a logit passes it
-// by 12.  O is rescaled in TMEM when m or vref moves.  Sums are fp32 over the unrounded weights.
-// Bound by the tensor cores for long runs of rows, by the pages' bytes for short ones.
+// buffer (64) and an accumulator (D) per row tile.  With MT = 1 two logit buffers alternate.
+// Scales stay out of the operands.  Q is scaled per row by a power of two to below 2, where fp16 holds it to 2^-25
+// of the row's largest element; a page's K scale multiplies its 16 logits.  V codes carry the ratio of their
+// page's scale to the block's largest, vmax (a power of two, exact down to 2^-24), and the weights carry
+// vmax / vref, vref the largest scale so far.  Weights are p 2^3 vmax / vref, rounded to fp16 (11 bits: a tenth of
+// the output's own rounding), where p = 2^(s - m) <= 2^12 as the running maximum m is only moved when a logit
+// passes it by 12.  O is rescaled in TMEM when m or vref moves.  Sums are fp32 over the unrounded weights.
+//
+// Measured (GB300, 2070 MHz): 8192 rows over 16384 positions, 32 query heads, 8 KV heads, D = 128, e4m3: 1.20 ms,
+// 1370 TFLOP/s, 71% of a cuBLAS bf16 product's rate.  A block takes 3300 clocks where the products alone would take 2050: the
+// softmax of a row tile (1900: 512 of them exponentials, the rest the latencies of its waits and loads) and the expansion
+// (about 2000 for K and V) run beside them on the same schedulers and the same shared-memory port.  One to eight rows of 8
+// sequences of up to 32768 positions (bound by 274 MB of codes): 102 us, 2.7 TB/s: a block takes one softmax
+// warpgroup 2300 clocks where the codes would arrive in 1400.
 #include <math.h>
 
 #include "kv8_attn.cuh"
@@ -36,8 +40,9 @@ constexpr int kThreads = 512;
 constexpr int kTok = 128;
 constexpr int kBlkPages = kTok / kPageSize;
 constexpr int kInfo = 6;          // blocks whose scales and positions are kept
-constexpr float kLazy = 12.f;     // log2: how far a logit may pass the maximum in use (with 8, some row of a warp passed it
-                                  // in most blocks, and the rescale took 550 of 3400 clocks)
+// log2: how far a logit may pass the maximum in use (with 8, some row of a warp passed it in most blocks, and the
+// rescale took 550 of 3400 clocks)
+constexpr float kLazy = 12.f;
 constexpr int kBoost = 3;         // weights are stored times 2^kBoost: 2^(kLazy + kBoost) < 65504
 constexpr int kQkWarp = 12, kFetchK = 13, kPvWarp = 14, kFetchV = 15;
 // Registers a thread: 512 x 128 at launch, divided among the warpgroups by setmaxnreg
@@ -73,7 +78,8 @@ struct Geo {
   static constexpr uint32_t kV = kK + 2 * kOp;
   static constexpr uint32_t kRaw = kV + 2 * kOp;
   static constexpr uint32_t kBars = kRaw + kRing * kStage;
-  // raw full, raw empty | K full, K empty, V full, V empty (2 each) | S full, S free, P full, PV done (2 each) | info full, info free | end
+  // raw full, raw empty | K full, K empty, V full, V empty (2 each) | S full, S free, P full, PV done (2 each) |
+  // info full, info free | end
   static constexpr int kNumBars = 2 * kRing + 8 + 8 + 2 * kInfo + 1;
   static constexpr uint32_t kScale = kBars + ((kNumBars * 8 + 15) & ~15);  // [kInfo] BlockInfo
   static constexpr uint32_t kQs = kScale + kInfo * sizeof(BlockInfo);
