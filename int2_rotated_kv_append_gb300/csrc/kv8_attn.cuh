@@ -74,19 +74,19 @@ __device__ __forceinline__ void store_out4(__nv_bfloat16* out, float4 o, float l
       make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
-// One warp: partials first, first + step, ... of n (o [n][D] unnormalised, ml [n][2] = maximum in log2 units,
-// sum): l and four channels r of lane's c4 = lane % (D / 4), relative to the maximum `base`.  Eight partials are in flight
-// at once.
+// One warp: partials first, first + step, ... of n (o [n][D] unnormalised, ml [n][2] = maximum in log2
+// units, sum): l and four channels r of lane's c4 = lane % (D / 4), relative to the largest of all n maxima (0 where
+// there is none).  Eight partials are in flight at once, the first of them while the maximum is found.
 template <int D>
-__device__ __forceinline__ void merge_part(const float* o, const float* ml, int n, int first, int step, float base,
-                                           int lane, float& l, float4& r) {
+__device__ __forceinline__ void merge_part(const float* o, const float* ml, int n, int first, int step, int lane,
+                                           float& l, float4& r) {
   constexpr int kSub = 128 / D, kFly = 8;  // D = 64: two half warps take every second partial
   const int sub = lane / (D / 4), c4 = lane % (D / 4);
   l = 0.f;
   r = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = first * kSub + sub; i0 < n; i0 += step * kSub * kFly) {
-    float4 x[kFly];
-    float2 p[kFly];
+  float4 x[kFly];
+  float2 p[kFly];
+  auto load = [&](int i0) {
 #pragma unroll
     for (int k = 0; k < kFly; ++k) {
       const int i = i0 + k * step * kSub;
@@ -97,12 +97,24 @@ __device__ __forceinline__ void merge_part(const float* o, const float* ml, int 
         x[k] = *reinterpret_cast<const float4*>(o + static_cast<size_t>(i) * D + 4 * c4);
       }
     }
+  };
+  int i0 = first * kSub + sub;
+  load(i0);
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, ml[2 * i]);
+#pragma unroll
+  for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  const float base = M == -INFINITY ? 0.f : M;
+  while (true) {
 #pragma unroll
     for (int k = 0; k < kFly; ++k) {
       const float w = fast_exp2(p[k].x - base);  // 0 for a partial of nothing (-inf)
       l = fmaf(w, p[k].y, l);
       r.x = fmaf(w, x[k].x, r.x); r.y = fmaf(w, x[k].y, r.y); r.z = fmaf(w, x[k].z, r.z); r.w = fmaf(w, x[k].w, r.w);
     }
+    i0 += step * kSub * kFly;
+    if (!__any_sync(0xffffffffu, i0 < n)) break;
+    load(i0);
   }
   if (kSub == 2) {
     l += __shfl_xor_sync(0xffffffffu, l, 16);
@@ -113,21 +125,12 @@ __device__ __forceinline__ void merge_part(const float* o, const float* ml, int 
   }
 }
 
-// One warp: the largest of n partials' maxima (0 where there is none).
-__device__ __forceinline__ float merge_max(const float* ml, int n, int lane) {
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, ml[2 * i]);
-#pragma unroll
-  for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  return M == -INFINITY ? 0.f : M;
-}
-
 // One warp: the merge of n partials into a row of the output.
 template <int D>
 __device__ __forceinline__ void merge_row(const float* o, const float* ml, int n, __nv_bfloat16* out, int lane) {
   float l;
   float4 r;
-  merge_part<D>(o, ml, n, 0, 1, merge_max(ml, n, lane), lane, l, r);
+  merge_part<D>(o, ml, n, 0, 1, lane, l, r);
   if (lane < D / 4) store_out4(out + 4 * lane, r, l);
 }
 

@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
   const int s = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int gqa = a.Hq / a.H;
+  if (tid == 0) umma::prefetch_map(&map);
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int L = clamped_len(a, b);
@@ -105,7 +106,6 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
       pid = -1;
     }
     pid_s[i] = pid;
-    if (pid >= 0) scale_s[i] = __ldg(reinterpret_cast<const float2*>(a.scales) + static_cast<size_t>(pid) * a.H + h);
   }
   uint64_t* my_bars = bars + warp * kStages;
   const uint32_t my_ring = smem_u32(smem) + warp * kStages * kPage;
@@ -128,6 +128,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
   const bool issuer = umma::elect_one();
   if (issuer)
     for (int i = 0; i < min(n_my, kStages); ++i) issue(i);
+
+  // the scales, while the first pages are on their way
+  for (int i = tid; i < npg; i += kWarps * 32)
+    if (pid_s[i] >= 0)
+      scale_s[i] = __ldg(reinterpret_cast<const float2*>(a.scales) + static_cast<size_t>(pid_s[i]) * a.H + h);
 
   // Q: lane (g, t) holds query g, channels 16 ks + 4 t .. + 3 (k = 2t, 2t+1, 2t+8, 2t+9 of k-step ks)
   uint32_t qa[kKs][2];
@@ -159,6 +164,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
 #pragma unroll
   for (int j = 0; j < kNt; ++j) o[j] = make_float2(0.f, 0.f);
   float m_run = -INFINITY, l_run = 0.f;  // l: this lane's tokens
+  __syncthreads();  // scales
   bool aborted = false;
   int i = 0;
   for (; i < n_my; ++i) {
@@ -330,16 +336,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(SplitArgs s
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const size_t row = blockIdx.x;
   const int b = static_cast<int>(row / a.Hq);
-  grid_dep_wait();
+  // (the lengths come from before the split kernel, which waited for whoever wrote them)
   const int L = min(max(__ldg(a.seq_lens + b), 0), a.max_seq_len);
   const Visible vis = visible(L - 1, L - 1, a.sink, a.window);
   const int n = (vis.n + sa.pps - 1) / sa.pps;
+  grid_dep_wait();
   if (n <= 1) return;  // the split kernel wrote the output
   const float* o = sa.part_o + row * sa.ns * D;
   const float* ml = sa.part_ml + row * sa.ns * 2;
   float l;
   float4 r;
-  merge_part<D>(o, ml, n, warp, kMergeWarps, merge_max(ml, n, lane), lane, l, r);
+  merge_part<D>(o, ml, n, warp, kMergeWarps, lane, l, r);
   if (lane < D / 4) part[warp][lane] = r;
   if (lane == 0) sums[warp] = l;
   __syncthreads();

@@ -681,9 +681,10 @@ constexpr int kMergeRows = 4;
 template <int D, int TM>
 __global__ void __launch_bounds__(kMergeRows * 32) kv8_extend_merge_kernel(ExtArgs ea) {
   const AttnArgs& a = ea.a;
-  grid_dep_wait();
   constexpr int kParts = TM / kMergeRows;
+  // (what it reads comes from before the attention kernel, which waited for whoever wrote it)
   const Tile T = tile_of<TM>(a, blockIdx.z, blockIdx.x / kParts);
+  grid_dep_wait();
   if (!T.ok) return;
   const int n = (T.blocks + ea.bps - 1) / ea.bps;
   const int r = blockIdx.x % kParts * kMergeRows + (threadIdx.x >> 5);
