@@ -372,12 +372,24 @@ bool make_plan(const oscar_dims_t* d, int batch, int max_seq_len, int pps, int s
   if (d->num_kv_heads > 65535 || static_cast<long long>(batch) * d->num_q_heads > 0x7fffffffLL) return false;
   const long long pages = max_visible_pages(max_seq_len, sink, window, 1);
   if (pps == 0) {
+    // Splits that fill whole waves of the 3 CTAs an SM holds, of 16 to 128 pages (longer ones leave uneven lengths
+    // unbalanced): the cheapest of four wave counts, a wave taking its pages and as long as 16 more for start and end.
+    // Against splits = slots / units rounded up: 8 x 8192 36 -> 29 us, 32 x 4096 64 -> 56 us.
     const long long units = static_cast<long long>(batch > 0 ? batch : 1) * d->num_kv_heads;
-    const long long slots = 3LL * num_sms();
-    const long long splits = (slots + units - 1) / units;
-    long long want = (pages + splits - 1) / splits;
-    want = want < 4 * kWarps ? 4 * kWarps : want > 128 ? 128 : want;
-    pps = static_cast<int>(want);
+    const long long slots = 3LL * num_sms(), most = (pages + 4 * kWarps - 1) / (4 * kWarps);
+    const long long least = (pages + 127) / 128;
+    const long long waves = (least * units + slots - 1) / slots;
+    long long best = 0;
+    for (long long w = waves; w < waves + 4; ++w) {
+      const long long splits = w * slots / units < most ? w * slots / units : most;
+      if (splits < 1 || splits > 65535) continue;
+      const long long len = (pages + splits - 1) / splits, cost = w * (len + 16);
+      if (best == 0 || cost < best) {
+        best = cost;
+        pps = static_cast<int>(len);
+      }
+    }
+    if (pps < 4 * kWarps) pps = 4 * kWarps;
   }
   if (pps > kMaxPps) pps = kMaxPps;
   const long long ns = pages > 0 ? (pages + pps - 1) / pps : 1;
