@@ -306,6 +306,31 @@ def test_pages_far_into_a_large_pool():
     assert torch.equal(codes[ids[-1].item()], small.codes[small.table[0, -1].item()])
 
 
+@pytest.mark.parametrize("D,fmt", [(64, R.E4M3), (64, R.INT8), (128, R.E4M3), (128, R.INT8)])
+@pytest.mark.parametrize("gqa,most", [(1, 64), (1, 65), (7, 9), (7, 10), (8, 8), (8, 9), (3, 21), (3, 22)])
+@pytest.mark.parametrize("sink,window", [(0, 0), (5, 40), (70, 1), (0, 500)])
+def test_extend_around_64_rows_of_a_tile(D, fmt, gqa, most, sink, window):
+    lens = [1, 64, 65, 129, 128, 700, 1500, 0, 63]
+    rows = [min(n, r) for n, r in zip(lens, (1, most, most, most, 1, most, 2, 0, most))]
+    c = Cache(2, D, fmt, lens, seed=D + fmt + gqa + most + window)
+    seq = [b for b, r in enumerate(rows) for _ in range(r)]
+    pos = [lens[b] - r + i for b, r in enumerate(rows) for i in range(r)]
+    q = c.q(len(seq), 2 * gqa)
+    for pps in (0, 8):
+        c.check(c.extend(q, rows, sink, window, pps=pps), q, seq, pos, sink=sink, window=window)
+    assert ok.oscar_device_errors(reset=True) == 0
+
+
+@pytest.mark.parametrize("batch,length", [(8, 8192), (32, 4096), (3, 16384), (1, 16), (1, 17), (70, 300)])
+def test_decode_split_rule(batch, length):
+    lens = [length - 5 * b for b in range(batch)]
+    lens = [max(n, 1) for n in lens]
+    c = Cache(2, 64, R.INT8, lens, seed=batch)
+    q = c.q(batch, 4)
+    c.check_decode(c.decode(q), q)
+    c.check_decode(c.decode(q, 16, 900), q, sink=16, window=900)
+
+
 def test_nan_queries_stay_in_their_rows():
     c = Cache(2, 128, R.E4M3, [700, 90], seed=19)
     q = c.q(2, 8)
