@@ -118,7 +118,9 @@ class _LazyLib:
     def __getattr__(self, name):
         if _LazyLib._handle is None:
             _LazyLib._handle = _load()
-        return getattr(_LazyLib._handle, name)
+        fn = getattr(_LazyLib._handle, name)
+        self.__dict__[name] = fn  # found without this call from then on
+        return fn
 
 
 lib = _LazyLib()
