@@ -808,10 +808,22 @@ bool make_plan(const oscar_dims_t* d, int batch, int rows, int max_seq_len, int 
     long long units = static_cast<long long>(rows) * gqa / tm + batch;
     if (units > tiles * batch) units = tiles * batch;
     units *= d->num_kv_heads;
-    // CTAs per SM aimed at: short runs (bound by the pages' bytes) 3 -- with lengths of 1000 to 32768 and 8 sequences, 1: 160 us,
-    // 2: 139, 3: 114, 4: 128, 6: 135, 8: 149 -- and long runs 2.
-    const long long want = (p->mt == 1 ? 3LL : 2LL) * num_sms();
-    const long long splits = units > 0 && units < want ? want / units : 1;
+    long long splits = 1;
+    // The cheapest of the split counts that fill whole waves of one CTA per SM, a wave taking its blocks and as long as 5
+    // (short runs) or 12 more for its start and end; the 12 also stand for the merge and for causal tiles that end
+    // early (with 8, 4096 rows of 8192 positions take 445 us in two splits, 355 in one).  Against a fixed 3 (2) CTAs per SM:
+    // 8 rows of one or two sequences of 32768 tokens 4.4 -> 2.6 times their bytes' time, 512 rows of 8192 positions 89 -> 76 us.
+    const long long extra = p->mt == 1 ? 5 : 12;
+    long long best = 0;
+    for (long long w = 1; w <= 8; ++w) {
+      const long long n = w * num_sms() / (units > 0 ? units : 1);
+      if (n < 1) continue;
+      const long long cost = w * ((blocks + n - 1) / n + extra);
+      if (best == 0 || cost < best) {
+        best = cost;
+        splits = n;
+      }
+    }
     bps = (blocks + splits - 1) / splits;
     if (bps < 4) bps = 4;
   }
