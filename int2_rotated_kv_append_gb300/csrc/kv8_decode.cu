@@ -14,7 +14,7 @@
 //   O += f (P V)    f = 2^(m - running maximum) * the page's V scale, in fp32.
 // Bound by the bytes of the pages (2 D per token and KV head): 64 sequences of 1024 to 16384 tokens, 8 KV heads,
 // D = 128, 1.12 GB: 184 us with the merge, 6.1 TB/s, 90% of a plain copy's rate.  A page costs about 200
-// instructions a warp; one sequence of 32768 tokens (67 MB) takes 21 us, half of it the start of the
+// instructions a warp; one sequence of 32768 tokens (67 MB) takes 20 us, half of it the start of the
 // chain (length, page ids, first pages) and the merge.
 // Then the warps are merged, and a second kernel merges the splits where there are several.
 #include <math.h>
