@@ -3,6 +3,8 @@
 // 8 significant bits) and a change of scale exact but for what falls below the new step.
 #pragma once
 
+#include <math.h>
+
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -93,7 +95,7 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
   }
 }
 
-// The same, times a power of two f (both halves): one operation more for e4m3, none for int8.
+// The same, times a power of two f (both halves), f1152 = 1152 f: one operation more for e4m3, none for int8.
 template <int F>
 __device__ __forceinline__ void codes_to_f16_scaled(uint32_t w, __half2 f, __half2 f1152, uint32_t& lo, uint32_t& hi) {
   if constexpr (F == kE4M3) {
@@ -110,6 +112,11 @@ __device__ __forceinline__ void codes_to_f16_scaled(uint32_t w, __half2 f, __hal
     lo = *reinterpret_cast<const uint32_t*>(&x);
     hi = *reinterpret_cast<const uint32_t*>(&y);
   }
+}
+
+// log2 of a scale, a power of two; -infinity for 0.
+__device__ __forceinline__ float scale_log2_of(float s) {
+  return s > 0.f ? static_cast<float>(static_cast<int>(__float_as_uint(s) >> 23) - 127) : -INFINITY;
 }
 
 // Positions of a sequence that a row at position `row` sees: [0, sink_end) and [lo, row], as a list of

@@ -66,51 +66,75 @@ __device__ __forceinline__ int clamped_len(const AttnArgs& a, int b) {
   return L;
 }
 
-// Four channels of an output row: o / l, 0 where nothing was attended (a NaN of the query stays one).
-__device__ __forceinline__ void store_out4(__nv_bfloat16* out, float4 o, float l) {
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv), y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+// 2^e as the product of two floats, for |e| < 250 (below: as good as 0; NaN, of a row that is NaN or empty, as that).
+__device__ __forceinline__ void pow2_pair(float e, float& f, float& g) {
+  e = fmaxf(e, -250.f);
+  const float h = truncf(0.5f * e);
+  f = fast_exp2(h);
+  g = fast_exp2(e - h);
+}
+
+// Numerator and denominator of a row have a unit each: o counts 2^t (weights times V scales: t near the largest of
+// these products) and l counts 2^m (weights alone).  With one unit for both, values near either end of the scales' range
+// would leave fp32.  Two units t may be further apart than a float's exponents reach: o goes from one to another by a pair.
+
+// Four channels of an output row: o 2^t / (l 2^m) with e = t - m, 0 where nothing was attended (a NaN of the query stays one).
+__device__ __forceinline__ void store_out4(__nv_bfloat16* out, float4 o, float l, float e) {
+  float f, g;
+  pow2_pair(e, f, g);
+  const float inv = l == 0.f ? 0.f : f / l;
+  const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv * g, o.y * inv * g),
+                       y = __floats2bfloat162_rn(o.z * inv * g, o.w * inv * g);
   *reinterpret_cast<uint2*>(out) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
-// One warp: partials first, first + step, ... of n (o [n][D] unnormalised, ml [n][2] = maximum in log2
-// units, sum): l and four channels r of lane's c4 = lane % (D / 4), relative to the largest of all n maxima (0 where
-// there is none).  Eight partials are in flight at once, the first of them while the maximum is found.
+// One warp: partials first, first + step, ... of n (o [n][D] unnormalised, ml [n][4] = m, l, t, -; -infinity for the units of a
+// partial of nothing): l and four channels r of lane's c4 = lane % (D / 4), in units of the largest m and t of all n,
+// whose difference is e.  Eight partials are in flight at once, the first of them while the maxima are found.
 template <int D>
 __device__ __forceinline__ void merge_part(const float* o, const float* ml, int n, int first, int step, int lane,
-                                           float& l, float4& r) {
+                                           float& l, float4& r, float& e) {
   constexpr int kSub = 128 / D, kFly = 8;  // D = 64: two half warps take every second partial
   const int sub = lane / (D / 4), c4 = lane % (D / 4);
   l = 0.f;
   r = make_float4(0.f, 0.f, 0.f, 0.f);
-  float4 x[kFly];
-  float2 p[kFly];
+  float4 x[kFly], p[kFly];
   auto load = [&](int i0) {
 #pragma unroll
     for (int k = 0; k < kFly; ++k) {
       const int i = i0 + k * step * kSub;
-      p[k] = make_float2(-INFINITY, 0.f);
+      p[k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
       x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < n) {
-        p[k] = *reinterpret_cast<const float2*>(ml + 2 * i);
+        p[k] = *reinterpret_cast<const float4*>(ml + 4 * i);
         x[k] = *reinterpret_cast<const float4*>(o + static_cast<size_t>(i) * D + 4 * c4);
       }
     }
   };
   int i0 = first * kSub + sub;
   load(i0);
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, ml[2 * i]);
+  float M = -INFINITY, T = -INFINITY;
+  for (int i = lane; i < n; i += 32) {
+    const float4 v = *reinterpret_cast<const float4*>(ml + 4 * i);
+    M = fmaxf(M, v.x);
+    T = fmaxf(T, v.z);
+  }
 #pragma unroll
-  for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  const float base = M == -INFINITY ? 0.f : M;
+  for (int off = 16; off; off >>= 1) {
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    T = fmaxf(T, __shfl_xor_sync(0xffffffffu, T, off));
+  }
+  e = T - M;
+  const float base = M == -INFINITY ? 0.f : M, base_t = T == -INFINITY ? 0.f : T;
   while (true) {
 #pragma unroll
     for (int k = 0; k < kFly; ++k) {
-      const float w = fast_exp2(p[k].x - base);  // 0 for a partial of nothing (-inf)
-      l = fmaf(w, p[k].y, l);
-      r.x = fmaf(w, x[k].x, r.x); r.y = fmaf(w, x[k].y, r.y); r.z = fmaf(w, x[k].z, r.z); r.w = fmaf(w, x[k].w, r.w);
+      l = fmaf(fast_exp2(p[k].x - base), p[k].y, l);  // (a factor of 0 for a partial of nothing)
+      float f, g;
+      pow2_pair(p[k].z - base_t, f, g);
+      r.x = fmaf(f, x[k].x * g, r.x); r.y = fmaf(f, x[k].y * g, r.y);
+      r.z = fmaf(f, x[k].z * g, r.z); r.w = fmaf(f, x[k].w * g, r.w);
     }
     i0 += step * kSub * kFly;
     if (!__any_sync(0xffffffffu, i0 < n)) break;
@@ -128,10 +152,10 @@ __device__ __forceinline__ void merge_part(const float* o, const float* ml, int 
 // One warp: the merge of n partials into a row of the output.
 template <int D>
 __device__ __forceinline__ void merge_row(const float* o, const float* ml, int n, __nv_bfloat16* out, int lane) {
-  float l;
+  float l, e;
   float4 r;
-  merge_part<D>(o, ml, n, 0, 1, lane, l, r);
-  if (lane < D / 4) store_out4(out + 4 * lane, r, l);
+  merge_part<D>(o, ml, n, 0, 1, lane, l, r, e);
+  if (lane < D / 4) store_out4(out + 4 * lane, r, l, e);
 }
 
 }  // namespace kv8

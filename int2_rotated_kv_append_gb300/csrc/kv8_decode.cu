@@ -42,7 +42,7 @@ struct Geo {
 struct SplitArgs {
   AttnArgs a;
   float* part_o;   // [batch][Hq][ns][D]
-  float* part_ml;  // [batch][Hq][ns][2]
+  float* part_ml;  // [batch][Hq][ns][4]
   int ns, pps;
 };
 
@@ -317,11 +317,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
     }
     const size_t row = static_cast<size_t>(b) * a.Hq + h * gqa + qi;
     if (single) {
-      store_out4(a.out + row * D + 4 * c4, r, l);
+      store_out4(a.out + row * D + 4 * c4, r, l, 0.f);
     } else {
       const size_t part = row * sa.ns + s;
       *reinterpret_cast<float4*>(sa.part_o + part * D + 4 * c4) = r;
-      if (c4 == 0) *reinterpret_cast<float2*>(sa.part_ml + part * 2) = make_float2(M, l);
+      if (c4 == 0) *reinterpret_cast<float4*>(sa.part_ml + part * 4) = make_float4(M, l, M, 0.f);
     }
   }
 }
@@ -343,10 +343,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(SplitArgs s
   grid_dep_wait();
   if (n <= 1) return;  // the split kernel wrote the output
   const float* o = sa.part_o + row * sa.ns * D;
-  const float* ml = sa.part_ml + row * sa.ns * 2;
-  float l;
+  const float* ml = sa.part_ml + row * sa.ns * 4;
+  float l, e;
   float4 r;
-  merge_part<D>(o, ml, n, warp, kMergeWarps, lane, l, r);
+  merge_part<D>(o, ml, n, warp, kMergeWarps, lane, l, r, e);
   if (lane < D / 4) part[warp][lane] = r;
   if (lane == 0) sums[warp] = l;
   __syncthreads();
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(SplitArgs s
       l += sums[w];
       r.x += x.x; r.y += x.y; r.z += x.z; r.w += x.w;
     }
-    store_out4(a.out + row * D + 4 * threadIdx.x, r, l);
+    store_out4(a.out + row * D + 4 * threadIdx.x, r, l, e);
   }
 }
 
@@ -398,7 +398,7 @@ bool make_plan(const oscar_dims_t* d, int batch, int max_seq_len, int pps, int s
   p->pps = pps;
   const size_t parts = ns > 1 ? static_cast<size_t>(batch) * d->num_q_heads * ns : 0;
   p->off_ml = align_up(parts * d->head_dim * sizeof(float), 256);
-  p->total = p->off_ml + align_up(parts * 2 * sizeof(float), 256) + 256;
+  p->total = p->off_ml + align_up(parts * 4 * sizeof(float), 256) + 256;
   return true;
 }
 

@@ -18,12 +18,18 @@
 // it in registers, so that the next logits of either tile are formed while both compute weights; a weight
 // buffer (64) and an accumulator (D) per row tile.  With MT = 1 two logit buffers alternate, and Q is the products'
 // left side from TMEM, so that at D = 128 its place in shared memory becomes a third stage of codes.
-// Scales stay out of the operands.  Q is scaled per row by a power of two to below 2, where fp16 holds it to 2^-25
-// of the row's largest element; a page's K scale multiplies its 16 logits.  V codes carry the ratio of their
-// page's scale to the block's largest, vmax (a power of two, exact down to 2^-24), and the weights carry
-// vmax / vref, vref the largest scale so far.  Weights are p 2^3 vmax / vref, rounded to fp16 (11 bits: a tenth of
-// the output's own rounding), where p = 2^(s - m) <= 2^12 as the running maximum m is only moved when a logit
-// passes it by 12.  O is rescaled in TMEM when m or vref moves.  Sums are fp32 over the unrounded weights.
+// Q is scaled per row by a power of two to below 2, where fp16 holds it to 2^-25 of the row's largest element; a page's K
+// scale multiplies its 16 logits.  V scales 2^v go into the weights: the operand is 2^(s + v - t + 3) where t, the row's own,
+// is at least the largest s + v that the row sees less 12, by which it may be passed before it moves; the sum has
+// 2^(s - m), m likewise for s alone.  What the mask hides from a row has no part in its m and t (but that a page has one v).
+// m and t are whole numbers: every factor between units is exact.  O is rescaled in TMEM when t moves.  Sums are fp32
+// over the unrounded weights.
+// As long as the largest V scale so far is at most 2^kTame times a block's smallest, weights are fp16 (11 bits: a tenth of the output's
+// own rounding) with the block's largest v, and the codes carry the ratio of their page's scale to it (exact).  Then,
+// whatever other tokens of its pages make of a row's t, a weight's smallest step is 2^-22 of the row's largest.  In other
+// blocks ("wild": an infinite V element that was saturated, say) each page has its own v in the weights and the operands are
+// bf16, weights (8 bits) and codes (exact) alike, with fp32's range of exponents: there t may stay kWildUp lower, so
+// that a page whose scale comes from a token hidden from the row takes no bits from the row's other pages.
 //
 // Measured (GB300, 2070 MHz): 8192 rows over 16384 positions, 32 query heads, 8 KV heads, D = 128, e4m3: 1.20 ms,
 // 1370 TFLOP/s, 71% of a cuBLAS bf16 product's rate.  A block takes 3300 clocks where the products alone would
@@ -33,6 +39,8 @@
 // 3.3 TB/s (97 us with a block's 128 tokens to one thread and two stages): a block takes about 1700 clocks where
 // the codes would arrive in 1400, a CTA 5000 before its first block, and uneven lengths leave the last CTAs alone.
 #include <math.h>
+
+#include <type_traits>
 
 #include "kv8_attn.cuh"
 #include "umma.cuh"
@@ -51,6 +59,11 @@ static_assert(kInfo % 2 == 0, "two warps take turns");
 // rescale took 550 of 3400 clocks)
 constexpr float kLazy = 12.f;
 constexpr int kBoost = 3;         // weights are stored times 2^kBoost: 2^(kLazy + kBoost) < 65504
+constexpr float kTame = 4.f;      // log2
+constexpr float kWildUp = 76.f;   // 2^(kWildUp + kLazy + kBoost) times a code (2^9) times 2^27 tokens is within fp32
+// Bounds of lb (below) for blocks that are not wild: under kLbLo there are only scales of 0, above kLbHi logits more than
+// 2^100 below the largest
+constexpr float kLbLo = -100.f, kLbHi = 126.f;
 constexpr int kQkWarp = 12, kFetchK = 13, kPvWarp = 14, kFetchV = 15;
 // Registers a thread: 512 x 128 at launch, divided among the warpgroups by setmaxnreg
 constexpr int kRegsLaunch = 128;
@@ -65,13 +78,14 @@ struct Regs {
 struct alignas(16) BlockInfo {
   float k_scale[kBlkPages];  // 1 where there is no page
   int pos[kBlkPages];        // first position; kNoPage: none
-  __half v_ratio[kBlkPages];  // a page's V scale over vmax (below 2^-24: 0)
-  float vmax;                // largest V scale
+  __half v_ratio[kBlkPages];  // a page's V scale over the largest
+  __half v_log2[kBlkPages];   // log2 of the V scale; -infinity: 0, or no page
+  float v_top;                // the largest of them
   uint32_t flags;
 };
 constexpr int kNoPage = 0x7fffffff - kPageSize;
-// flags: every row of row tile 0 / 1 sees the whole block; some row is behind the last token
-constexpr uint32_t kFull0 = 1, kTail = 4;
+// flags: every row of row tile 0 / 1 sees the whole block; some row is behind the last token; V scales far apart
+constexpr uint32_t kFull0 = 1, kTail = 4, kWild = 8;
 
 template <int D, int MT>
 struct Geo {
@@ -95,12 +109,13 @@ struct Geo {
   static constexpr uint32_t kQs = kScale + kInfo * sizeof(BlockInfo);
   static constexpr uint32_t kMisc = kQs + MT * 128 * 4;
   static constexpr size_t kSmem = 1024 + kMisc + 16;
+  static_assert(kSmem <= 232448, "what a CTA may have");
 };
 
 struct ExtArgs {
   AttnArgs a;
   float* part_o;   // [rows x Hq][ns][D]
-  float* part_ml;  // [rows x Hq][ns][2]
+  float* part_ml;  // [rows x Hq][ns][4]
   int ns, bps, tiles;
 };
 
@@ -156,6 +171,16 @@ __device__ __forceinline__ uint32_t half2_bits(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+__device__ __forceinline__ uint32_t bfloat2_bits(float x, float y) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// 2^-x for a whole number x, |x| <= 126: x is in the low bits of x + 1.5 2^23.
+__device__ __forceinline__ float pow2_neg(float x) {
+  return __uint_as_float(0x3f800000u - (__float_as_uint(x + 12582912.f) << 23));
+}
+
 // The lowest n of 16 bits (n < 0: none).
 __device__ __forceinline__ uint32_t low_bits(int n) { return (1u << min(max(n, 0), 16)) - 1u; }
 
@@ -195,7 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
   // (operand barriers: 2 x side + buffer)
   BlockInfo* infos = reinterpret_cast<BlockInfo*>(sm + G::kScale);
   float* q_scale = reinterpret_cast<float*>(sm + G::kQs);
-  uint32_t* misc = reinterpret_cast<uint32_t*>(sm + G::kMisc);  // TMEM base
+  // TMEM base; whether the codes in each V operand are bf16 (written and read as the operand itself)
+  volatile uint32_t* misc = reinterpret_cast<uint32_t*>(sm + G::kMisc);
   const int active = (T.rows + 127) / 128;
   if (tid == 0) {
     for (int i = 0; i < G::kRing; ++i) {
@@ -223,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
   __syncthreads();
   const int wg = warp >> 2;
   const bool fetches = warp == kFetchK || warp == kFetchV;  // these start at once; the others get Q and TMEM ready
-  if (warp == kQkWarp) umma::tmem_alloc(smem_u32(misc), 512);
+  if (warp == kQkWarp) umma::tmem_alloc(sb + G::kMisc, 512);
   // Q as fp16, K-major with the 128-byte swizzle: a lane takes 8 channels of a row, and every load is in flight at once
   if (wg < 3) {
     constexpr int kLanes = D / 8, kAtOnce = 12 * 32 / kLanes;  // lanes of a row; rows of one round of the 12 warps
@@ -318,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
         umma::tmem_st32(p_tmem[0] + t_lane + (part ^ 1) * (kCols / 2), z);
         umma::tmem_st_wait();
       }
-      float m = -INFINITY, l = 0.f, vref = 0.f;
+      float m = -INFINITY, l = 0.f, mt = -INFINITY;
       bool ok = true;
       for (int j = 0; j < cnt; ++j) {
         const int sbuf = MT == 2 ? wg : j & 1;  // barrier and buffer of the logits
@@ -330,105 +356,156 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           break;
         }
         umma::fence_after_sync();
+        const BlockInfo& bi = infos[info];
+        const uint32_t flags = bi.flags;
         uint32_t v[kCols / 32][32];
 #pragma unroll
         for (int c = 0; c < kCols / 32; ++c) umma::tmem_ld32(s_tmem[sbuf] + t_lane + part * kCols + 32 * c, v[c]);
         umma::tmem_ld_wait();
-        umma::fence_before_sync();
-        mbar_arrive(bar(kSFree + sbuf));
-        const BlockInfo& bi = infos[info];
-        const float vmax = bi.vmax;
-        float ks[kPages];
-#pragma unroll
-        for (int c = 0; c < kPages; c += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(bi.k_scale + part * kPages + c);
-          const float k4[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) ks[c + e] = fmaxf(k4[e] * qs, 1.2e-38f);  // (never 0: -inf stays -inf)
-        }
-        if ((bi.flags & (kFull0 << wg)) == 0) {
-#pragma unroll
-          for (int pg = 0; pg < kPages; ++pg) {
-            // bit c: the row sees position pp + c
-            const int pp = bi.pos[part * kPages + pg];
-            const uint32_t see = low_bits(pos - pp + 1) & (~low_bits(after - pp + 1) | low_bits(a.sink - pp));
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-              if ((see & (1u << c)) == 0) v[pg >> 1][(pg & 1) * 16 + c] = 0xff800000u;
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kInfoFree + info));
-        float mx = -INFINITY;
-#pragma unroll
-        for (int pg = 0; pg < kPages; ++pg) {
-          const uint32_t* x = &v[pg >> 1][(pg & 1) * 16];
-          float y = __uint_as_float(x[0]);
-#pragma unroll
-          for (int c = 1; c + 1 < 16; c += 2) y = fmax3(y, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-          y = fmaxf(y, __uint_as_float(x[15]));
-          mx = fmaxf(mx, y * ks[pg]);
-        }
-        // The product before is over: its weights' columns and O are free.  (Every phase of this barrier is waited
-        // for in its turn: a parity says nothing two phases ahead.)
-        if (j > 0) {
-          ok = mbar_wait_bounded(bar(kPvDone + (MT == 2 ? wg : 0)), (j - 1) & 1);
-          umma::fence_after_sync();
-        }
-        const bool move = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
-        const bool v_move = vmax > vref;
-        if (__any_sync(0xffffffffu, move) || v_move) {
-          const float m_new = move ? mx : m;
-          const float am = move ? (m == -INFINITY ? 0.f : fast_exp2(m - m_new)) : 1.f;
-          l *= am;
-          m = m_new;
-          float alpha = am;
-          if (v_move) {
-            alpha *= vref / vmax;
-            vref = vmax;
-          }
+        // bit c: the row sees token c of the part's page pg
+        auto seen = [&](int pg) {
+          const int pp = bi.pos[part * kPages + pg];
+          return low_bits(pos - pp + 1) & (~low_bits(after - pp + 1) | low_bits(a.sink - pp));
+        };
+        auto k_scale = [&](float k) { return fmaxf(k * qs, 1.2e-38f); };  // (never 0: -inf stays -inf)
+        // The largest logit and product of the block, once seen: m, t and what they count move where they have to.
+        auto settle = [&](float mx, float tx) {
+          // The product before is over: its weights' columns and O are free.  (Every phase of this barrier is waited
+          // for in its turn: a parity says nothing two phases ahead.)
           if (j > 0) {
+            ok = mbar_wait_bounded(bar(kPvDone + (MT == 2 ? wg : 0)), (j - 1) & 1);
+            umma::fence_after_sync();
+          }
+          const bool move = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
+          const bool t_move = tx > mt + kLazy || (mt == -INFINITY && tx > -INFINITY);
+          if (move) {
+            const float m_new = ceilf(mx);
+            l *= fast_exp2(m - m_new);
+            m = m_new;
+          }
+          if (__any_sync(0xffffffffu, t_move)) {
+            const float t_new = t_move ? ceilf(tx) : mt;
+            float gap = j > 0 ? fmaxf(mt - t_new, -240.f) : 0.f;  // (below: 0 in the end)
+            mt = t_new;
+            while (__any_sync(0xffffffffu, gap < 0.f)) {  // by up to 2^-120 at a time
+              const float alpha = fast_exp2(fmaxf(gap, -120.f));
+              gap = fminf(gap + 120.f, 0.f);
 #pragma unroll 1  // (rare: kept small for the instruction cache)
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t o[16];
-              umma::tmem_ld16(o_tmem[wg] + t_lane + 16 * c, o);
-              umma::tmem_ld_wait();
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                umma::tmem_ld16(o_tmem[wg] + t_lane + 16 * c, o);
+                umma::tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              umma::tmem_st16(o_tmem[wg] + t_lane + 16 * c, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                umma::tmem_st16(o_tmem[wg] + t_lane + 16 * c, o);
+              }
+              umma::tmem_st_wait();
             }
           }
-        }
-        // weights: 2^(s - m + lb), lb = kBoost + log2(vmax / vref)
-        const int lb = vref > 0.f ? max(kBoost + static_cast<int>(__float_as_uint(vmax) >> 23) -
-                                            static_cast<int>(__float_as_uint(vref) >> 23), -110)
-                                  : 0;
-        const float off = static_cast<float>(lb) - (m == -INFINITY ? 0.f : m);
-        const float2 off2 = make_float2(off, off);
-        float2 sum[4];  // four chains of additions
+        };
+        if ((flags & kWild) == 0) {
+          umma::fence_before_sync();
+          mbar_arrive(bar(kSFree + sbuf));
+          const float v_top = bi.v_top;
+          float ks[kPages];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) sum[c] = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int half = 0; half < kCols / 64; ++half) {
-          uint32_t p[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const int col = half * 64 + 2 * c;
-            const float k = ks[col >> 4];
-            const float2 e = f2fma(make_float2(__uint_as_float(v[col >> 5][col & 31]),
-                                               __uint_as_float(v[col >> 5][(col & 31) + 1])),
-                                   make_float2(k, k), off2);
-            const float2 w = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-            sum[c & 3] = f2add(sum[c & 3], w);
-            p[c] = half2_bits(w.x, w.y);
+          for (int c = 0; c < kPages; c += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(bi.k_scale + part * kPages + c);
+            ks[c] = k_scale(x.x); ks[c + 1] = k_scale(x.y); ks[c + 2] = k_scale(x.z); ks[c + 3] = k_scale(x.w);
           }
-          umma::tmem_st32(p_tmem[wg] + t_lane + part * (kCols / 2) + 32 * half, p);
+          if ((flags & (kFull0 << wg)) == 0) {
+#pragma unroll
+            for (int pg = 0; pg < kPages; ++pg) {
+              const uint32_t see = seen(pg);
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                if ((see & (1u << c)) == 0) v[pg >> 1][(pg & 1) * 16 + c] = 0xff800000u;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kInfoFree + info));
+          float mx = -INFINITY;
+#pragma unroll
+          for (int pg = 0; pg < kPages; ++pg) {
+            const uint32_t* x = &v[pg >> 1][(pg & 1) * 16];
+            float y = __uint_as_float(x[0]);
+#pragma unroll
+            for (int c = 1; c + 1 < 16; c += 2) y = fmax3(y, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+            y = fmaxf(y, __uint_as_float(x[15]));
+            mx = fmaxf(mx, y * ks[pg]);
+          }
+          settle(mx, mx + v_top);
+          // weights 2^(s - m + lb), lb = v - t + m + kBoost; the sum takes the 2^lb out again
+          const float lb = fminf(fmaxf(v_top + (mt == -INFINITY ? 0.f : kBoost - mt + m), kLbLo), kLbHi);
+          const float off = lb - (m == -INFINITY ? 0.f : m);
+          const float2 off2 = make_float2(off, off);
+          float2 sum[4];  // four chains of additions
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sum[c] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int half = 0; half < kCols / 64; ++half) {
+            uint32_t p[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const int col = half * 64 + 2 * c;
+              const float k = ks[col >> 4];
+              const float2 e = f2fma(make_float2(__uint_as_float(v[col >> 5][col & 31]),
+                                                 __uint_as_float(v[col >> 5][(col & 31) + 1])),
+                                     make_float2(k, k), off2);
+              const float2 w = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+              sum[c & 3] = f2add(sum[c & 3], w);
+              p[c] = half2_bits(w.x, w.y);
+            }
+            umma::tmem_st32(p_tmem[wg] + t_lane + part * (kCols / 2) + 32 * half, p);
+          }
+          umma::tmem_st_wait();
+          umma::fence_before_sync();
+          mbar_arrive(bar(kPFull + (MT == 2 ? wg : 0)));
+          sum[0] = f2add(f2add(sum[0], sum[1]), f2add(sum[2], sum[3]));
+          l = fmaf(sum[0].x + sum[0].y, pow2_neg(lb), l);
+        } else {
+          // Rare: a page at a time, once for the largest and once for the weights (little code, for the instruction cache).
+          float mx = -INFINITY, tx = -INFINITY;
+#pragma unroll 1
+          for (int pg = 0; pg < 2 * kPages; ++pg) {
+            const int at = pg % kPages;
+            if (pg == kPages) settle(mx, tx - kWildUp);
+            uint32_t x[16];
+            __syncwarp();
+            umma::tmem_ld16(s_tmem[sbuf] + t_lane + part * kCols + 16 * at, x);
+            umma::tmem_ld_wait();
+            const uint32_t see = seen(at);
+            const float k = k_scale(bi.k_scale[part * kPages + at]), v = __half2float(bi.v_log2[part * kPages + at]);
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              if ((see & (1u << c)) == 0) x[c] = 0xff800000u;
+            if (pg < kPages) {
+              float y = -INFINITY;
+#pragma unroll
+              for (int c = 0; c < 16; ++c) y = fmaxf(y, __uint_as_float(x[c]));
+              mx = fmaxf(mx, y * k);
+              tx = fmaxf(tx, fmaf(y, k, v));
+            } else {
+              // (for the products and for the sum: their units may be further apart than a float's exponents reach)
+              const float off = kBoost + v - (mt == -INFINITY ? 0.f : mt), off_l = m == -INFINITY ? 0.f : -m;
+              float sum = 0.f;
+              uint32_t p[8];
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const float x0 = __uint_as_float(x[2 * c]), x1 = __uint_as_float(x[2 * c + 1]);
+                sum += fast_exp2(fmaf(x0, k, off_l)) + fast_exp2(fmaf(x1, k, off_l));
+                p[c] = bfloat2_bits(fast_exp2(fmaf(x0, k, off)), fast_exp2(fmaf(x1, k, off)));
+              }
+              l += sum;
+              umma::tmem_st8(p_tmem[wg] + t_lane + part * (kCols / 2) + 8 * at, p);
+            }
+          }
+          umma::tmem_st_wait();
+          umma::fence_before_sync();
+          mbar_arrive(bar(kSFree + sbuf));
+          mbar_arrive(bar(kPFull + (MT == 2 ? wg : 0)));
+          if (lane == 0) mbar_arrive(bar(kInfoFree + info));  // (the stores' wait was the whole warp's)
         }
-        umma::tmem_st_wait();
-        umma::fence_before_sync();
-        mbar_arrive(bar(kPFull + (MT == 2 ? wg : 0)));
-        sum[0] = f2add(f2add(sum[0], sum[1]), f2add(sum[2], sum[3]));
-        l = fmaf(sum[0].x + sum[0].y, pow2i(-lb), l);
       }
       if (ok) ok = mbar_wait_bounded(bar(kPvDone + (MT == 2 ? wg : 0)), (cnt - 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
@@ -437,9 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       const bool single = T.blocks <= ea.bps;
       const bool store = r < T.rows;
       const size_t row = store ? out_row(r) : 0;
-      float unit = ok ? vref * (1.f / (1 << kBoost)) : 0.f;
+      float t = mt - kBoost;  // log2 of what the accumulators count
       if (!ok) l = 0.f;
-      float other = 0.f;  // what the other part's accumulators count; which of the parts saw nothing
+      float u0 = 1.f, u1 = 1.f, v0 = 0.f, v1 = 0.f;  // the parts' accumulators to the merged ones' unit; which saw nothing
       bool none0 = false, none1 = false;
       const float* theirs = nullptr;
       if (PARTS == 2) {
@@ -458,20 +535,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           for (int e = 0; e < 16; e += 4)
             *reinterpret_cast<uint4*>(mine + 16 * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
-        *reinterpret_cast<float4*>(mine + D / 2) = make_float4(l == 0.f ? -INFINITY : m, l, unit, 0.f);
+        none0 = l == 0.f;
+        if (none0) m = t = -INFINITY;
+        *reinterpret_cast<float4*>(mine + D / 2) = make_float4(m, l, t, 0.f);
         asm volatile("bar.sync 2, 128;" ::: "memory");
         const float4 x = *reinterpret_cast<const float4*>(theirs + D / 2);
-        const float m0 = l == 0.f ? -INFINITY : m, top = fmaxf(m0, x.x), base = top == -INFINITY ? 0.f : top;
-        const float a0 = fast_exp2(m0 - base), a1 = fast_exp2(x.x - base);
-        none0 = l == 0.f;
         none1 = x.y == 0.f;
-        l = (none0 ? 0.f : l * a0) + (none1 ? 0.f : x.y * a1);
-        unit = none0 ? 0.f : unit * a0;
-        other = none1 ? 0.f : x.z * a1;
+        const float top = fmaxf(m, x.x), base = top == -INFINITY ? 0.f : top;
+        const float top_t = fmaxf(t, x.z), base_t = top_t == -INFINITY ? 0.f : top_t;
+        l = (none0 ? 0.f : l * fast_exp2(m - base)) + (none1 ? 0.f : x.y * fast_exp2(x.x - base));
+        pow2_pair(t - base_t, u0, u1);
+        pow2_pair(x.z - base_t, v0, v1);
         m = top;
+        t = top_t;
       }
-      const float inv = l == 0.f ? 0.f : PARTS == 2 ? 1.f / l : unit / l;
-      const float scale = PARTS == 2 ? 1.f : unit;
+      float f, g;
+      pow2_pair(t - m, f, g);
+      const float inv = l == 0.f ? 0.f : f / l;
 #pragma unroll 2
       for (int c = part * (D / 32); c < (PARTS == 2 ? (part + 1) * (D / 32) : D / 16); ++c) {
         uint32_t o[16];
@@ -481,16 +561,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
         if (PARTS == 2) {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            o[e] = __float_as_uint((none0 ? 0.f : __uint_as_float(o[e]) * unit) +
-                                   (none1 ? 0.f : theirs[16 * (c - part * (D / 32)) + e] * other));
+            o[e] = __float_as_uint((none0 ? 0.f : __uint_as_float(o[e]) * u0 * u1) +
+                                   (none1 ? 0.f : theirs[16 * (c - part * (D / 32)) + e] * v0 * v1));
         }
         if (store && single) {
           uint32_t y[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const __nv_bfloat162 z = __floats2bfloat162_rn(l == 0.f ? 0.f : __uint_as_float(o[2 * e]) * inv,
-                                                           l == 0.f ? 0.f : __uint_as_float(o[2 * e + 1]) * inv);
-            y[e] = *reinterpret_cast<const uint32_t*>(&z);
+            y[e] = l == 0.f ? 0u : bfloat2_bits(__uint_as_float(o[2 * e]) * inv * g, __uint_as_float(o[2 * e + 1]) * inv * g);
           }
           uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + 16 * c);
           dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
@@ -500,13 +578,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             dst[e] = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                              : make_float4(__uint_as_float(o[4 * e]) * scale, __uint_as_float(o[4 * e + 1]) * scale,
-                                            __uint_as_float(o[4 * e + 2]) * scale, __uint_as_float(o[4 * e + 3]) * scale);
+                              : make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                            __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
         }
       }
       if (store && !single && part == 0)
-        *reinterpret_cast<float2*>(ea.part_ml + (row * ea.ns + split) * 2) =
-            make_float2(l == 0.f ? -INFINITY : m, l);
+        *reinterpret_cast<float4*>(ea.part_ml + (row * ea.ns + split) * 4) =
+            l == 0.f ? make_float4(-INFINITY, 0.f, -INFINITY, 0.f) : make_float4(m, l, t, 0.f);
     }
   } else if (wg < 3) {
     // ---- codes -> fp16 operands: K and V in turn (MT = 2), V or K (MT = 1: warpgroups 1 and 2) ------------
@@ -563,6 +641,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
         st_shared_v4(dst0 + to + i * (kStep * 128), y[0], y[1], y[2], y[3]);
         st_shared_v4(dst1 + to + i * (kStep * 128), y[4], y[5], y[6], y[7]);
       }
+      if (side == 1) {
+        const uint32_t wild = bi.flags & kWild;
+        if (wild) {  // rare: this thread's values once more, as bf16 (exact)
+#pragma unroll 1
+          for (int i = 0; i < 2 * kUnits; ++i) {
+            const uint32_t at = (i & 1 ? dst1 : dst0) + to + (i >> 1) * (kStep * 128);
+            uint32_t y[4];
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                         : "r"(at)
+                         : "memory");
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&y[e]));
+              y[e] = bfloat2_bits(x.x, x.y);
+            }
+            st_shared_v4(at, y[0], y[1], y[2], y[3]);
+          }
+        }
+        if (pt == 0) misc[1 + (j & 1)] = wild;
+      }
       fence_async();
       mbar_arrive(bar(kOpFull + op));
       if (side == 1) {
@@ -602,6 +701,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       const bool issuer = umma::elect_one();
       int pid = -1, pid1 = checked(look_up(0)), pid2 = look_up(1);
       float2 sc = make_float2(1.f, 0.f), sc1 = scales(pid1);
+      float v_top = -INFINITY;  // log2 of the largest V scale of all blocks looked at
+      float v_own = -INFINITY, v_blk = -INFINITY;  // of this lane's page and block
+      bool wild = false;
       bool ok = true;
       int issued = 0;
       for (int j = 0; j < cnt && ok; ++j) {
@@ -612,6 +714,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           pid1 = checked(pid2);
           sc1 = scales(pid1);
           pid2 = look_up((j >> 2) + 2);
+          // of the lane's block (8 lanes): largest so far and smallest V scale
+          v_own = scale_log2_of(sc.y);
+          float hi = v_own, lo = v_own == -INFINITY ? INFINITY : v_own;
+#pragma unroll
+          for (int o = 1; o < kBlkPages; o <<= 1) {
+            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+          }
+          v_blk = hi;
+#pragma unroll
+          for (int o = kBlkPages; o < 32; o <<= 1) {
+            const float before = __shfl_up_sync(0xffffffffu, hi, o);
+            if (lane >= o) hi = fmaxf(hi, before);
+          }
+          hi = fmaxf(hi, v_top);
+          v_top = __shfl_sync(0xffffffffu, hi, 31);
+          wild = lo < hi - kTame;
         }
         const bool mine = (lane >> 3) == (j & 3);  // this lane holds a page of block j
         const bool copies = mine && pid >= 0 && (!G::kWhole || ((lane >> 2) & 1) == side);
@@ -649,10 +768,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
             break;
           }
           const int pos = pid < 0 ? kNoPage : T.vis.page((blk0 + j) * kBlkPages + (lane & 7)) * kPageSize;
-          float vmax = sc.y;
-#pragma unroll
-          for (int o = 1; o < kBlkPages; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
-          const float ratio = pid >= 0 && vmax > 0.f ? sc.y / vmax : 1.f;  // exact: powers of two
           auto any = [&](bool x) { return __any_sync(0xffffffffu, mine & x); };
           uint32_t flags = 0;
 #pragma unroll
@@ -660,13 +775,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
             if (!any((pos > p_lo[t] - (kPageSize - 1)) | ((pos <= p_after[t]) & (pos > a.sink - kPageSize))))
               flags |= kFull0 << t;
           if (any((pid < 0) | (pos > T.L - kPageSize))) flags |= kTail;
+          if (any(wild)) flags |= kWild;
           if (mine) {
             BlockInfo& bi = infos[info];
             bi.k_scale[lane & 7] = sc.x;
-            bi.v_ratio[lane & 7] = __float2half_rn(ratio);
+            // (exact; for a wild block's bf16 the codes as they are)
+            bi.v_ratio[lane & 7] = __float2half_rn(wild ? 1.f : fast_exp2(v_own == -INFINITY ? v_own : v_own - v_blk));
+            bi.v_log2[lane & 7] = __float2half_rn(v_own);
             bi.pos[lane & 7] = pos;
             if ((lane & 7) == 0) {
-              bi.vmax = vmax;
+              bi.v_top = v_blk;
               bi.flags = flags;
             }
           }
@@ -687,7 +805,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       // The whole warp goes through this code and one elected lane issues: with uniform control flow the
       // operands stay in uniform registers (65 clocks a 128 x 128 x 16 product with A in TMEM, the pipe's rate, where a branch
       // on the lane number took 112).
-      constexpr uint32_t kIdQk = umma::idesc_f16_f32(128, kTok, false), kIdPv = umma::idesc_f16_f32_b_mn(128, D);
+      constexpr uint32_t kIdQk = umma::idesc_f16_f32(128, kTok, false), kIdPv = umma::idesc_f16_f32_b_mn(128, D),
+                         kIdPvBf16 = umma::idesc_bf16_f32_b_mn(128, D);
       const bool issuer = umma::elect_one();
       bool ok = true;
       auto wait = [&](int i, int parity) { ok = ok && mbar_wait_bounded(bar(i), parity & 1); };
@@ -732,6 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           const int buf = j & 1;
           const uint64_t dv = umma::desc_mn_sw128(sb + G::kV + buf * G::kOp, kTok * 128);
           wait(kOpFull + 2 + buf, j >> 1);
+          const uint32_t id = __shfl_sync(0xffffffffu, misc[1 + buf], 0) ? kIdPvBf16 : kIdPv;
           for (int t = 0; t < nt; ++t) {
             wait(kPFull + t, j);
             if (!__all_sync(0xffffffffu, ok)) {
@@ -742,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
             if (issuer) {
 #pragma unroll
               for (int ks = 0; ks < kTok / 16; ++ks)
-                umma::mma_f16_ts(o_tmem[t], p_tmem[t] + ks * 8, dv + ks * (2048 >> 4), kIdPv, j > 0 || ks > 0);
+                umma::mma_f16_ts(o_tmem[t], p_tmem[t] + ks * 8, dv + ks * (2048 >> 4), id, j > 0 || ks > 0);
               umma::commit(bar(kPvDone + t));
               if (t == nt - 1) umma::commit(bar(kOpEmpty + 2 + buf));
             }
@@ -777,7 +897,7 @@ __global__ void __launch_bounds__(kMergeRows * 32) kv8_extend_merge_kernel(ExtAr
   if (n <= 1 || r >= T.rows) return;  // (one split: written by the attention kernel)
   const int gqa = a.Hq / a.H, x = T.r0 + r;
   const size_t row = static_cast<size_t>(T.q0 + x / gqa) * a.Hq + blockIdx.y * gqa + x % gqa;
-  merge_row<D>(ea.part_o + row * ea.ns * D, ea.part_ml + row * ea.ns * 2, n, a.out + row * D, threadIdx.x & 31);
+  merge_row<D>(ea.part_o + row * ea.ns * D, ea.part_ml + row * ea.ns * 4, n, a.out + row * D, threadIdx.x & 31);
 }
 
 struct Plan {
@@ -835,7 +955,7 @@ bool make_plan(const oscar_dims_t* d, int batch, int rows, int max_seq_len, int 
   p->bps = static_cast<int>(bps);
   const size_t parts = ns > 1 ? static_cast<size_t>(rows) * d->num_q_heads * ns : 0;
   p->off_ml = align_up(parts * d->head_dim * sizeof(float), 256);
-  p->total = p->off_ml + align_up(parts * 2 * sizeof(float), 256) + 256;
+  p->total = p->off_ml + align_up(parts * 4 * sizeof(float), 256) + 256;
   return true;
 }
 

@@ -111,9 +111,10 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
-// kind::f16 with fp16 operands, A from TMEM (128 lanes, two fp16 a column), B in shared
-// memory: instruction descriptor, B MN-major.
+// kind::f16 with A from TMEM (128 lanes, two 16-bit values a column), B in shared memory: instruction
+// descriptors for fp16 and for bf16 operands, B MN-major.
 __host__ __device__ constexpr uint32_t idesc_f16_f32_b_mn(int M, int N) { return idesc_f16_f32(M, N, false) | (1u << 16); }
+__host__ __device__ constexpr uint32_t idesc_bf16_f32_b_mn(int M, int N) { return idesc_bf16_f32(M, N) | (1u << 16); }
 
 // One thread: D[tmem] (+)= A[tmem] . B[smem].
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -167,6 +168,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+
+// Whole warp: store 8 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // Whole warp: store 32 consecutive 32-bit columns of this thread's TMEM lane.

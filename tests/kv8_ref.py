@@ -205,3 +205,50 @@ class Pages:
         for s, d in moves:
             self.refs[d], self.refs[s] = self.refs[s], 0
         return n, moves
+
+
+def attention_of_rows(codes, scales, q, row_seq, row_pos, table, fmt, sink, window, decode):
+    """float64 (out, tolerance), the tolerance from what each row sees alone: a position that a row does not see, in
+    the same page or in another, has no part in it.  A = sum w |v| / sum w over the visible positions, w = 1 for
+    the largest logit.
+
+    Both: the output is bf16 (half a step, 2^-8 of itself; 2^-133 where bf16 is subnormal), logits are fp32 sums of D
+    exact products and three fp32 roundings, (D + 16) 2^-24 of sum |q k|, once in the numerator and once in the sum;
+    exponentials and fp32 sums over n positions: 2^-20 + n 2^-24 of A.
+
+    Decode: weights in two fp16 parts hold 2^-22 of themselves and at worst 2^-50 of the largest.
+    Extend: weights as bf16 (2^-8 of themselves) where the V scales of pages are far apart; as fp16 (2^-11, less than
+    that) where the largest so far is at most 2^4 times a block's smallest.  There a row's largest w 2^3 s / r is over
+    1/2 for a reference r, so r <= 2^4 s 2 for every s in the block, and a step of 2^-24 leaves w off by 2^-25 r / (2^3
+    s) <= 2^-23: of |v| at that position, whatever else is in its page."""
+    R, hq, D = q.shape
+    H = codes.shape[1]
+    out = torch.zeros(R, hq, D, dtype=torch.float64, device=q.device)
+    tol = torch.zeros_like(out)
+    as_type = torch.float8_e4m3fn if fmt == E4M3 else torch.int8
+    for b in sorted(set(row_seq)):
+        rows = [r for r in range(R) if row_seq[r] == b and row_pos[r] >= 0]
+        top = max(row_pos[r] for r in rows) + 1
+        j = torch.arange(top, device=q.device)
+        p = torch.tensor([row_pos[r] for r in rows], device=q.device)[:, None]
+        see = j <= p
+        if window:
+            see &= (j < sink) | (j > p - window)
+        ids = torch.as_tensor(table[b][:-(-top // P)], device=q.device).long().clamp(min=0)
+        kv = codes[ids].view(as_type).double() * scales[ids].double()[..., None, None]
+        kv = kv.permute(1, 2, 0, 3, 4).reshape(H, 2, -1, D)[:, :, :top]
+        kv = torch.where(see.any(0)[None, None, :, None], kv, 0.0)
+        n = see.sum(1, keepdim=True)
+        for h in range(hq):
+            qq, kk, vv = q[rows, h].double(), kv[h * H // hq, 0], kv[h * H // hq, 1]
+            s = (qq @ kk.T / math.sqrt(D)).masked_fill(~see, -math.inf)
+            w = torch.exp(s - s.amax(1, keepdim=True))
+            total = w.sum(1, keepdim=True)
+            w = w / total
+            dlog = (D + 16) * 2.0 ** -24 * (qq.abs() @ kk.abs().T / math.sqrt(D)).masked_fill(~see, 0).amax(1, keepdim=True)
+            o, a = w @ vv, w @ vv.abs()
+            own, step = (2.0 ** -22, 2.0 ** -50) if decode else (2.0 ** -8, 2.0 ** -23)
+            out[rows, h] = o
+            tol[rows, h] = (2.0 ** -8 * o.abs() + 2.0 ** -133 + (own + 2.0 ** -20 + n * 2.0 ** -24 + 2 * dlog) * a * 1.01
+                            + step / total * (see.double() @ vv.abs()))
+    return out, tol

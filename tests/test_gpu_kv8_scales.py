@@ -1,0 +1,126 @@
+"""V scales that differ between pages by far: what a row gets depends on what it sees alone, for the decode and the
+extend over the 8-bit cache.  Reference and tolerance: kv8_ref.attention_of_rows."""
+
+import numpy as np
+import pytest
+import torch
+
+import int2_rotated_kv_append_gb300 as ok
+import kv8_ref as R
+from test_gpu_kv8_attention import Cache
+
+pytestmark = pytest.mark.gpu
+
+
+def check(c, out, q, seq, pos, sink, window, decode=False):
+    assert torch.isfinite(out).all()
+    ref, tol = R.attention_of_rows(c.codes, c.scales, q, seq, pos, c.table.tolist(), c.fmt, sink, window, decode)
+    err = (out.double() - ref).abs()
+    worst = (err / tol).max().item()
+    assert (err <= tol).all(), f"{worst:.3g} times the tolerance, at {(err > tol).nonzero()[:4].tolist()}"
+
+
+def scaled(c, exponents):
+    """The V scales of each sequence's pages times 2^exponents[page]."""
+    for b, L in enumerate(c.lens):
+        for j in range(-(-L // 16)):
+            c.scales[c.table[b, j].item(), :, 1] *= 2.0 ** int(exponents[j])
+
+
+PATTERNS = {
+    "one large page": lambda n: np.where(np.arange(n) == n // 2, 40, 0),
+    "every seventh": lambda n: np.where(np.arange(n) % 7 == 3, 26, 0),
+    "rising": lambda n: np.linspace(0, 40, n).round(),
+    "falling": lambda n: np.linspace(10, -30, n).round(),
+    "any": lambda n: np.random.default_rng(n).integers(-60, 60, n),
+    "large at both ends": lambda n: np.where((np.arange(n) == 0) | (np.arange(n) == n - 1), 30, 0),
+}
+
+
+@pytest.mark.parametrize("pattern", list(PATTERNS))
+@pytest.mark.parametrize("D,gqa,fmt", [(64, 5, R.INT8), (128, 8, R.E4M3), (128, 1, R.INT8), (64, 2, R.E4M3)])
+@pytest.mark.parametrize("sink,window", [(0, 0), (0, 64), (20, 100)])
+def test_page_scales_far_apart(pattern, D, gqa, fmt, sink, window):
+    lens = [1100, 333]
+    c = Cache(2, D, fmt, lens, seed=D + gqa + fmt + window)
+    scaled(c, PATTERNS[pattern](-(-max(lens) // 16)))
+    for rows in ([700, 333], [100, 40], [5, 2], [1, 1]):  # two row tiles, one (or two at D = 128), half a tile
+        seq = [b for b, r in enumerate(rows) for _ in range(r)]
+        pos = [lens[b] - r + i for b, r in enumerate(rows) for i in range(r)]
+        q = c.q(len(seq), 2 * gqa)
+        for pps in (0, 16):
+            check(c, c.extend(q, rows, sink, window, pps=pps), q, seq, pos, sink, window)
+    for pps in (0, 3):
+        check(c, c.decode(q, sink, window, pps=pps), q, seq, pos, sink, window, decode=True)
+    assert ok.oscar_device_errors(reset=True) == 0
+
+
+@pytest.mark.parametrize("fmt", [R.E4M3, R.INT8])
+@pytest.mark.parametrize("sink,window", [(0, 0), (0, 48), (37, 48)])
+@pytest.mark.parametrize("at", [[200], [40, 41], [200, 201, 500, 39]])
+def test_infinite_values_are_seen_by_the_rows_that_see_them_alone(fmt, sink, window, at):
+    # the append saturates them and their pages get the largest scale: the other rows of these pages keep what their
+    # codes hold, the other pages' rows all of it
+    H, D, L = 2, 128, 600
+    c = Cache(H, D, fmt, [L], seed=fmt + window + len(at))
+    k, v = (torch.randn(L, H, D, device="cuda", generator=c.g).bfloat16() for _ in range(2))
+    v[at, :, 3] = float("inf")
+    v[at, 1, 70] = -float("inf")
+    start = torch.tensor([0, L], dtype=torch.int32, device="cuda")
+    ok.oscar_kv8_append(c.dims(2 * H), fmt, 1, L, k, v, start, c.table_d, c.lens_d, c.codes, c.scales)
+    for rows in (600, 60, 25, 1):
+        q = c.q(rows, 2 * H)
+        check(c, c.extend(q, [rows], sink, window), q, [0] * rows, list(range(L - rows, L)), sink, window)
+        check(c, c.extend(q, [rows], sink, window, pps=8), q, [0] * rows, list(range(L - rows, L)), sink, window)
+    # rows that end the sequence early: a decode of each length
+    for n in (30, 39, 40, 42, 45, 190, 200, 205, 500, 520):
+        c.lens_d[0] = n
+        q = c.q(1, 2 * H)
+        check(c, c.extend(q, [1], sink, window), q, [0], [n - 1], sink, window)
+
+
+def test_weights_on_pages_of_small_values():
+    # the logits favour the pages with the smallest V, by up to what their scale lacks: every page's share counts
+    c = Cache(1, 128, R.E4M3, [900], seed=31)
+    n = -(-900 // 16)
+    e = np.random.default_rng(5).integers(-20, 1, n)
+    scaled(c, e)
+    for j in range(n):
+        page = c.table[0, j].item()
+        x = c.codes[page, 0, 0].view(torch.float8_e4m3fn).float()
+        x[:, 0] = float(-e[j])  # q's first channel times this: about log 2 per step of the exponent
+        c.codes[page, 0, 0] = x.to(torch.float8_e4m3fn).view(torch.uint8)
+        c.scales[page, 0, 0] = 2.0 ** -5
+    for rows in (300, 10, 1):
+        q = c.q(rows, 4, 0.05)
+        q[:, :, 0] = 256.0
+        pos = list(range(900 - rows, 900))
+        check(c, c.extend(q, [rows]), q, [0] * rows, pos, 0, 0)
+        check(c, c.extend(q, [rows], 0, 200, pps=8), q, [0] * rows, pos, 0, 200)
+    check(c, c.decode(q), q, [0], [899], 0, 0, decode=True)
+
+
+def test_values_of_zero_scale_beside_others():
+    c = Cache(2, 64, R.INT8, [500], seed=32)
+    for j in (3, 4, 20):
+        c.scales[c.table[0, j].item()] = 0.0
+    for j in (7, 9):
+        c.scales[c.table[0, j].item(), :, 1] = 2.0 ** -100
+        c.codes[c.table[0, j].item(), :, 1] = 0
+    for rows in (200, 9, 1):
+        q = c.q(rows, 6)
+        check(c, c.extend(q, [rows]), q, [0] * rows, list(range(500 - rows, 500)), 0, 0)
+    check(c, c.decode(q), q, [0], [499], 0, 0, decode=True)
+
+
+@pytest.mark.parametrize("fmt", [R.E4M3, R.INT8])
+def test_jumps_of_different_sizes_within_a_warp(fmt):
+    # rows that see a page 2^110 above the ones before them beside rows that see one 2^188 above
+    c = Cache(1, 128, fmt, [192], seed=33 + fmt)
+    scaled(c, [-70] * 8 + [40, 118, -70, 0])
+    for rows, hq in ((64, 1), (64, 2), (64, 4), (40, 1), (192, 3)):
+        q = c.q(rows, hq)
+        pos = list(range(192 - rows, 192))
+        check(c, c.extend(q, [rows]), q, [0] * rows, pos, 0, 0)
+        check(c, c.extend(q, [rows], pps=8), q, [0] * rows, pos, 0, 0)
+        check(c, c.extend(q, [rows], 5, 17), q, [0] * rows, pos, 5, 17)
