@@ -11,7 +11,8 @@
 //                   lo = (p - hi) * 2^26, it keeps 22 bits down to 2^-29 and a step of 2^-50 below,
 //                   whatever the other pages hold.  The fragments of S are already those of P: hi parts in
 //                   rows 0..7, lo parts in rows 8..15 of the same A operand;
-//   O += f (P V)    f = 2^(m - running maximum) * the page's V scale, in fp32.
+//   O += f (P V)    f = 2^(m - running maximum) * the page's V scale, in fp32.  In a split with a scale over 2^90 (infinite V
+//                   elements, saturated) O counts 2^40, so that sums of such values stay within fp32.
 // Bound by the bytes of the pages (2 D per token and KV head): 64 sequences of 1024 to 16384 tokens, 8 KV heads,
 // D = 128, 1.12 GB: 184 us with the merge, 6.1 TB/s, 90% of a plain copy's rate.  A page costs about 200
 // instructions a warp; one sequence of 32768 tokens (67 MB) takes 20 us, half of it the start of the
@@ -29,6 +30,8 @@ using namespace oscar::kv8;
 
 constexpr int kWarps = 4;
 constexpr float kHi = 16384.f, kLo = 4096.f;  // p * kHi and the rest * kLo as fp16
+constexpr float kBigScale = 0x1p90f;  // up to here 2^90 times a code (2^9) times 2^27 tokens is within fp32
+constexpr int kBigUnit = 40;
 constexpr int kMaxPps = 512;  // page ids and scales of a split in shared memory
 
 template <int D>
@@ -130,9 +133,13 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
     for (int i = 0; i < min(n_my, kStages); ++i) issue(i);
 
   // the scales, while the first pages are on their way
+  bool big = false;
   for (int i = tid; i < npg; i += kWarps * 32)
-    if (pid_s[i] >= 0)
-      scale_s[i] = __ldg(reinterpret_cast<const float2*>(a.scales) + static_cast<size_t>(pid_s[i]) * a.H + h);
+    if (pid_s[i] >= 0) {
+      const float2 x = __ldg(reinterpret_cast<const float2*>(a.scales) + static_cast<size_t>(pid_s[i]) * a.H + h);
+      scale_s[i] = make_float2(x.x, x.y * (1.f / kHi));
+      big = big || x.y > kBigScale;
+    }
 
   // Q: lane (g, t) holds query g, channels 16 ks + 4 t .. + 3 (k = 2t, 2t+1, 2t+8, 2t+9 of k-step ks)
   uint32_t qa[kKs][2];
@@ -164,7 +171,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
 #pragma unroll
   for (int j = 0; j < kNt; ++j) o[j] = make_float2(0.f, 0.f);
   float m_run = -INFINITY, l_run = 0.f;  // l: this lane's tokens
-  __syncthreads();  // scales
+  big = __syncthreads_or(big);  // scales
+  if (big) {
+    for (int i = tid; i < npg; i += kWarps * 32)
+      if (pid_s[i] >= 0) scale_s[i].y *= pow2i(-kBigUnit);
+    __syncthreads();
+  }
   bool aborted = false;
   int i = 0;
   for (; i < n_my; ++i) {
@@ -230,7 +242,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
         pa[2 * c] = *reinterpret_cast<const uint32_t*>(&hi[c]);
         pa[2 * c + 1] = pack_half2(fmaf(p[2 * c], kHi, -back.x) * kLo, fmaf(p[2 * c + 1], kHi, -back.y) * kLo);
       }
-      const float fv = f * sc.y * (1.f / kHi);
+      const float fv = f * sc.y;
       const float2 fv2 = make_float2(fv, fv), lo2 = make_float2(1.f / kLo, 1.f / kLo);
       // V: this lane's tokens, channels kNt g .. kNt g + kNt - 1
       uint32_t w[4][kNt / 4];
@@ -300,6 +312,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
   }
   __syncthreads();
   const bool single = vis.n <= sa.pps;  // the only split of this sequence
+  const float unit = big ? kBigUnit : 0.f;
   for (int idx = tid; idx < gqa * (D / 4); idx += kWarps * 32) {
     const int qi = idx / (D / 4), c4 = idx % (D / 4);
     float M = -INFINITY;
@@ -317,11 +330,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
     }
     const size_t row = static_cast<size_t>(b) * a.Hq + h * gqa + qi;
     if (single) {
-      store_out4(a.out + row * D + 4 * c4, r, l, 0.f);
+      store_out4(a.out + row * D + 4 * c4, r, l, unit);
     } else {
       const size_t part = row * sa.ns + s;
       *reinterpret_cast<float4*>(sa.part_o + part * D + 4 * c4) = r;
-      if (c4 == 0) *reinterpret_cast<float4*>(sa.part_ml + part * 4) = make_float4(M, l, M, 0.f);
+      if (c4 == 0) *reinterpret_cast<float4*>(sa.part_ml + part * 4) = make_float4(M, l, M + unit, 0.f);
     }
   }
 }

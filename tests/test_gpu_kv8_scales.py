@@ -124,3 +124,33 @@ def test_jumps_of_different_sizes_within_a_warp(fmt):
         check(c, c.extend(q, [rows]), q, [0] * rows, pos, 0, 0)
         check(c, c.extend(q, [rows], pps=8), q, [0] * rows, pos, 0, 0)
         check(c, c.extend(q, [rows], 5, 17), q, [0] * rows, pos, 5, 17)
+
+
+@pytest.mark.parametrize("fmt", [R.E4M3, R.INT8])
+@pytest.mark.parametrize("sink,window", [(0, 0), (37, 48)])
+@pytest.mark.parametrize("pps", [0, 1, 4])
+def test_decode_of_several_infinite_values(fmt, sink, window, pps):
+    # their weighted sum is beyond fp32 before it is divided by the weights' sum
+    c = Cache(2, 128, fmt, [900, 400, 50], seed=fmt + window + 40)
+    k, v = (torch.randn(1350, 2, 128, device="cuda", generator=c.g).bfloat16() for _ in range(2))
+    v[[5, 30, 31, 870, 880, 899, 900, 901, 930, 1299, 1310, 1311], :, 3] = float("inf")
+    v[[20, 890, 1290, 1305], 1, 70:90] = -float("inf")
+    start = torch.tensor([0, 900, 1300, 1350], dtype=torch.int32, device="cuda")
+    ok.oscar_kv8_append(c.dims(8), fmt, 3, 900, k, v, start, c.table_d, c.lens_d, c.codes, c.scales)
+    for factor in (0.01, 1.0, 8.0):  # even weights (the sum of many), and a few large ones
+        q = c.q(3, 8, factor)
+        check(c, c.decode(q, sink, window, pps=pps), q, [0, 1, 2], [899, 399, 49], sink, window, decode=True)
+        check(c, c.extend(q, [1, 1, 1], sink, window, pps=8 * pps), q, [0, 1, 2], [899, 399, 49], sink, window)
+
+
+def test_decode_beside_a_token_of_a_large_scale_behind_the_window():
+    # the window's first page has its scale from a token that is out of the window
+    c = Cache(1, 64, R.INT8, [300], seed=45)
+    scaled(c, [-60] * 19)
+    page = c.table[0, 10].item()
+    c.scales[page, 0, 1] = 2.0 ** 118
+    c.codes[page, 0, 1, 8:] = 0
+    q = c.q(1, 4)
+    check(c, c.decode(q, 0, 300 - 168), q, [0], [299], 0, 300 - 168, decode=True)
+    check(c, c.decode(q, 0, 300 - 168, pps=3), q, [0], [299], 0, 300 - 168, decode=True)
+    check(c, c.extend(q, [1], 0, 300 - 168), q, [0], [299], 0, 300 - 168)
