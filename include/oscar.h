@@ -493,6 +493,18 @@ oscar_status_t oscar_kv8_append(const oscar_dims_t* dims, int32_t kv_format, int
                                 float* kv8_scales, void* stream);
 
 /*
+ * oscar_kv8_append_granted -- the same for steps whose reservation may have been refused (oscar_pages_reserve): a
+ * sequence with granted[b] == 0 (device int32 [batch]; NULL: none) is skipped, its rows of k and v are not read.  Without it
+ * the tokens would go to the last n_b positions of a length that has not grown: over earlier tokens, in pages that
+ * other sequences may share.  After the step such a sequence is as it was before: a decode sees its earlier
+ * tokens alone, and the rows of an extend, which ask for positions that it does not have, mean nothing.
+ */
+oscar_status_t oscar_kv8_append_granted(const oscar_dims_t* dims, int32_t kv_format, int32_t batch, int64_t num_tokens,
+                                        int32_t max_tokens_per_seq, const void* k, const void* v,
+                                        const int32_t* t_start, const int32_t* page_table, const int32_t* seq_lens,
+                                        const int32_t* granted, uint8_t* kv8_pages, float* kv8_scales, void* stream);
+
+/*
  * oscar_kv8_decode -- paged GQA decode attention over the 8-bit cache, with an
  * optional sliding window whose first tokens stay visible (sinks).
  * For sequence b of length L = seq_lens[b], query head hq, KV head hq / (Hq/Hkv):
@@ -598,7 +610,7 @@ oscar_status_t oscar_pages_copy(const oscar_dims_t* dims, int32_t num_pools, con
  * seq_lens[b] becomes L + new_tokens[b].  granted[b] (device int32, may be NULL) is 1, or 0 where
  * the request was refused: sequences are served in order, and one whose pages, together with
  * those that all sequences before it asked for, outnumber the free pages is refused (nothing of it
- * changes; OSCAR_DEVERR_NO_PAGES).
+ * changes; OSCAR_DEVERR_NO_PAGES).  Its tokens must not be appended (oscar_kv8_append_granted).
  */
 oscar_status_t oscar_pages_reserve(const oscar_dims_t* dims, int32_t batch, const int32_t* new_tokens,
                                    int32_t* page_table, int32_t* seq_lens, int32_t* page_refs, int32_t* granted,

@@ -88,6 +88,7 @@ def _load():
         "oscar_calibrate": (I32, [D, I64, P, P, I32, ctypes.c_double, ctypes.POINTER(oscar_calib_out_t),
                                   ctypes.POINTER(oscar_calib_out_t), P, SZ, P]),
         "oscar_kv8_append": (I32, [D, I32, I32, I64, I32, P, P, P, P, P, P, P, P]),
+        "oscar_kv8_append_granted": (I32, [D, I32, I32, I64, I32, P, P, P, P, P, P, P, P, P]),
         "oscar_kv8_decode_workspace_bytes": (SZ, [D, I32, I32, I32, I32, I32]),
         "oscar_kv8_decode": (I32, [D, I32, I32, I32, I32, P, P, P, P, P, I32, I32, F32, P, P, SZ, P]),
         "oscar_kv8_extend_varlen_workspace_bytes": (SZ, [D, I32, I32, I32, I32, I32, I32, I32]),
@@ -328,14 +329,17 @@ def _nbytes(t) -> int:
 
 
 def oscar_kv8_append(dims, kv_format, batch, max_tokens_per_seq, k, v, t_start, page_table, seq_lens, kv8_pages,
-                     kv8_scales, stream=None):
+                     kv8_scales, stream=None, granted=None):
     """Quantise the new tokens k, v (bf16 [T][Hkv][D]; rows t_start[b] .. t_start[b+1]-1 are the
     last positions of sequence b) into the 8-bit pool: codes and a power-of-two scale per
-    (page, KV head, K | V)."""
-    _check(lib.oscar_kv8_append(ctypes.byref(_dims(dims)), int(kv_format), int(batch), int(k.shape[0]),
-                                int(max_tokens_per_seq), _ptr(k), _ptr(v), _ptr(t_start), _ptr(page_table),
-                                _ptr(seq_lens), _ptr(kv8_pages), _ptr(kv8_scales), _stream(stream)),
-           "oscar_kv8_append")
+    (page, KV head, K | V).  ``granted`` (int32 [batch], as oscar_pages_reserve leaves it, or None):
+    sequences with a 0 are skipped."""
+    if granted is not None and granted.numel() < batch:
+        raise ValueError("granted has one entry per sequence")
+    _check(lib.oscar_kv8_append_granted(ctypes.byref(_dims(dims)), int(kv_format), int(batch), int(k.shape[0]),
+                                        int(max_tokens_per_seq), _ptr(k), _ptr(v), _ptr(t_start), _ptr(page_table),
+                                        _ptr(seq_lens), _ptr(granted), _ptr(kv8_pages), _ptr(kv8_scales),
+                                        _stream(stream)), "oscar_kv8_append")
 
 
 def oscar_kv8_decode_workspace_bytes(dims, batch, max_seq_len, pages_per_split, sink_len, window_len) -> int:

@@ -178,7 +178,7 @@ class Kv8Cache:
         self.page_table = torch.full((batch, self.dims.max_pages_per_seq), -1, dtype=torch.int32, device=d)
         self.seq_lens = torch.zeros(batch, dtype=torch.int32, device=d)
         self.page_refs = torch.zeros(num_pages, dtype=torch.int32, device=d)
-        self.granted = torch.zeros(batch, dtype=torch.int32, device=d)
+        self.granted = torch.ones(batch, dtype=torch.int32, device=d)  # of the last reserve
         self._ws = []  # the last one is used; smaller ones stay for captured graphs that point to them
 
     def _workspace(self, nbytes):
@@ -195,9 +195,10 @@ class Kv8Cache:
         return self.granted
 
     def append(self, k, v, t_start, max_tokens_per_seq, stream=None):
-        """Quantise the reserved tokens k, v [T][Hkv][D]; t_start int32 device [batch + 1]."""
+        """Quantise the reserved tokens k, v [T][Hkv][D]; t_start int32 device [batch + 1].  Sequences that the
+        last ``reserve`` refused are skipped and stay as they were."""
         oscar_kv8_append(self.dims, self.kv_format, self.batch, max_tokens_per_seq, k, v, t_start, self.page_table,
-                         self.seq_lens, self.pages, self.scales, stream)
+                         self.seq_lens, self.pages, self.scales, stream, granted=self.granted)
 
     def decode(self, q, out=None, sm_scale=0.0, pages_per_split=0, stream=None):
         if out is None:

@@ -21,6 +21,7 @@ struct AppendArgs {
   const int32_t* t_start;
   const int32_t* page_table;
   const int32_t* seq_lens;
+  const int32_t* granted;  // null: every sequence
   uint8_t* pages;
   float* scales;
   int H, num_pages, max_pages, max_new;
@@ -37,7 +38,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_append_kernel(AppendArgs a) {
   const int b = blockIdx.z;
   const int t0 = __ldg(a.t_start + b), t1 = __ldg(a.t_start + b + 1), L = __ldg(a.seq_lens + b);
   const int n = t1 - t0;
-  if (n == 0) return;
+  if (n == 0 || (a.granted != nullptr && __ldg(a.granted + b) == 0)) return;
   if (n < 0 || n > a.max_new || n > L || t0 < 0 || t1 > a.num_tokens || L > a.max_pages * kPageSize) {
     if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) record_error(OSCAR_DEVERR_POSITION);
     return;
@@ -130,13 +131,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_append_kernel(AppendArgs a) {
   if (lane == 0 && scale != stored) a.scales[block] = scale;
 }
 
-}  // namespace
-
-extern "C" oscar_status_t oscar_kv8_append(const oscar_dims_t* dims, int32_t kv_format, int32_t batch,
-                                           int64_t num_tokens, int32_t max_tokens_per_seq, const void* k,
-                                           const void* v, const int32_t* t_start, const int32_t* page_table,
-                                           const int32_t* seq_lens, uint8_t* kv8_pages, float* kv8_scales,
-                                           void* stream) {
+oscar_status_t append(const oscar_dims_t* dims, int32_t kv_format, int32_t batch, int64_t num_tokens,
+                      int32_t max_tokens_per_seq, const void* k, const void* v, const int32_t* t_start,
+                      const int32_t* page_table, const int32_t* seq_lens, const int32_t* granted, uint8_t* kv8_pages,
+                      float* kv8_scales, void* stream) {
   const oscar_status_t st = check_dims(dims);
   if (st != OSCAR_OK) return st;
   if (kv_format != OSCAR_KV8_E4M3 && kv_format != OSCAR_KV8_INT8) return OSCAR_ERR_INVALID_ARG;
@@ -153,8 +151,8 @@ extern "C" oscar_status_t oscar_kv8_append(const oscar_dims_t* dims, int32_t kv_
   if (gy > 65535 || batch > 65535) return OSCAR_ERR_UNSUPPORTED;
   if (static_cast<long long>(dims->max_pages_per_seq) * kPageSize > 0x7fffffffLL) return OSCAR_ERR_UNSUPPORTED;
   AppendArgs a{static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), t_start, page_table,
-               seq_lens, kv8_pages, kv8_scales, dims->num_kv_heads, dims->num_pages, dims->max_pages_per_seq,
-               max_tokens_per_seq, num_tokens};
+               seq_lens, granted, kv8_pages, kv8_scales, dims->num_kv_heads, dims->num_pages,
+               dims->max_pages_per_seq, max_tokens_per_seq, num_tokens};
   const dim3 grid(static_cast<unsigned>(gx), gy, batch);
   const bool d128 = dims->head_dim == 128;
   auto* kernel = kv_format == OSCAR_KV8_E4M3
@@ -162,6 +160,26 @@ extern "C" oscar_status_t oscar_kv8_append(const oscar_dims_t* dims, int32_t kv_
                      : (d128 ? kv8_append_kernel<kInt8, 128> : kv8_append_kernel<kInt8, 64>);
   kernel<<<grid, kWarps * 32, 0, as_stream(stream)>>>(a);
   return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" oscar_status_t oscar_kv8_append(const oscar_dims_t* dims, int32_t kv_format, int32_t batch,
+                                           int64_t num_tokens, int32_t max_tokens_per_seq, const void* k,
+                                           const void* v, const int32_t* t_start, const int32_t* page_table,
+                                           const int32_t* seq_lens, uint8_t* kv8_pages, float* kv8_scales,
+                                           void* stream) {
+  return append(dims, kv_format, batch, num_tokens, max_tokens_per_seq, k, v, t_start, page_table, seq_lens, nullptr,
+                kv8_pages, kv8_scales, stream);
+}
+
+extern "C" oscar_status_t oscar_kv8_append_granted(const oscar_dims_t* dims, int32_t kv_format, int32_t batch,
+                                                   int64_t num_tokens, int32_t max_tokens_per_seq, const void* k,
+                                                   const void* v, const int32_t* t_start, const int32_t* page_table,
+                                                   const int32_t* seq_lens, const int32_t* granted, uint8_t* kv8_pages,
+                                                   float* kv8_scales, void* stream) {
+  return append(dims, kv_format, batch, num_tokens, max_tokens_per_seq, k, v, t_start, page_table, seq_lens, granted,
+                kv8_pages, kv8_scales, stream);
 }
 
 oscar_status_t oscar_internal_kv8_append_errors(uint32_t* flags, int reset) {

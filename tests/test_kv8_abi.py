@@ -141,3 +141,19 @@ def test_python_pools_are_contiguous_tensors_of_equal_pages():
         ok._pools([torch.zeros(0)], 10)
     arr = ok._pools([torch.zeros(10, 4), torch.zeros(30, dtype=torch.bfloat16)], 10)
     assert (arr[0].page_bytes, arr[1].page_bytes) == (16, 6)
+
+
+def test_append_granted_refuses_what_append_refuses(lib):
+    def call(d=None, fmt=0, batch=2, tokens=4, most=3, **ptr):
+        a = {n: P for n in "k v start table lens granted pages scales".split()}
+        a.update(ptr)
+        return lib.oscar_kv8_append_granted(dims() if d is None else d[0], fmt, batch, tokens, most, a["k"], a["v"], a["start"],
+                                            a["table"], a["lens"], a["granted"], a["pages"], a["scales"], None)
+    for d, want in BAD_DIMS:
+        assert call((d,)) == want
+    assert call(tokens=0) == OK and call(tokens=0, granted=None) == OK
+    assert call(fmt=2) == BAD and call(batch=-1) == BAD and call(most=0) == BAD and call(batch=65536) == UNS
+    for n in "k v start table lens pages scales".split():
+        assert call(**{n: None}) == BAD
+    with pytest.raises(ValueError):
+        ok.oscar_kv8_append(None, 0, 2, 1, torch.zeros(2, 8, 128), None, None, None, None, None, None, granted=torch.ones(1))
