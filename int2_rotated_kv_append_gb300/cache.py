@@ -162,16 +162,18 @@ class Bf16Cache:
 
 
 class Kv8Cache:
-    """An 8-bit paged cache for up to ``batch`` sequences, with its page table, lengths and page
-    counts.  With ``window_len`` >= 1 attention sees the last window_len positions and the first
-    sink_len, and ``trim`` gives back the pages behind the window."""
+    """An 8-bit paged cache for up to ``batch`` sequences of max_seq_len tokens (rounded up to whole
+    pages of 16), with its page table, lengths and page counts.  With ``window_len`` >= 1 attention
+    sees the last window_len positions and the first sink_len, and ``trim`` gives back the pages
+    behind the window."""
 
     def __init__(self, num_q_heads, num_kv_heads, head_dim, num_pages, batch, max_seq_len, kv_format=OSCAR_KV8_E4M3,
                  sink_len=0, window_len=0, device="cuda"):
         self.device = torch.device(device)
-        self.batch, self.max_seq_len, self.kv_format = batch, max_seq_len, kv_format
+        self.batch, self.kv_format = batch, kv_format
         self.sink_len, self.window_len = sink_len, window_len
         self.dims = make_dims(num_q_heads, num_kv_heads, head_dim, 16, head_dim, num_pages, max(1, -(-max_seq_len // 16)))
+        self.max_seq_len = 16 * self.dims.max_pages_per_seq  # what reserve grants, the attention sees
         d = self.device
         self.pages = torch.zeros((num_pages, num_kv_heads, 2, 16, head_dim), dtype=torch.uint8, device=d)
         self.scales = torch.zeros((num_pages, num_kv_heads, 2), dtype=torch.float32, device=d)
