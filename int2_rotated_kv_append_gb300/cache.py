@@ -6,9 +6,14 @@ speedup reference; ``Kv8Cache`` owns an 8-bit pool whose pages it manages itself
 (reserve, fork, free, trim, compact).  They only allocate torch memory and call the
 library, as does ``calibrate`` (the offline step that produces R and the clipping
 thresholds).
+
+``Int2Cache`` and ``Bf16Cache`` have one workspace each: calls of one such cache are
+made on one stream at a time.  ``Kv8Cache`` has one per stream.
 """
 
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
@@ -17,7 +22,7 @@ from . import (OSCAR_KV8_E4M3, make_dims, oscar_append, oscar_append_mixed, osca
                oscar_decode_workspace_bytes, oscar_extend, oscar_extend_varlen, oscar_extend_varlen_workspace_bytes,
                oscar_extend_workspace_bytes, oscar_kv8_append, oscar_kv8_decode, oscar_kv8_decode_workspace_bytes,
                oscar_kv8_extend_varlen, oscar_kv8_extend_varlen_workspace_bytes, oscar_pages_compact, oscar_pages_fork,
-               oscar_pages_free, oscar_pages_reserve, oscar_pages_trim, oscar_pages_workspace_bytes)
+               oscar_pages_free, oscar_pages_reserve, oscar_pages_trim, oscar_pages_workspace_bytes, _stream)
 from .synth import Workload
 
 SENTINEL = 0xA5
@@ -165,7 +170,12 @@ class Kv8Cache:
     """An 8-bit paged cache for up to ``batch`` sequences of max_seq_len tokens (rounded up to whole
     pages of 16), with its page table, lengths and page counts.  With ``window_len`` >= 1 attention
     sees the last window_len positions and the first sink_len, and ``trim`` gives back the pages
-    behind the window."""
+    behind the window.
+
+    Every method takes the stream of its call (a torch stream or a handle; None: the current one).
+    Calls on different streams have workspaces of their own, so two that only read the cache may
+    run at once; graphs captured on one stream share its workspace and are replayed one after
+    another.  Outputs that a method makes belong to its stream."""
 
     def __init__(self, num_q_heads, num_kv_heads, head_dim, num_pages, batch, max_seq_len, kv_format=OSCAR_KV8_E4M3,
                  sink_len=0, window_len=0, device="cuda"):
@@ -181,19 +191,33 @@ class Kv8Cache:
         self.seq_lens = torch.zeros(batch, dtype=torch.int32, device=d)
         self.page_refs = torch.zeros(num_pages, dtype=torch.int32, device=d)
         self.granted = torch.ones(batch, dtype=torch.int32, device=d)  # of the last reserve
-        self._ws = []  # the last one is used; smaller ones stay for captured graphs that point to them
+        self._ws = {}  # by stream: the last one is used, smaller ones stay for captured graphs that point to them
 
-    def _workspace(self, nbytes):
+    def _allocating(self, stream):
+        """The context in which what a call on ``stream`` uses is allocated."""
+        if stream is None or self.device.type != "cuda":
+            return contextlib.nullcontext()
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device) if int(stream) else torch.cuda.default_stream(self.device)
+        return torch.cuda.stream(stream)
+
+    def _workspace(self, nbytes, stream):
         if nbytes == 0:
             raise ValueError("invalid arguments for workspace sizing")
-        if not self._ws or self._ws[-1].numel() < nbytes:
-            self._ws.append(torch.empty(nbytes, dtype=torch.uint8, device=self.device))
-        return self._ws[-1]
+        own = self._ws.setdefault(_stream(stream), [])
+        if not own or own[-1].numel() < nbytes:
+            with self._allocating(stream):
+                own.append(torch.empty(nbytes, dtype=torch.uint8, device=self.device))
+        return own[-1]
+
+    def _output(self, q, stream):
+        with self._allocating(stream):
+            return torch.empty_like(q)
 
     def reserve(self, new_tokens, stream=None):
         """Pages for new_tokens[b] (int32 device [batch]) more tokens of each sequence; returns ``granted``."""
         oscar_pages_reserve(self.dims, new_tokens, self.page_table, self.seq_lens, self.page_refs, self.granted,
-                            self._workspace(oscar_pages_workspace_bytes(self.dims, self.batch, 0)), stream)
+                            self._workspace(oscar_pages_workspace_bytes(self.dims, self.batch, 0), stream), stream)
         return self.granted
 
     def append(self, k, v, t_start, max_tokens_per_seq, stream=None):
@@ -204,9 +228,9 @@ class Kv8Cache:
 
     def decode(self, q, out=None, sm_scale=0.0, pages_per_split=0, stream=None):
         if out is None:
-            out = torch.empty_like(q)
+            out = self._output(q, stream)
         ws = self._workspace(oscar_kv8_decode_workspace_bytes(self.dims, self.batch, self.max_seq_len, pages_per_split,
-                                                              self.sink_len, self.window_len))
+                                                              self.sink_len, self.window_len), stream)
         oscar_kv8_decode(self.dims, self.kv_format, self.batch, self.max_seq_len, pages_per_split, q, self.pages,
                          self.scales, self.page_table, self.seq_lens, self.sink_len, self.window_len, sm_scale, out, ws,
                          stream)
@@ -214,10 +238,10 @@ class Kv8Cache:
 
     def extend(self, q, q_start, max_rows_per_seq, out=None, sm_scale=0.0, pages_per_split=0, stream=None):
         if out is None:
-            out = torch.empty_like(q)
+            out = self._output(q, stream)
         ws = self._workspace(oscar_kv8_extend_varlen_workspace_bytes(
             self.dims, self.batch, q.shape[0], self.max_seq_len, max_rows_per_seq, pages_per_split, self.sink_len,
-            self.window_len))
+            self.window_len), stream)
         oscar_kv8_extend_varlen(self.dims, self.kv_format, self.batch, self.max_seq_len, max_rows_per_seq,
                                 pages_per_split, q, q_start, self.pages, self.scales, self.page_table, self.seq_lens,
                                 self.sink_len, self.window_len, sm_scale, out, ws, stream)
@@ -226,7 +250,7 @@ class Kv8Cache:
     def fork(self, src_seq, dst_seq, granted=None, stream=None):
         oscar_pages_fork(self.dims, [self.pages, self.scales], src_seq, dst_seq, self.page_table, self.seq_lens,
                          self.page_refs, granted,
-                         self._workspace(oscar_pages_workspace_bytes(self.dims, self.batch, src_seq.numel())), stream)
+                         self._workspace(oscar_pages_workspace_bytes(self.dims, self.batch, src_seq.numel()), stream), stream)
 
     def free(self, seqs, stream=None):
         oscar_pages_free(self.dims, seqs, self.page_table, self.seq_lens, self.page_refs, stream)
@@ -237,7 +261,7 @@ class Kv8Cache:
 
     def compact(self, num_used=None, stream=None):
         oscar_pages_compact(self.dims, [self.pages, self.scales], self.page_table, self.seq_lens, self.page_refs,
-                            num_used, self._workspace(oscar_pages_workspace_bytes(self.dims, self.batch, 0)), stream)
+                            num_used, self._workspace(oscar_pages_workspace_bytes(self.dims, self.batch, 0), stream), stream)
 
 
 def calibrate(k=None, v=None, centered: bool = True, clip_quantile: float = 1.0, with_cov: bool = False,

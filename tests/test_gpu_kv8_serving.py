@@ -147,3 +147,21 @@ def test_fork_of_an_int2_cache_decodes_the_same():
     again = c.decode(q)
     assert torch.equal(again[2], out[2]) and torch.equal(again[3], out[3]) and not again[:2].any()
     assert used.item() == 32 + 21 and ok.oscar_device_errors(reset=True) == 0
+
+
+def test_decode_and_extend_of_one_cache_on_two_streams():
+    s = Server(num_q_heads=16, num_kv_heads=2, head_dim=128, num_pages=400, batch=2, max_seq_len=3000, kv_format=R.INT8)
+    c = s.c
+    s.add([3000, 1500])
+    q, qx = (torch.randn(n, 16, 128, device="cuda", generator=s.g).bfloat16() for n in (2, 300))
+    start = i32([0, 200, 300])
+    want, wantx = c.decode(q), c.extend(qx, start, 200)
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for i in range(20):
+        got.append((c.decode(q, stream=a if i % 2 else a.cuda_stream), want))
+        got.append((c.extend(qx, start, 200, stream=b), wantx))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in got)
+    assert torch.equal(c.decode(q, stream=0), want)
