@@ -226,25 +226,37 @@ class Kv8Cache:
         oscar_kv8_append(self.dims, self.kv_format, self.batch, max_tokens_per_seq, k, v, t_start, self.page_table,
                          self.seq_lens, self.pages, self.scales, stream, granted=self.granted)
 
-    def decode(self, q, out=None, sm_scale=0.0, pages_per_split=0, stream=None):
+    def _bound(self, max_seq_len):
+        if max_seq_len is None:
+            return self.max_seq_len
+        if not 0 <= max_seq_len <= self.max_seq_len:
+            raise ValueError(f"max_seq_len is between 0 and the cache's {self.max_seq_len}")
+        return max_seq_len
+
+    def decode(self, q, out=None, sm_scale=0.0, pages_per_split=0, stream=None, max_seq_len=None):
+        """One query row per sequence.  ``max_seq_len``: a bound on every length (None: the cache's room); the work is
+        split for it, so a bound near the longest length is quicker than a large cache's room."""
+        bound = self._bound(max_seq_len)
         if out is None:
             out = self._output(q, stream)
-        ws = self._workspace(oscar_kv8_decode_workspace_bytes(self.dims, self.batch, self.max_seq_len, pages_per_split,
+        ws = self._workspace(oscar_kv8_decode_workspace_bytes(self.dims, self.batch, bound, pages_per_split,
                                                               self.sink_len, self.window_len), stream)
-        oscar_kv8_decode(self.dims, self.kv_format, self.batch, self.max_seq_len, pages_per_split, q, self.pages,
-                         self.scales, self.page_table, self.seq_lens, self.sink_len, self.window_len, sm_scale, out, ws,
-                         stream)
+        oscar_kv8_decode(self.dims, self.kv_format, self.batch, bound, pages_per_split, q, self.pages, self.scales,
+                         self.page_table, self.seq_lens, self.sink_len, self.window_len, sm_scale, out, ws, stream)
         return out
 
-    def extend(self, q, q_start, max_rows_per_seq, out=None, sm_scale=0.0, pages_per_split=0, stream=None):
+    def extend(self, q, q_start, max_rows_per_seq, out=None, sm_scale=0.0, pages_per_split=0, stream=None,
+               max_seq_len=None):
+        """The last rows of each sequence, q_start int32 device [batch + 1]; ``max_seq_len`` as in ``decode``."""
+        bound = self._bound(max_seq_len)
         if out is None:
             out = self._output(q, stream)
         ws = self._workspace(oscar_kv8_extend_varlen_workspace_bytes(
-            self.dims, self.batch, q.shape[0], self.max_seq_len, max_rows_per_seq, pages_per_split, self.sink_len,
+            self.dims, self.batch, q.shape[0], bound, max_rows_per_seq, pages_per_split, self.sink_len,
             self.window_len), stream)
-        oscar_kv8_extend_varlen(self.dims, self.kv_format, self.batch, self.max_seq_len, max_rows_per_seq,
-                                pages_per_split, q, q_start, self.pages, self.scales, self.page_table, self.seq_lens,
-                                self.sink_len, self.window_len, sm_scale, out, ws, stream)
+        oscar_kv8_extend_varlen(self.dims, self.kv_format, self.batch, bound, max_rows_per_seq, pages_per_split, q,
+                                q_start, self.pages, self.scales, self.page_table, self.seq_lens, self.sink_len,
+                                self.window_len, sm_scale, out, ws, stream)
         return out
 
     def fork(self, src_seq, dst_seq, granted=None, stream=None):

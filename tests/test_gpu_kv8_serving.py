@@ -165,3 +165,17 @@ def test_decode_and_extend_of_one_cache_on_two_streams():
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in got)
     assert torch.equal(c.decode(q, stream=0), want)
+
+
+def test_a_tight_length_bound_gives_the_same_rows():
+    s = Server(num_q_heads=8, num_kv_heads=2, head_dim=64, num_pages=100, batch=2, max_seq_len=100000)
+    s.add([1000, 333])
+    q, qx = (torch.randn(n, 8, 64, device="cuda", generator=s.g).bfloat16() for n in (2, 50))
+    c, start = s.c, i32([0, 40, 50])
+    for bound in (None, 1000, 50000):
+        ref, tol = R.attention(c.pages, c.scales, q, [0, 1], [999, 332], c.page_table.tolist(), c.kv_format, 0, 0)
+        assert ((c.decode(q, max_seq_len=bound).double() - ref).abs() <= tol).all()
+        pos = list(range(960, 1000)) + list(range(323, 333))
+        ref, tol = R.attention(c.pages, c.scales, qx, [0] * 40 + [1] * 10, pos, c.page_table.tolist(), c.kv_format, 0, 0)
+        assert ((c.extend(qx, start, 40, max_seq_len=bound).double() - ref).abs() <= tol).all()
+    assert ok.oscar_device_errors(reset=True) == 0

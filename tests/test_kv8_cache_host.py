@@ -49,3 +49,25 @@ def test_a_grown_workspace_leaves_the_smaller_one_to_captured_graphs(recorded):
     small, large, again = (ws for _, ws, _ in recorded)
     assert small.numel() < large.numel() and again.data_ptr() == large.data_ptr()
     assert any(w.data_ptr() == small.data_ptr() for w in c._ws[3])
+
+
+def test_attention_is_planned_for_the_longest_length_that_the_caller_names(recorded, monkeypatch):
+    sizes = []
+    for name in ("oscar_kv8_decode_workspace_bytes", "oscar_kv8_extend_varlen_workspace_bytes"):
+        real = getattr(cache, name)
+        monkeypatch.setattr(cache, name, lambda *a, real=real: sizes.append(a) or real(*a))
+    lengths = []
+    for name, at in (("oscar_kv8_decode", 3), ("oscar_kv8_extend_varlen", 3)):
+        monkeypatch.setattr(cache, name, lambda *a, at=at: lengths.append(a[at]))
+    c = make()
+    q = torch.zeros(2, 8, 64, dtype=torch.bfloat16)
+    start = torch.tensor([0, 1, 2], dtype=torch.int32)
+    for given, want in ((None, 2000), (700, 700), (2000, 2000)):
+        c.decode(q, max_seq_len=given, stream=3)
+        c.extend(q, start, 1, max_seq_len=given, stream=3)
+        assert lengths[-2:] == [want, want] and sizes[-2][2] == want and sizes[-1][3] == want
+    for given in (2001, -1):
+        with pytest.raises(ValueError):
+            c.decode(q, max_seq_len=given, stream=3)
+        with pytest.raises(ValueError):
+            c.extend(q, start, 1, max_seq_len=given, stream=3)
