@@ -142,13 +142,18 @@ def make_dims(num_q_heads, num_kv_heads, head_dim, page_size, group_size, num_pa
                         int(num_pages), int(max_pages_per_seq))
 
 
+_DIM_NAMES = frozenset(n for n, _ in oscar_dims_t._fields_)
+
+
 def _dims(d) -> oscar_dims_t:
     if isinstance(d, oscar_dims_t):
         return d
-    try:
-        return oscar_dims_t(**d)
-    except TypeError:  # numbers of other types
-        return make_dims(**d)
+    if d.keys() == _DIM_NAMES:
+        try:
+            return oscar_dims_t(**d)
+        except TypeError:  # numbers of other types
+            pass
+    return make_dims(**d)  # (which names a missing or an unknown field)
 
 
 def _ptr(t) -> int | None:

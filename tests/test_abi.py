@@ -223,3 +223,17 @@ def test_decode_plan_fused_form_rules(lib):
     assert plan(64, 2, 131072, 256)["fused"] == 0     # GQA 8: more than 512 pages per split
     assert plan(64, 1, 131072, 256)["fused"] == 1     # GQA 8: about 455 pages per split
     assert plan(64, 4, 131072, 256, pps=2800)["fused"] == 1
+
+
+def test_dims_given_as_a_dict_have_exactly_the_fields():
+    import numpy as np
+
+    from int2_rotated_kv_append_gb300 import _dims
+    good = dict(num_q_heads=8, num_kv_heads=2, head_dim=128, page_size=16, group_size=64, num_pages=10, max_pages_per_seq=4)
+    want = [good[n] for n, _ in ok.oscar_dims_t._fields_]
+    assert [getattr(_dims(good), n) for n, _ in ok.oscar_dims_t._fields_] == want
+    assert [getattr(_dims({k: np.int64(v) for k, v in good.items()}), n) for n, _ in ok.oscar_dims_t._fields_] == want
+    for bad in (dict(good, num_page=3), {k: v for k, v in good.items() if k != "page_size"},
+                dict({k: v for k, v in good.items() if k != "num_pages"}, num_page=10)):
+        with pytest.raises(TypeError):
+            _dims(bad)
