@@ -514,7 +514,7 @@ oscar_status_t oscar_kv8_append_granted(const oscar_dims_t* dims, int32_t kv_for
  * A sequence with L == 0 gets zeros.  Pages without a visible position are not read: their
  * page table entries may hold anything (oscar_pages_trim sets them to -1).
  * Arguments
- *   max_seq_len   host bound on every seq_lens[b] (<= max_pages_per_seq * P); larger or negative
+ *   max_seq_len   host bound on every seq_lens[b] (<= max_pages_per_seq * P, < 2^31 - 32); larger or negative
  *                 device values are clamped and flagged (OSCAR_DEVERR_SEQ_LEN)
  *   pages_per_split  0 = chosen from the grid size; else >= 1 pages of one split (no more than 512
  *                 are taken; at most 65535 splits per sequence; batch <= 65535)

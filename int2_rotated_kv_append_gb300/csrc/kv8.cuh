@@ -14,6 +14,7 @@ namespace kv8 {
 constexpr int kE4M3 = OSCAR_KV8_E4M3;
 constexpr int kInt8 = OSCAR_KV8_INT8;
 constexpr int kExpLo = -100;
+constexpr int kMaxLen = 0x7fffffff - 2 * kPageSize;  // positions, rounded up to whole pages, are 32-bit numbers
 
 template <int F>
 __device__ __forceinline__ constexpr float code_max() { return F == kE4M3 ? 448.f : 127.f; }

@@ -381,7 +381,7 @@ struct Plan {
 bool make_plan(const oscar_dims_t* d, int batch, int max_seq_len, int pps, int sink, int window, Plan* p) {
   if (check_dims(d) != OSCAR_OK || batch < 0 || batch > 65535 || max_seq_len < 0 || pps < 0 || sink < 0 || window < 0)
     return false;
-  if (max_seq_len > static_cast<long long>(d->max_pages_per_seq) * kPageSize) return false;
+  if (max_seq_len > kMaxLen || max_seq_len > static_cast<long long>(d->max_pages_per_seq) * kPageSize) return false;
   if (d->num_kv_heads > 65535 || static_cast<long long>(batch) * d->num_q_heads > 0x7fffffffLL) return false;
   const long long pages = max_visible_pages(max_seq_len, sink, window, 1);
   if (pps == 0) {

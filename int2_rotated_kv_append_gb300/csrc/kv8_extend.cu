@@ -910,7 +910,9 @@ bool make_plan(const oscar_dims_t* d, int batch, int rows, int max_seq_len, int 
   if (check_dims(d) != OSCAR_OK || batch < 0 || batch > 65535 || rows < 0 || max_rows < 0 || max_seq_len < 0 ||
       pps < 0 || sink < 0 || window < 0)
     return false;
-  if (max_seq_len > static_cast<long long>(d->max_pages_per_seq) * kPageSize || d->num_kv_heads > 65535) return false;
+  if (max_seq_len > kMaxLen || max_seq_len > static_cast<long long>(d->max_pages_per_seq) * kPageSize ||
+      d->num_kv_heads > 65535)
+    return false;
   const int gqa = d->num_q_heads / d->num_kv_heads;
   if (max_rows > rows) max_rows = rows;
   const long long per_seq = static_cast<long long>(max_rows) * gqa;

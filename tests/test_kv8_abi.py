@@ -157,3 +157,12 @@ def test_append_granted_refuses_what_append_refuses(lib):
         assert call(**{n: None}) == BAD
     with pytest.raises(ValueError):
         ok.oscar_kv8_append(None, 0, 2, 1, torch.zeros(2, 8, 128), None, None, None, None, None, None, granted=torch.ones(1))
+
+
+def test_lengths_beyond_what_positions_can_count_are_refused(lib):
+    d = dims(max_pages_per_seq=1 << 27)
+    for n, fits in (((1 << 31) - 33, True), ((1 << 31) - 32, False), ((1 << 31) - 1, False)):
+        assert (lib.oscar_kv8_decode_workspace_bytes(d, 1, n, 0, 0, 64) > 0) == fits
+        assert (lib.oscar_kv8_extend_varlen_workspace_bytes(d, 1, 4, n, 4, 0, 0, 64) > 0) == fits
+    assert lib.oscar_kv8_decode(d, 0, 1, (1 << 31) - 1, 0, P, P, P, P, P, 0, 64, 0.0, P, P, 1 << 30, None) == BAD
+    assert lib.oscar_kv8_extend_varlen(d, 0, 1, 4, (1 << 31) - 1, 4, 0, P, P, P, P, P, P, 0, 64, 0.0, P, P, 1 << 30, None) == BAD
