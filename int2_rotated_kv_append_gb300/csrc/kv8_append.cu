@@ -146,7 +146,8 @@ oscar_status_t append(const oscar_dims_t* dims, int32_t kv_format, int32_t batch
   if (misaligned16(k) || misaligned16(v) || misaligned16(kv8_pages) || misaligned16(kv8_scales))
     return OSCAR_ERR_INVALID_ARG;
   const int units = 2 * dims->num_kv_heads;
-  const long long gx = (static_cast<long long>(max_tokens_per_seq) + 2 * kPageSize - 2) / kPageSize;
+  const long long most = max_tokens_per_seq < num_tokens ? max_tokens_per_seq : num_tokens;  // of one sequence
+  const long long gx = (most + 2 * kPageSize - 2) / kPageSize;
   const int gy = (units + kWarps - 1) / kWarps;
   if (gy > 65535 || batch > 65535) return OSCAR_ERR_UNSUPPORTED;
   if (static_cast<long long>(dims->max_pages_per_seq) * kPageSize > 0x7fffffffLL) return OSCAR_ERR_UNSUPPORTED;

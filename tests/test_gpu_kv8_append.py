@@ -136,3 +136,20 @@ def test_append_prompt_of_many_pages_equals_the_reference_on_a_sample():
     R.append(c.codes, c.scales, k.double().cpu().numpy(), v.double().cpu().numpy(), [0, 5000, 8001], c.table,
              [5000, 3001], R.E4M3)
     c.check()
+
+
+@pytest.mark.parametrize("most", [5, 1000, 2 ** 31 - 1])
+def test_append_with_a_bound_far_above_the_tokens(most):
+    # the grid goes by the tokens that there are
+    c = Case(2, 64, R.INT8, [40, 40], seed=10)
+    k, v = c.kv(6)
+    start, lens = torch.tensor([0, 5, 6], dtype=torch.int32, device="cuda"), torch.tensor([5, 1], dtype=torch.int32, device="cuda")
+    R.append(c.codes, c.scales, k.double().numpy(), v.double().numpy(), [0, 5, 6], c.table, [5, 1], R.INT8)
+    t0, t1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    t0.record()
+    ok.oscar_kv8_append(c.dims, R.INT8, 2, most, k.cuda(), v.cuda(), start, torch.from_numpy(c.table).cuda(), lens, c.g_codes,
+                        c.g_scales)
+    t1.record()
+    torch.cuda.synchronize()
+    c.check()
+    assert t0.elapsed_time(t1) < 100  # (2^28 empty blocks took longer)
