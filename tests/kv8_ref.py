@@ -252,3 +252,26 @@ def attention_of_rows(codes, scales, q, row_seq, row_pos, table, fmt, sink, wind
             tol[rows, h] = (2.0 ** -8 * o.abs() + 2.0 ** -133 + (own + 2.0 ** -20 + n * 2.0 ** -24 + 2 * dlog) * a * 1.01
                             + step / total * (see.double() @ vv.abs()))
     return out, tol
+
+
+def cancelling_page(D, seed):
+    """One int8 page whose values nearly cancel under the softmax of the query (1, 0, ...): (K codes of channel 0 [P], to
+    be scaled by 2^-4; V codes [P][D]; exact weights [P] at sm_scale 1/8).  Tokens come in pairs of opposite signs, the
+    second code the first times the quotient of their weights, rounded: the output is about 2^-9 of sum w |v|, so that its
+    own rounding leaves the weights' errors to be seen."""
+    g = np.random.default_rng(seed)
+    k = -g.permutation(np.arange(3, 3 + 7 * P, 7))[:P]
+    k = np.sort(k).reshape(2, P // 2).T.reshape(P)  # in each pair the first weighs less
+    w = np.exp(k * 2.0 ** -4 / 8)
+    c = g.integers(64, 128, (P // 2, D)) * g.choice([-1, 1], (P // 2, D))
+    v = np.zeros((P, D))
+    v[0::2], v[1::2] = c, -np.rint(c * (w[0::2] / w[1::2])[:, None])
+    return k, v, w
+
+
+def cancelling_tolerance(v, w):
+    """Of the decode's output over a cancelling_page: it is bf16 (2^-8 of itself); weights in two fp16 parts hold 2^-22, exponentials
+    2^-22, and their argument, one exact product, is rounded three times and subtracted from (4 2^-24 at |s| < 2), in the
+    numerator and in the sum; 16 fp32 additions each: together below 2^-22 (1 + 1 + 2 + 2 + 4 + 4) of A = sum w |v| / sum w."""
+    o, a = w @ v / w.sum(), w @ np.abs(v) / w.sum()
+    return o, 2.0 ** -8 * np.abs(o) + 14 * 2.0 ** -22 * a

@@ -154,3 +154,42 @@ def test_decode_beside_a_token_of_a_large_scale_behind_the_window():
     check(c, c.decode(q, 0, 300 - 168), q, [0], [299], 0, 300 - 168, decode=True)
     check(c, c.decode(q, 0, 300 - 168, pps=3), q, [0], [299], 0, 300 - 168, decode=True)
     check(c, c.extend(q, [1], 0, 300 - 168), q, [0], [299], 0, 300 - 168)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("gqa", [1, 5, 8])
+def test_decode_holds_weights_in_two_parts(D, gqa):
+    # (tests/test_kv8_ref.py: one part alone is outside the tolerance)
+    lens = [16] * 5
+    c = Cache(1, D, R.INT8, lens, seed=D + gqa)
+    pages = [R.cancelling_page(D, seed) for seed in range(5)]
+    for b, (k, v, _) in enumerate(pages):
+        page = c.table[b, 0].item()
+        codes = torch.zeros(2, 16, D, dtype=torch.int8)
+        codes[0, :, 0], codes[1] = torch.from_numpy(k), torch.from_numpy(v)
+        c.codes[page, 0] = codes.view(torch.uint8).cuda()
+        c.scales[page, 0] = torch.tensor([2.0 ** -4, 1.0], device="cuda")
+    q = torch.zeros(5, gqa, D, device="cuda", dtype=torch.bfloat16)
+    q[:, :, 0] = 1.0
+    out = c.decode(q, sm_scale=0.125).double().cpu().numpy()
+    for b, (k, v, w) in enumerate(pages):
+        want, tol = R.cancelling_tolerance(v, w)
+        assert (np.abs(out[b] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", [R.E4M3, R.INT8])
+@pytest.mark.parametrize("D,gqa", [(128, 4), (64, 7)])
+@pytest.mark.parametrize("pps", [0, 40])
+def test_one_chunk_beside_many_single_rows(fmt, D, gqa, pps):
+    # one varlen call of a prompt chunk and of sequences that decode, as a mixed serving step makes it
+    g = np.random.default_rng(gqa)
+    lens = [4100] + [int(n) for n in g.integers(1, 6000, 40)]
+    rows = [700] + [1] * 40
+    rows[7] = 0
+    c = Cache(2, D, fmt, lens, seed=fmt + gqa)
+    q = c.q(sum(rows), 2 * gqa)
+    seq = [b for b, r in enumerate(rows) for _ in range(r)]
+    pos = [lens[b] - r + i for b, r in enumerate(rows) for i in range(r)]
+    check(c, c.extend(q, rows, pps=pps), q, seq, pos, 0, 0)
+    check(c, c.extend(q, rows, 8, 500, pps=pps), q, seq, pos, 8, 500)
+    assert ok.oscar_device_errors(reset=True) == 0

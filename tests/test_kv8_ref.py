@@ -41,3 +41,21 @@ def test_pages_fork_then_free_gives_everything_back():
     assert granted == [1, 1] and copies == [(2, 3), (2, 4)] and m.refs[:5] == [3, 3, 1, 1, 1]
     m.free([0, 1, 2])
     assert not any(m.refs)
+
+
+def test_a_cancelling_page_shows_the_second_part_of_the_weights():
+    # the decode's weights, emulated in numpy: two fp16 parts hold the tolerance, one alone, or one mis-scaled, does not
+    for seed in range(5):
+        k, v, w = R.cancelling_page(128, seed)
+        want, tol = R.cancelling_tolerance(v, w)
+        s = (k * 2.0 ** -7 * np.log2(np.e)).astype(np.float32)
+        p = np.exp2(s - np.ceil(s.max())).astype(np.float32)
+        hi = (p * np.float32(2 ** 14)).astype(np.float16)
+        lo = ((p * np.float32(2 ** 14) - hi.astype(np.float32)) * np.float32(2 ** 12)).astype(np.float16)
+
+        def out(second):
+            o = ((hi.astype(np.float64) + second * lo.astype(np.float64)) / 2 ** 14) @ v / p.astype(np.float64).sum()
+            return torch.from_numpy(o).bfloat16().double().numpy()
+        assert (np.abs(out(2.0 ** -12) - want) <= tol).all()
+        for planted in (0.0, 2.0 ** -11, 2.0 ** -14):
+            assert (np.abs(out(planted) - want) > tol).sum() > 30, planted
