@@ -581,6 +581,11 @@ oscar_status_t oscar_kv8_extend_varlen(const oscar_dims_t* dims, int32_t kv_form
  * Free pages are handed out lowest id first, in the order of the requests, so results do not
  * depend on timing.  A page is written by one sequence only as long as a partial last page is
  * never shared: oscar_pages_fork copies it.
+ * Lengths are the caller's to lower within the last page only (rejected drafts that began in it): entries behind a length are
+ * not held any more, but their pages still count.  To give them back, lower seq_lens[b] to the new length L', fork b to an
+ * empty sequence, restore seq_lens[b] and free b: the pages of L' are then the other sequence's.
+ * Layers that share one page table are forked or compacted together, up to OSCAR_MAX_POOLS pools; a model of more pools has a
+ * table for each group of layers.
  * Lengths outside [0, max_pages_per_seq * P] and sequence ids outside [0, batch) skip that
  * request and flag OSCAR_DEVERR_POSITION; page ids out of range, and a release of a page that
  * is free already, are skipped and flag OSCAR_DEVERR_PAGE_ID.

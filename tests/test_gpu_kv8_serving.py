@@ -179,3 +179,21 @@ def test_a_tight_length_bound_gives_the_same_rows():
         ref, tol = R.attention(c.pages, c.scales, qx, [0] * 40 + [1] * 10, pos, c.page_table.tolist(), c.kv_format, 0, 0)
         assert ((c.extend(qx, start, 40, max_seq_len=bound).double() - ref).abs() <= tol).all()
     assert ok.oscar_device_errors(reset=True) == 0
+
+
+@pytest.mark.parametrize("kept", [100, 96, 81, 80, 1])
+def test_rejected_drafts_are_given_back_through_a_fork(kept):
+    # 100 tokens, of which `kept` stay: the length is lowered, the sequence forked, the old one freed at its full length
+    s = Server(num_q_heads=4, num_kv_heads=1, head_dim=64, num_pages=20, batch=3, max_seq_len=320, kv_format=R.INT8)
+    c = s.c
+    s.add([100, 30, 0])
+    c.seq_lens[0] = kept
+    c.fork(i32([0]), i32([2]), granted=c.granted)
+    assert c.granted[0].item() == 1
+    c.seq_lens[0] = 100
+    c.free(i32([0]))
+    assert c.seq_lens.tolist() == [0, 30, kept] and c.page_refs.sum().item() == -(-kept // 16) + 2
+    assert c.page_refs.max().item() == 1
+    s.check([0, 1, 1])
+    s.add([0, 1, 40])
+    s.check([0, 1, 7])
