@@ -74,11 +74,12 @@ __device__ __forceinline__ void pow2_pair(float e, float& f, float& g) {
   g = fast_exp2(e - h);
 }
 
-// Numerator and denominator of a row have a unit each: o counts 2^t (weights times V scales: t near the largest of
-// these products) and l counts 2^m (weights alone).  With one unit for both, values near either end of the scales' range
-// would leave fp32.  Two units t may be further apart than a float's exponents reach: o goes from one to another by a pair.
+// Numerator and denominator of a row have a unit each: l counts 2^m (weights alone) and o counts 2^(m + r) (weights times V
+// scales: near the largest of these products).  With one unit for both, values near either end of the scales' range would
+// leave fp32; r is kept, not m + r, which rounds where logits are large.  Two units may be further apart than a float's exponents
+// reach: o goes from one to another by a pair.
 
-// Four channels of an output row: o 2^t / (l 2^m) with e = t - m, 0 where nothing was attended (a NaN of the query stays one).
+// Four channels of an output row: 2^e o / l, e the unit r; 0 where nothing was attended (a NaN of the query stays one).
 __device__ __forceinline__ void store_out4(__nv_bfloat16* out, float4 o, float l, float e) {
   float f, g;
   pow2_pair(e, f, g);
@@ -89,9 +90,9 @@ __device__ __forceinline__ void store_out4(__nv_bfloat16* out, float4 o, float l
       make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
-// One warp: partials first, first + step, ... of n (o [n][D] unnormalised, ml [n][4] = m, l, t, -; -infinity for the units of a
-// partial of nothing): l and four channels r of lane's c4 = lane % (D / 4), in units of the largest m and t of all n,
-// whose difference is e.  Eight partials are in flight at once, the first of them while the maxima are found.
+// One warp: partials first, first + step, ... of n (o [n][D] unnormalised, ml [n][4] = m, l, r, -; -infinity for the units of a
+// partial of nothing): l and four channels r of lane's c4 = lane % (D / 4), in units of the largest m and m + r of all n, the
+// latter e above the former.  Eight partials are in flight at once, the first of them while the maxima are found.
 template <int D>
 __device__ __forceinline__ void merge_part(const float* o, const float* ml, int n, int first, int step, int lane,
                                            float& l, float4& r, float& e) {
@@ -114,25 +115,31 @@ __device__ __forceinline__ void merge_part(const float* o, const float* ml, int 
   };
   int i0 = first * kSub + sub;
   load(i0);
-  float M = -INFINITY, T = -INFINITY;
+  float M = -INFINITY, R = -INFINITY;  // a lane's own, then all lanes'
   for (int i = lane; i < n; i += 32) {
     const float4 v = *reinterpret_cast<const float4*>(ml + 4 * i);
-    M = fmaxf(M, v.x);
-    T = fmaxf(T, v.z);
+    if (v.x > -INFINITY) {
+      const float m = fmaxf(M, v.x);
+      R = fmaxf(R + (M - m), v.z + (v.x - m));
+      M = m;
+    }
   }
 #pragma unroll
   for (int off = 16; off; off >>= 1) {
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    T = fmaxf(T, __shfl_xor_sync(0xffffffffu, T, off));
+    const float m2 = __shfl_xor_sync(0xffffffffu, M, off), r2 = __shfl_xor_sync(0xffffffffu, R, off);
+    const float m = fmaxf(M, m2);
+    if (m > -INFINITY) R = fmaxf(R + (M - m), r2 + (m2 - m));
+    M = m;
   }
-  e = T - M;
-  const float base = M == -INFINITY ? 0.f : M, base_t = T == -INFINITY ? 0.f : T;
+  e = R;
+  const float base = M == -INFINITY ? 0.f : M, base_r = R == -INFINITY ? 0.f : R;
   while (true) {
 #pragma unroll
     for (int k = 0; k < kFly; ++k) {
-      l = fmaf(fast_exp2(p[k].x - base), p[k].y, l);  // (a factor of 0 for a partial of nothing)
+      const float d = p[k].x - base;
+      l = fmaf(fast_exp2(d), p[k].y, l);  // (a factor of 0 for a partial of nothing)
       float f, g;
-      pow2_pair(p[k].z - base_t, f, g);
+      pow2_pair(d + p[k].z - base_r, f, g);
       r.x = fmaf(f, x[k].x * g, r.x); r.y = fmaf(f, x[k].y * g, r.y);
       r.z = fmaf(f, x[k].z * g, r.z); r.w = fmaf(f, x[k].w * g, r.w);
     }

@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
     if (pid_s[k] >= 0) {
       const uint32_t st = my_ring + (i % kStages) * kPage;
       const float2 sc = scale_s[k];
+      const float k_scale = sc.x * qs;  // (first: a logit may be within fp32 where its product with one of them is not)
       const int pos0 = vis.page(v0 + k) * kPageSize;
       float acc[2][2][4];  // two chains of products per eight tokens
 #pragma unroll
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
       const bool full = pos0 + kPageSize <= vis.end && (pos0 + kPageSize <= vis.sink_end || pos0 >= vis.lo);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        sx[c] = sx[c] * sc.x * qs;
+        sx[c] *= k_scale;
         if (!full && !vis.sees(pos0 + 2 * t + (c & 1) + 8 * (c >> 1))) sx[c] = -INFINITY;
       }
       float mp = fmaxf(fmaxf(sx[0], sx[1]), fmaxf(sx[2], sx[3]));
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
     } else {
       const size_t part = row * sa.ns + s;
       *reinterpret_cast<float4*>(sa.part_o + part * D + 4 * c4) = r;
-      if (c4 == 0) *reinterpret_cast<float4*>(sa.part_ml + part * 4) = make_float4(M, l, M + unit, 0.f);
+      if (c4 == 0) *reinterpret_cast<float4*>(sa.part_ml + part * 4) = make_float4(M, l, M == -INFINITY ? M : unit, 0.f);
     }
   }
 }

@@ -19,16 +19,16 @@
 // buffer (64) and an accumulator (D) per row tile.  With MT = 1 two logit buffers alternate, and Q is the products'
 // left side from TMEM, so that at D = 128 its place in shared memory becomes a third stage of codes.
 // Q is scaled per row by a power of two to below 2, where fp16 holds it to 2^-25 of the row's largest element; a page's K
-// scale multiplies its 16 logits.  V scales 2^v go into the weights: the operand is 2^(s + v - t + 3) where t, the row's own,
-// is at least the largest s + v that the row sees less 12, by which it may be passed before it moves; the sum has
-// 2^(s - m), m likewise for s alone.  What the mask hides from a row has no part in its m and t (but that a page has one v).
-// m and t are whole numbers: every factor between units is exact.  O is rescaled in TMEM when t moves.  Sums are fp32
+// scale multiplies its 16 logits.  V scales 2^v go into the weights: the operand is 2^(s - m + v - r + 3) where m + r, the row's
+// own, is at least the largest s + v that the row sees less 12, by which it may be passed before it moves; the sum has
+// 2^(s - m), m likewise for s alone.  What the mask hides from a row has no part in its m and r (but that a page has one v).
+// m and r are whole numbers: every factor between units is exact.  O is rescaled in TMEM when r moves.  Sums are fp32
 // over the unrounded weights.
 // As long as the largest V scale so far is at most 2^kTame times a block's smallest, weights are fp16 (11 bits: a tenth of the output's
 // own rounding) with the block's largest v, and the codes carry the ratio of their page's scale to it (exact).  Then,
-// whatever other tokens of its pages make of a row's t, a weight's smallest step is 2^-22 of the row's largest.  In other
+// whatever other tokens of its pages make of a row's r, a weight's smallest step is 2^-22 of the row's largest.  In other
 // blocks ("wild": an infinite V element that was saturated, say) each page has its own v in the weights and the operands are
-// bf16, weights (8 bits) and codes (exact) alike, with fp32's range of exponents: there t may stay kWildUp lower, so
+// bf16, weights (8 bits) and codes (exact) alike, with fp32's range of exponents: there r may stay kWildUp lower, so
 // that a page whose scale comes from a token hidden from the row takes no bits from the row's other pages.
 //
 // Measured (GB300, 2070 MHz): 8192 rows over 16384 positions, 32 query heads, 8 KV heads, D = 128, e4m3: 1.20 ms,
@@ -61,9 +61,9 @@ constexpr float kLazy = 12.f;
 constexpr int kBoost = 3;         // weights are stored times 2^kBoost: 2^(kLazy + kBoost) < 65504
 constexpr float kTame = 4.f;      // log2
 constexpr float kWildUp = 76.f;   // 2^(kWildUp + kLazy + kBoost) times a code (2^9) times 2^27 tokens is within fp32
-// Bounds of lb (below) for blocks that are not wild: under kLbLo there are only scales of 0, above kLbHi logits more than
-// 2^100 below the largest
+// Bounds of lb (below) for blocks that are not wild: under kLbLo there are only scales of 0, above kLbHi weights under 2^-100
 constexpr float kLbLo = -100.f, kLbHi = 126.f;
+constexpr float kFar = 1048576.f;  // logits above this: sums with them lose what is small beside them
 constexpr int kQkWarp = 12, kFetchK = 13, kPvWarp = 14, kFetchV = 15;
 // Registers a thread: 512 x 128 at launch, divided among the warpgroups by setmaxnreg
 constexpr int kRegsLaunch = 128;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
         umma::tmem_st32(p_tmem[0] + t_lane + (part ^ 1) * (kCols / 2), z);
         umma::tmem_st_wait();
       }
-      float m = -INFINITY, l = 0.f, mt = -INFINITY;
+      float m = -INFINITY, l = 0.f, r_unit = -INFINITY;
       bool ok = true;
       for (int j = 0; j < cnt; ++j) {
         const int sbuf = MT == 2 ? wg : j & 1;  // barrier and buffer of the logits
@@ -368,25 +368,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           return low_bits(pos - pp + 1) & (~low_bits(after - pp + 1) | low_bits(a.sink - pp));
         };
         auto k_scale = [&](float k) { return fmaxf(k * qs, 1.2e-38f); };  // (never 0: -inf stays -inf)
-        // The largest logit and product of the block, once seen: m, t and what they count move where they have to.
-        auto settle = [&](float mx, float tx) {
+        // mx: the block's largest logit; vx: the largest of logit - mx + v.  m, r and what they count move where they have to.
+        auto settle = [&](float mx, float vx) {
           // The product before is over: its weights' columns and O are free.  (Every phase of this barrier is waited
           // for in its turn: a parity says nothing two phases ahead.)
           if (j > 0) {
             ok = mbar_wait_bounded(bar(kPvDone + (MT == 2 ? wg : 0)), (j - 1) & 1);
             umma::fence_after_sync();
           }
-          const bool move = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
-          const bool t_move = tx > mt + kLazy || (mt == -INFINITY && tx > -INFINITY);
-          if (move) {
+          if (mx > m + kLazy || (m == -INFINITY && mx > -INFINITY)) {
             const float m_new = ceilf(mx);
             l *= fast_exp2(m - m_new);
+            r_unit += m - m_new;
             m = m_new;
           }
-          if (__any_sync(0xffffffffu, t_move)) {
-            const float t_new = t_move ? ceilf(tx) : mt;
-            float gap = j > 0 ? fmaxf(mt - t_new, -240.f) : 0.f;  // (below: 0 in the end)
-            mt = t_new;
+          const float top = mx == -INFINITY ? mx : mx - m + vx;
+          const bool r_move = top > r_unit + kLazy || (r_unit == -INFINITY && top > -INFINITY);
+          if (__any_sync(0xffffffffu, r_move)) {
+            const float r_new = r_move ? ceilf(top) : r_unit;
+            float gap = j > 0 && r_move ? fmaxf(r_unit - r_new, -240.f) : 0.f;  // (below: 0 in the end)
+            r_unit = r_new;
             while (__any_sync(0xffffffffu, gap < 0.f)) {  // by up to 2^-120 at a time
               const float alpha = fast_exp2(fmaxf(gap, -120.f));
               gap = fminf(gap + 120.f, 0.f);
@@ -434,10 +435,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
             y = fmaxf(y, __uint_as_float(x[15]));
             mx = fmaxf(mx, y * ks[pg]);
           }
-          settle(mx, mx + v_top);
-          // weights 2^(s - m + lb), lb = v - t + m + kBoost; the sum takes the 2^lb out again
-          const float lb = fminf(fmaxf(v_top + (mt == -INFINITY ? 0.f : kBoost - mt + m), kLbLo), kLbHi);
-          const float off = lb - (m == -INFINITY ? 0.f : m);
+          settle(mx, v_top);
+          // weights 2^(s - m + lb), lb = v - r + kBoost; the sum takes the 2^lb out again
+          const float lb = fminf(fmaxf(v_top + (r_unit == -INFINITY ? 0.f : kBoost - r_unit), kLbLo), kLbHi);
+          float off = lb - (m == -INFINITY ? 0.f : m);
+          const bool far = fabsf(m) > kFar && m > -INFINITY;
+          // rare: m is taken away before anything smaller is added, from the rounded product that m came from (packed products
+          // and sums get fused by the assembler)
+          if (__any_sync(0xffffffffu, far)) {
+            const float m_far = far ? m : 0.f;
+#pragma unroll
+            for (int pg = 0; pg < kPages; ++pg) {
+              const float k = far ? ks[pg] : 1.f;
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                uint32_t& x = v[pg >> 1][(pg & 1) * 16 + c];
+                x = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(x), k), m_far));
+              }
+              if (far) ks[pg] = 1.f;
+            }
+            if (far) off = lb;
+          }
           const float2 off2 = make_float2(off, off);
           float2 sum[4];  // four chains of additions
 #pragma unroll
@@ -465,11 +483,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           l = fmaf(sum[0].x + sum[0].y, pow2_neg(lb), l);
         } else {
           // Rare: a page at a time, once for the largest and once for the weights (little code, for the instruction cache).
-          float mx = -INFINITY, tx = -INFINITY;
+          float mx = -INFINITY, vx = -INFINITY;
 #pragma unroll 1
           for (int pg = 0; pg < 2 * kPages; ++pg) {
             const int at = pg % kPages;
-            if (pg == kPages) settle(mx, tx - kWildUp);
+            if (pg == kPages) settle(mx, vx - kWildUp);
             uint32_t x[16];
             __syncwarp();
             umma::tmem_ld16(s_tmem[sbuf] + t_lane + part * kCols + 16 * at, x);
@@ -483,18 +501,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
               float y = -INFINITY;
 #pragma unroll
               for (int c = 0; c < 16; ++c) y = fmaxf(y, __uint_as_float(x[c]));
-              mx = fmaxf(mx, y * k);
-              tx = fmaxf(tx, fmaf(y, k, v));
+              y *= k;
+              if (y > -INFINITY) {
+                const float m_all = fmaxf(mx, y);
+                vx = fmaxf(vx + (mx - m_all), v + (y - m_all));
+                mx = m_all;
+              }
             } else {
               // (for the products and for the sum: their units may be further apart than a float's exponents reach)
-              const float off = kBoost + v - (mt == -INFINITY ? 0.f : mt), off_l = m == -INFINITY ? 0.f : -m;
+              const float off = v + (r_unit == -INFINITY ? 0.f : kBoost - r_unit), m_use = m == -INFINITY ? 0.f : m;
               float sum = 0.f;
               uint32_t p[8];
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
-                const float x0 = __uint_as_float(x[2 * c]), x1 = __uint_as_float(x[2 * c + 1]);
-                sum += fast_exp2(fmaf(x0, k, off_l)) + fast_exp2(fmaf(x1, k, off_l));
-                p[c] = bfloat2_bits(fast_exp2(fmaf(x0, k, off)), fast_exp2(fmaf(x1, k, off)));
+                const float x0 = __fmul_rn(__uint_as_float(x[2 * c]), k) - m_use;
+                const float x1 = __fmul_rn(__uint_as_float(x[2 * c + 1]), k) - m_use;
+                sum += fast_exp2(x0) + fast_exp2(x1);
+                p[c] = bfloat2_bits(fast_exp2(x0 + off), fast_exp2(x1 + off));
               }
               l += sum;
               umma::tmem_st8(p_tmem[wg] + t_lane + part * (kCols / 2) + 8 * at, p);
@@ -514,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       const bool single = T.blocks <= ea.bps;
       const bool store = r < T.rows;
       const size_t row = store ? out_row(r) : 0;
-      float t = mt - kBoost;  // log2 of what the accumulators count
+      float u = r_unit - kBoost;  // the accumulators count 2^(m + u)
       if (!ok) l = 0.f;
       float u0 = 1.f, u1 = 1.f, v0 = 0.f, v1 = 0.f;  // the parts' accumulators to the merged ones' unit; which saw nothing
       bool none0 = false, none1 = false;
@@ -536,21 +559,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
             *reinterpret_cast<uint4*>(mine + 16 * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
         none0 = l == 0.f;
-        if (none0) m = t = -INFINITY;
-        *reinterpret_cast<float4*>(mine + D / 2) = make_float4(m, l, t, 0.f);
+        if (none0) m = u = -INFINITY;
+        *reinterpret_cast<float4*>(mine + D / 2) = make_float4(m, l, u, 0.f);
         asm volatile("bar.sync 2, 128;" ::: "memory");
         const float4 x = *reinterpret_cast<const float4*>(theirs + D / 2);
         none1 = x.y == 0.f;
         const float top = fmaxf(m, x.x), base = top == -INFINITY ? 0.f : top;
-        const float top_t = fmaxf(t, x.z), base_t = top_t == -INFINITY ? 0.f : top_t;
+        const float t0 = m - base + u, t1 = x.x - base + x.z, top_t = fmaxf(t0, t1), base_t = top_t == -INFINITY ? 0.f : top_t;
         l = (none0 ? 0.f : l * fast_exp2(m - base)) + (none1 ? 0.f : x.y * fast_exp2(x.x - base));
-        pow2_pair(t - base_t, u0, u1);
-        pow2_pair(x.z - base_t, v0, v1);
+        pow2_pair(t0 - base_t, u0, u1);
+        pow2_pair(t1 - base_t, v0, v1);
         m = top;
-        t = top_t;
+        u = top_t;
       }
       float f, g;
-      pow2_pair(t - m, f, g);
+      pow2_pair(u, f, g);
       const float inv = l == 0.f ? 0.f : f / l;
 #pragma unroll 2
       for (int c = part * (D / 32); c < (PARTS == 2 ? (part + 1) * (D / 32) : D / 16); ++c) {
@@ -584,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
       }
       if (store && !single && part == 0)
         *reinterpret_cast<float4*>(ea.part_ml + (row * ea.ns + split) * 4) =
-            l == 0.f ? make_float4(-INFINITY, 0.f, -INFINITY, 0.f) : make_float4(m, l, t, 0.f);
+            l == 0.f ? make_float4(-INFINITY, 0.f, -INFINITY, 0.f) : make_float4(m, l, u, 0.f);
     }
   } else if (wg < 3) {
     // ---- codes -> fp16 operands: K and V in turn (MT = 2), V or K (MT = 1: warpgroups 1 and 2) ------------

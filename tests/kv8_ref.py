@@ -213,7 +213,8 @@ def attention_of_rows(codes, scales, q, row_seq, row_pos, table, fmt, sink, wind
     the largest logit.
 
     Both: the output is bf16 (half a step, 2^-8 of itself; 2^-133 where bf16 is subnormal), logits are fp32 sums of D
-    exact products and three fp32 roundings, (D + 16) 2^-24 of sum |q k|, once in the numerator and once in the sum;
+    exact products and three fp32 roundings, (D + 16) 2^-24 of sum |q k|, once in the numerator and once in the sum (of the
+    positions that have a weight in 64 bits; a row's only one has the weight 1 whatever its logit is);
     exponentials and fp32 sums over n positions: 2^-20 + n 2^-24 of A.
 
     Decode: weights in two fp16 parts hold 2^-22 of themselves and at worst 2^-50 of the largest.
@@ -245,7 +246,8 @@ def attention_of_rows(codes, scales, q, row_seq, row_pos, table, fmt, sink, wind
             w = torch.exp(s - s.amax(1, keepdim=True))
             total = w.sum(1, keepdim=True)
             w = w / total
-            dlog = (D + 16) * 2.0 ** -24 * (qq.abs() @ kk.abs().T / math.sqrt(D)).masked_fill(~see, 0).amax(1, keepdim=True)
+            size = (qq.abs() @ kk.abs().T / math.sqrt(D)).masked_fill(w == 0, 0)
+            dlog = (D + 16) * 2.0 ** -24 * size.amax(1, keepdim=True) * ((w > 0).sum(1, keepdim=True) > 1)
             o, a = w @ vv, w @ vv.abs()
             own, step = (2.0 ** -22, 2.0 ** -50) if decode else (2.0 ** -8, 2.0 ** -23)
             out[rows, h] = o

@@ -193,3 +193,26 @@ def test_one_chunk_beside_many_single_rows(fmt, D, gqa, pps):
     check(c, c.extend(q, rows, pps=pps), q, seq, pos, 0, 0)
     check(c, c.extend(q, rows, 8, 500, pps=pps), q, seq, pos, 8, 500)
     assert ok.oscar_device_errors(reset=True) == 0
+
+
+@pytest.mark.parametrize("fmt", [R.E4M3, R.INT8])
+@pytest.mark.parametrize("at", [[300], [20, 21], [599, 130, 131]])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_infinite_keys_take_or_lose_all_the_weight(fmt, at, sign):
+    # saturated, their logits are around 1e37: finite, and far beyond where a float tells neighbours apart
+    H, D, L = 2, 128, 600
+    c = Cache(H, D, fmt, [L], seed=fmt + len(at) + 50)
+    k, v = (torch.randn(L, H, D, device="cuda", generator=c.g).bfloat16() for _ in range(2))
+    for i, t in enumerate(at):
+        k[t, :, 5 + i % 2] = sign * float("inf")
+    start = torch.tensor([0, L], dtype=torch.int32, device="cuda")
+    ok.oscar_kv8_append(c.dims(2 * H), fmt, 1, L, k, v, start, c.table_d, c.lens_d, c.codes, c.scales)
+    for rows in (600, 50, 1):
+        q = c.q(rows, 2 * H, 0.5)
+        q[:, :, 5] = q[:, :, 5].abs().clamp(max=1.0) + 0.25
+        q[:, :, 6] = 2 * q[:, :, 5]  # no two such keys have the same logit
+        pos = list(range(L - rows, L))
+        for pps, window in ((0, 0), (8, 0), (0, 100), (8, 100)):
+            check(c, c.extend(q, [rows], 0, window, pps=pps), q, [0] * rows, pos, 0, window)
+            if rows == 1:
+                check(c, c.decode(q, 0, window, pps=pps // 2), q, [0], pos, 0, window, decode=True)
