@@ -24,12 +24,13 @@
 // 2^(s - m), m likewise for s alone.  What the mask hides from a row has no part in its m and r (but that a page has one v).
 // m and r are whole numbers: every factor between units is exact.  O is rescaled in TMEM when r moves.  Sums are fp32
 // over the unrounded weights.
-// As long as the largest V scale so far is at most 2^kTame times a block's smallest, weights are fp16 (11 bits: a tenth of the output's
-// own rounding) with the block's largest v, and the codes carry the ratio of their page's scale to it (exact).  Then,
-// whatever other tokens of its pages make of a row's r, a weight's smallest step is 2^-22 of the row's largest.  In other
-// blocks ("wild": an infinite V element that was saturated, say) each page has its own v in the weights and the operands are
-// bf16, weights (8 bits) and codes (exact) alike, with fp32's range of exponents: there r may stay kWildUp lower, so
-// that a page whose scale comes from a token hidden from the row takes no bits from the row's other pages.
+// As long as the largest V scale so far is at most 2^kTame times a block's smallest, weights are fp16 (11 bits: a tenth of the
+// output's own rounding) with the block's largest v, and the codes carry the ratio of their page's scale to it (exact).
+// Then, whatever other tokens of its pages make of a row's r, a weight's smallest step is 2^-18 of the row's largest (2^-26
+// where V scales are alike).  In other blocks ("wild": an infinite V element that was saturated, say) each page has its own v
+// in the weights and the operands are bf16, weights (8 bits) and codes (exact) alike, with fp32's range of exponents:
+// there r may stay kWildUp lower, so that a page whose scale comes from a token hidden from the row takes no bits from the
+// row's other pages.
 //
 // Measured (GB300, 2070 MHz): 8192 rows over 16384 positions, 32 query heads, 8 KV heads, D = 128, e4m3: 1.20 ms,
 // 1370 TFLOP/s, 71% of a cuBLAS bf16 product's rate.  A block takes 3300 clocks where the products alone would
@@ -59,7 +60,7 @@ static_assert(kInfo % 2 == 0, "two warps take turns");
 // rescale took 550 of 3400 clocks)
 constexpr float kLazy = 12.f;
 constexpr int kBoost = 3;         // weights are stored times 2^kBoost: 2^(kLazy + kBoost) < 65504
-constexpr float kTame = 4.f;      // log2
+constexpr float kTame = 8.f;      // log2 (the rare path takes 2 to 5 times as long: with 4, V scales that differ by 2^6 took it)
 constexpr float kWildUp = 76.f;   // 2^(kWildUp + kLazy + kBoost) times a code (2^9) times 2^27 tokens is within fp32
 // Bounds of lb (below) for blocks that are not wild: under kLbLo there are only scales of 0, above kLbHi weights under 2^-100
 constexpr float kLbLo = -100.f, kLbHi = 126.f;

@@ -32,6 +32,7 @@ PATTERNS = {
     "every seventh": lambda n: np.where(np.arange(n) % 7 == 3, 26, 0),
     "rising": lambda n: np.linspace(0, 40, n).round(),
     "falling": lambda n: np.linspace(10, -30, n).round(),
+    "within 2^7": lambda n: np.random.default_rng(n).integers(0, 7, n),
     "any": lambda n: np.random.default_rng(n).integers(-60, 60, n),
     "large at both ends": lambda n: np.where((np.arange(n) == 0) | (np.arange(n) == n - 1), 30, 0),
 }
