@@ -317,9 +317,10 @@ __device__ __forceinline__ int used_mask(const int32_t* refs, int i0, int num_pa
   return f;
 }
 
-// Pools of up to kOwnChunks chunks: every planning block counts them all itself (a small pool's call 8.0 -> 7.3 us);
-// with more, a counting kernel before it is quicker (13 chunks: 139 against 142 us).
-constexpr int kOwnChunks = 4;
+// Pools of up to kOwnChunks chunks: every planning block counts them all itself; with more, a counting kernel before it is
+// quicker (nothing to move, one against two kernels: 2 chunks 5.9 and 6.9 us, 4: 7.5 and 8.3, 6: 8.6 and 9.0, 8: 10.0 and 9.7,
+// 13: 13.0 and 11.5).
+constexpr int kOwnChunks = 6;
 
 // Pages in use per chunk of kChunk counts.
 __global__ void __launch_bounds__(kPlanThreads) compact_count_kernel(const int32_t* refs, int num_pages,

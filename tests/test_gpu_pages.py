@@ -223,3 +223,19 @@ def test_free_pages_far_into_a_full_pool():
     ok.oscar_pages_reserve(dims, i32([1, 17, 1]), table, lens, refs, granted, ws)
     assert table[:, :2].tolist() == [[17, -1], [40000, 49999], [-1, -1]] and granted.tolist() == [1, 1, 0]
     assert ok.oscar_device_errors(reset=True) == ok.OSCAR_DEVERR_NO_PAGES
+
+
+@pytest.mark.parametrize("chunks", [1, 4, 6, 7, 9])
+@pytest.mark.parametrize("more", [-1, 0, 1, 5])
+def test_compact_around_whole_chunks_of_the_count(chunks, more):
+    n = 4096 * chunks + more
+    b = Both(n, 5, n // 4 + 2, pools=pools(n, seed=chunks))
+    b.reserve([16 * (n // 5), 16 * (n // 6) + 3, 40, 16 * (n // 5), 16 * (n // 5)])
+    b.compact()  # nothing moves
+    b.free([0, 2])
+    b.compact()
+    b.free([3])
+    b.fork([1], [0])
+    b.compact()
+    b.reserve([1, 1, 17, 0, 0])
+    b.compact()
