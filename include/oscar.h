@@ -547,7 +547,7 @@ oscar_status_t oscar_kv8_decode(const oscar_dims_t* dims, int32_t kv_format, int
  *   q_start           device int32 [batch + 1], non-decreasing, q_start[0] = 0
  * A row's result depends on the positions that it sees alone: V scales of other pages, or set by other tokens of its
  * pages, cost it nothing down to 2^-200 of the largest weight times scale among its pages.  Weights are held in 11 bits, with
- * a step of 2^-18 of the row's largest or less, or in 8 bits where the V scales of pages are more than 2^8 apart (which takes
+ * a step of 2^-20 of the row's largest or less, or in 8 bits where the V scales of pages are more than 2^8 apart (which takes
  * 2 to 5 times as long); the output has 8.
  * Rows that outnumber their sequence's tokens (n_b > L) have no position: they give zeros and
  * flag OSCAR_DEVERR_POSITION.  A q_start that decreases, leaves [0, num_rows] or makes n_b larger

@@ -19,14 +19,14 @@
 // buffer (64) and an accumulator (D) per row tile.  With MT = 1 two logit buffers alternate, and Q is the products'
 // left side from TMEM, so that at D = 128 its place in shared memory becomes a third stage of codes.
 // Q is scaled per row by a power of two to below 2, where fp16 holds it to 2^-25 of the row's largest element; a page's K
-// scale multiplies its 16 logits.  V scales 2^v go into the weights: the operand is 2^(s - m + v - r + 3) where m + r, the row's
+// scale multiplies its 16 logits.  V scales 2^v go into the weights: the operand is 2^(s - m + v - r + 4) where m + r, the row's
 // own, is at least the largest s + v that the row sees less 12, by which it may be passed before it moves; the sum has
 // 2^(s - m), m likewise for s alone.  What the mask hides from a row has no part in its m and r (but that a page has one v).
-// m and r are whole numbers: every factor between units is exact.  O is rescaled in TMEM when r moves.  Sums are fp32
-// over the unrounded weights.
+// The weight of a row's largest logit is a power of two, which costs it no rounding.  O is rescaled in TMEM when r moves.
+// Sums are fp32 over the unrounded weights.
 // As long as the largest V scale so far is at most 2^kTame times a block's smallest, weights are fp16 (11 bits: a tenth of the
 // output's own rounding) with the block's largest v, and the codes carry the ratio of their page's scale to it (exact).
-// Then, whatever other tokens of its pages make of a row's r, a weight's smallest step is 2^-18 of the row's largest (2^-26
+// Then, whatever other tokens of its pages make of a row's r, a weight's smallest step is 2^-20 of the row's largest (2^-28
 // where V scales are alike).  In other blocks ("wild": an infinite V element that was saturated, say) each page has its own v
 // in the weights and the operands are bf16, weights (8 bits) and codes (exact) alike, with fp32's range of exponents:
 // there r may stay kWildUp lower, so that a page whose scale comes from a token hidden from the row takes no bits from the
@@ -58,8 +58,8 @@ constexpr int kInfo = 6;          // blocks whose scales and positions are kept
 static_assert(kInfo % 2 == 0, "two warps take turns");
 // log2: how far a logit may pass the maximum in use (with 8, some row of a warp passed it in most blocks, and the
 // rescale took 550 of 3400 clocks)
-constexpr float kLazy = 12.f;
-constexpr int kBoost = 3;         // weights are stored times 2^kBoost: 2^(kLazy + kBoost) < 65504
+constexpr float kLazy = 11.9f;
+constexpr int kBoost = 4;         // weights are stored times 2^kBoost: 2^(kLazy + kBoost) < 65504
 constexpr float kTame = 8.f;      // log2 (the rare path takes 2 to 5 times as long: with 4, V scales that differ by 2^6 took it)
 constexpr float kWildUp = 76.f;   // 2^(kWildUp + kLazy + kBoost) times a code (2^9) times 2^27 tokens is within fp32
 // Bounds of lb (below) for blocks that are not wild: under kLbLo there are only scales of 0, above kLbHi weights under 2^-100
@@ -175,11 +175,6 @@ __device__ __forceinline__ uint32_t half2_bits(float x, float y) {
 __device__ __forceinline__ uint32_t bfloat2_bits(float x, float y) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// 2^-x for a whole number x, |x| <= 126: x is in the low bits of x + 1.5 2^23.
-__device__ __forceinline__ float pow2_neg(float x) {
-  return __uint_as_float(0x3f800000u - (__float_as_uint(x + 12582912.f) << 23));
 }
 
 // The lowest n of 16 bits (n < 0: none).
@@ -378,17 +373,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
             umma::fence_after_sync();
           }
           if (mx > m + kLazy || (m == -INFINITY && mx > -INFINITY)) {
-            const float m_new = ceilf(mx);
-            l *= fast_exp2(m - m_new);
-            r_unit += m - m_new;
-            m = m_new;
+            l *= fast_exp2(m - mx);
+            r_unit += m - mx;
+            m = mx;
           }
           const float top = mx == -INFINITY ? mx : mx - m + vx;
           const bool r_move = top > r_unit + kLazy || (r_unit == -INFINITY && top > -INFINITY);
           if (__any_sync(0xffffffffu, r_move)) {
-            const float r_new = r_move ? ceilf(top) : r_unit;
-            float gap = j > 0 && r_move ? fmaxf(r_unit - r_new, -240.f) : 0.f;  // (below: 0 in the end)
-            r_unit = r_new;
+            float gap = j > 0 && r_move ? fmaxf(r_unit - top, -240.f) : 0.f;  // (below: 0 in the end)
+            if (r_move) r_unit = top;
             while (__any_sync(0xffffffffu, gap < 0.f)) {  // by up to 2^-120 at a time
               const float alpha = fast_exp2(fmaxf(gap, -120.f));
               gap = fminf(gap + 120.f, 0.f);
@@ -441,17 +434,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           const float lb = fminf(fmaxf(v_top + (r_unit == -INFINITY ? 0.f : kBoost - r_unit), kLbLo), kLbHi);
           float off = lb - (m == -INFINITY ? 0.f : m);
           const bool far = fabsf(m) > kFar && m > -INFINITY;
-          // rare: m is taken away before anything smaller is added, from the rounded product that m came from (packed products
-          // and sums get fused by the assembler)
+          // rare: m is taken away before anything smaller is added, from the rounded product that m came from (a packed
+          // subtraction would be fused with the packed product)
           if (__any_sync(0xffffffffu, far)) {
             const float m_far = far ? m : 0.f;
 #pragma unroll
             for (int pg = 0; pg < kPages; ++pg) {
               const float k = far ? ks[pg] : 1.f;
 #pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                uint32_t& x = v[pg >> 1][(pg & 1) * 16 + c];
-                x = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(x), k), m_far));
+              for (int c = 0; c < 16; c += 2) {
+                uint32_t* x = &v[pg >> 1][(pg & 1) * 16 + c];
+                const float2 y = f2mul(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(k, k));
+                x[0] = __float_as_uint(__fsub_rn(y.x, m_far));
+                x[1] = __float_as_uint(__fsub_rn(y.y, m_far));
               }
               if (far) ks[pg] = 1.f;
             }
@@ -481,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           umma::fence_before_sync();
           mbar_arrive(bar(kPFull + (MT == 2 ? wg : 0)));
           sum[0] = f2add(f2add(sum[0], sum[1]), f2add(sum[2], sum[3]));
-          l = fmaf(sum[0].x + sum[0].y, pow2_neg(lb), l);
+          l = fmaf(sum[0].x + sum[0].y, fast_exp2(-lb), l);
         } else {
           // Rare: a page at a time, once for the largest and once for the weights (little code, for the instruction cache).
           float mx = -INFINITY, vx = -INFINITY;

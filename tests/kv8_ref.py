@@ -219,9 +219,9 @@ def attention_of_rows(codes, scales, q, row_seq, row_pos, table, fmt, sink, wind
 
     Decode: weights in two fp16 parts hold 2^-22 of themselves and at worst 2^-50 of the largest.
     Extend: weights as bf16 (2^-8 of themselves) where the V scales of pages are far apart; as fp16 (2^-11, less than
-    that) where the largest so far is at most 2^8 times a block's smallest.  There w 2^3 s / r is what is held, r a
-    power of two at most twice the largest w s so far, so r <= 2^9 s for every s in the block, and a step of 2^-24 leaves w
-    off by 2^-25 r / (2^3 s) <= 2^-19: of |v| at that position, whatever else is in its page."""
+    that) where the largest so far is at most 2^8 times a block's smallest.  There w 2^4 s / r is what is held, r at
+    most the largest w s so far, so r <= 2^8 s for every s in the block, and a step of 2^-24 leaves w off by 2^-25 r / (2^4
+    s) <= 2^-21: of |v| at that position, whatever else is in its page."""
     R, hq, D = q.shape
     H = codes.shape[1]
     out = torch.zeros(R, hq, D, dtype=torch.float64, device=q.device)
@@ -249,7 +249,7 @@ def attention_of_rows(codes, scales, q, row_seq, row_pos, table, fmt, sink, wind
             size = (qq.abs() @ kk.abs().T / math.sqrt(D)).masked_fill(w == 0, 0)
             dlog = (D + 16) * 2.0 ** -24 * size.amax(1, keepdim=True) * ((w > 0).sum(1, keepdim=True) > 1)
             o, a = w @ vv, w @ vv.abs()
-            own, step = (2.0 ** -22, 2.0 ** -50) if decode else (2.0 ** -8, 2.0 ** -19)
+            own, step = (2.0 ** -22, 2.0 ** -50) if decode else (2.0 ** -8, 2.0 ** -21)
             out[rows, h] = o
             tol[rows, h] = (2.0 ** -8 * o.abs() + 2.0 ** -133 + (own + 2.0 ** -20 + n * 2.0 ** -24 + 2 * dlog) * a * 1.01
                             + step / total * (see.double() @ vv.abs()))
