@@ -525,7 +525,8 @@ oscar_status_t oscar_kv8_append_granted(const oscar_dims_t* dims, int32_t kv_for
  *   workspace     at least oscar_kv8_decode_workspace_bytes(...) bytes, 256-byte aligned; needs no
  *                 initialisation
  * A page id out of range attends nothing of that page and flags OSCAR_DEVERR_PAGE_ID.  A NaN in a query row
- * makes that row NaN, as do logits beyond fp32's range.  What lies in pages or rows that hold no token of a sequence is never seen.
+ * makes that row NaN, as may logits beyond fp32's range.  What lies in pages or rows that hold no token of a sequence
+ * is never seen.
  */
 size_t oscar_kv8_decode_workspace_bytes(const oscar_dims_t* dims, int32_t batch, int32_t max_seq_len,
                                         int32_t pages_per_split, int32_t sink_len, int32_t window_len);

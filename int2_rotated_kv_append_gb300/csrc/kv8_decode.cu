@@ -189,7 +189,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_split_kernel(const __grid_
     if (pid_s[k] >= 0) {
       const uint32_t st = my_ring + (i % kStages) * kPage;
       const float2 sc = scale_s[k];
-      const float k_scale = sc.x * qs;  // (first: a logit may be within fp32 where its product with one of them is not)
+      // (first: a logit may be within fp32 where its product with one of them is not; towards 0: never infinite, so that
+      // logits of 0 stay 0)
+      const float k_scale = __fmul_rz(sc.x, qs);
       const int pos0 = vis.page(v0 + k) * kPageSize;
       float acc[2][2][4];  // two chains of products per eight tokens
 #pragma unroll

@@ -363,7 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_extend_kernel(ExtArgs ea) {
           const int pp = bi.pos[part * kPages + pg];
           return low_bits(pos - pp + 1) & (~low_bits(after - pp + 1) | low_bits(a.sink - pp));
         };
-        auto k_scale = [&](float k) { return fmaxf(k * qs, 1.2e-38f); };  // (never 0: -inf stays -inf)
+        // (exact; never infinite: towards 0, so that logits of 0 stay 0; never 0: -infinity stays that)
+        auto k_scale = [&](float k) { return fmaxf(__fmul_rz(k, qs), 1.2e-38f); };
         // mx: the block's largest logit; vx: the largest of logit - mx + v.  m, r and what they count move where they have to.
         auto settle = [&](float mx, float vx) {
           // The product before is over: its weights' columns and O are free.  (Every phase of this barrier is waited

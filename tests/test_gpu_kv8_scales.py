@@ -217,3 +217,22 @@ def test_infinite_keys_take_or_lose_all_the_weight(fmt, at, sign):
             check(c, c.extend(q, [rows], 0, window, pps=pps), q, [0] * rows, pos, 0, window)
             if rows == 1:
                 check(c, c.decode(q, 0, window, pps=pps // 2), q, [0], pos, 0, window, decode=True)
+
+
+@pytest.mark.parametrize("fmt", [R.E4M3, R.INT8])
+def test_large_queries_that_an_infinite_key_does_not_touch(fmt):
+    # its page's K scale times the query's size is beyond fp32; the logits of that page are 0
+    H, D, L = 1, 64, 300
+    c = Cache(H, D, fmt, [L], seed=fmt + 60)
+    k, v = (torch.randn(L, H, D, device="cuda", generator=c.g).bfloat16() for _ in range(2))
+    k[[100, 250], :, 5] = float("inf")
+    start = torch.tensor([0, L], dtype=torch.int32, device="cuda")
+    ok.oscar_kv8_append(c.dims(4), fmt, 1, L, k, v, start, c.table_d, c.lens_d, c.codes, c.scales)
+    for rows in (300, 60, 10, 1):
+        q = c.q(rows, 4, 2.0 ** 14)
+        q[:, :, 5] = 0.0
+        pos = list(range(L - rows, L))
+        check(c, c.extend(q, [rows]), q, [0] * rows, pos, 0, 0)
+        check(c, c.extend(q, [rows], 3, 70, pps=8), q, [0] * rows, pos, 3, 70)
+    check(c, c.decode(q), q, [0], pos, 0, 0, decode=True)
+    check(c, c.decode(q, 3, 70, pps=2), q, [0], pos, 3, 70, decode=True)
