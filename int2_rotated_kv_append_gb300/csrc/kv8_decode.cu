@@ -14,7 +14,7 @@
 //   O += f (P V)    f = 2^(m - running maximum) * the page's V scale, in fp32.  In a split with a scale over 2^90 (infinite V
 //                   elements, saturated) O counts 2^40, so that sums of such values stay within fp32.
 // Bound by the bytes of the pages (2 D per token and KV head): 64 sequences of 1024 to 16384 tokens, 8 KV heads,
-// D = 128, 1.12 GB: 184 us with the merge, 6.1 TB/s, 90% of a plain copy's rate.  A page costs about 200
+// D = 128, 1.12 GB: 186 us with the merge, 6.0 TB/s, 89% of a plain copy's rate.  A page costs about 200
 // instructions a warp; one sequence of 32768 tokens (67 MB) takes 20 us, half of it the start of the
 // chain (length, page ids, first pages) and the merge.
 // Then the warps are merged, and a second kernel merges the splits where there are several.
@@ -390,7 +390,7 @@ bool make_plan(const oscar_dims_t* d, int batch, int max_seq_len, int pps, int s
   if (pps == 0) {
     // Splits that fill whole waves of the 3 CTAs an SM holds, of 16 to 128 pages (longer ones leave uneven lengths
     // unbalanced): the cheapest of four wave counts, a wave taking its pages and as long as 16 more for start and end.
-    // Against splits = slots / units rounded up: 8 x 8192 36 -> 29 us, 32 x 4096 64 -> 56 us.
+    // Against splits = slots / units rounded up: 8 x 8192 37 -> 30 us, 12 x 4096 31 -> 26, 32 x 4096 68 -> 58, 1 x 32768 the same.
     const long long units = static_cast<long long>(batch > 0 ? batch : 1) * d->num_kv_heads;
     const long long slots = 3LL * num_sms(), most = (pages + 4 * kWarps - 1) / (4 * kWarps);
     const long long least = (pages + 127) / 128;

@@ -32,12 +32,12 @@
 // there r may stay kWildUp lower, so that a page whose scale comes from a token hidden from the row takes no bits from the
 // row's other pages.
 //
-// Measured (GB300, 2070 MHz): 8192 rows over 16384 positions, 32 query heads, 8 KV heads, D = 128, e4m3: 1.20 ms,
-// 1370 TFLOP/s, 71% of a cuBLAS bf16 product's rate.  A block takes 3300 clocks where the products alone would
+// Measured (GB300, 2070 MHz): 8192 rows over 16384 positions, 32 query heads, 8 KV heads, D = 128, e4m3: 1.21 ms,
+// 1360 TFLOP/s, 71% of a cuBLAS bf16 product's rate (6.3 ms where the V scales of all pages are 2^20 apart).  A block takes 3300 clocks where the products alone would
 // take 2050: the softmax of a row tile (1900: 512 of them exponentials, the rest the latencies of its waits and
 // loads) and the expansion (about 2000 for K and V) run beside them on the same schedulers and the same
-// shared-memory port.  One to eight rows of 8 sequences of up to 32768 positions (bound by 274 MB of codes): 84 us,
-// 3.3 TB/s (97 us with a block's 128 tokens to one thread and two stages): a block takes about 1700 clocks where
+// shared-memory port.  One to eight rows of 8 sequences of up to 32768 positions (bound by 274 MB of codes): 87 us,
+// 3.1 TB/s: a block takes about 1700 clocks where
 // the codes would arrive in 1400, a CTA 5000 before its first block, and uneven lengths leave the last CTAs alone.
 #include <math.h>
 
@@ -937,7 +937,7 @@ bool make_plan(const oscar_dims_t* d, int batch, int rows, int max_seq_len, int 
   if (max_rows > rows) max_rows = rows;
   const long long per_seq = static_cast<long long>(max_rows) * gqa;
   p->mt = per_seq > 128 ? 2 : 1;
-  p->parts = per_seq > 64 ? 1 : 2;  // (drafts of 8 rows, GQA 8: 97 us with 1, 84 us with 2)
+  p->parts = per_seq > 64 ? 1 : 2;  // (drafts of 8 rows, GQA 8: 97 us with 1, 87 with 2)
   const int tm = 128 * p->mt;
   const long long tiles = (per_seq + tm - 1) / tm;
   const long long pages = max_visible_pages(max_seq_len, sink, window, tm / gqa + 1);
@@ -953,8 +953,9 @@ bool make_plan(const oscar_dims_t* d, int batch, int rows, int max_seq_len, int 
     long long splits = 1;
     // The cheapest of the split counts that fill whole waves of one CTA per SM, a wave taking its blocks and as long as 5
     // (short runs) or 12 more for its start and end; the 12 also stand for the merge and for causal tiles that end
-    // early (with 8, 4096 rows of 8192 positions take 445 us in two splits, 355 in one).  Against a fixed 3 (2) CTAs per SM:
-    // 8 rows of one or two sequences of 32768 tokens 4.4 -> 2.6 times their bytes' time, 512 rows of 8192 positions 89 -> 76 us.
+    // early (with 8, 4096 rows of 8192 positions take 481 us in two splits, 357 in one).  Against a fixed 3 (2) CTAs per SM:
+    // 8 rows of one sequence of 32768 tokens 51 -> 31 us, of two 64 -> 45, of eight of 16384 92 -> 81, 512 rows of 8192
+    // positions 93 -> 81.
     const long long extra = p->mt == 1 ? 5 : 12;
     long long best = 0;
     for (long long w = 1; w <= 8; ++w) {

@@ -111,7 +111,8 @@ __device__ __forceinline__ void prefetch_l2_line(const void* addr) {
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
 
-// Packed fp32 pairs: two IEEE round-to-nearest operations per instruction.
+// Packed fp32 pairs: two IEEE round-to-nearest operations per instruction.  (A packed product that goes into a packed sum or
+// difference may come out as one fused operation; where its rounding matters, the latter is scalar.)
 __device__ __forceinline__ float2 f2mul(float2 a, float2 b) {
   float2 r;
   asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
