@@ -198,7 +198,9 @@ class Kv8Cache:
         if stream is None or self.device.type != "cuda":
             return contextlib.nullcontext()
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device) if int(stream) else torch.cuda.default_stream(self.device)
+            handle = int(stream)
+            stream = (torch.cuda.ExternalStream(handle, device=self.device) if handle
+                      else torch.cuda.default_stream(self.device))
         return torch.cuda.stream(stream)
 
     def _workspace(self, nbytes, stream):

@@ -390,7 +390,8 @@ bool make_plan(const oscar_dims_t* d, int batch, int max_seq_len, int pps, int s
   if (pps == 0) {
     // Splits that fill whole waves of the 3 CTAs an SM holds, of 16 to 128 pages (longer ones leave uneven lengths
     // unbalanced): the cheapest of four wave counts, a wave taking its pages and as long as 16 more for start and end.
-    // Against splits = slots / units rounded up: 8 x 8192 37 -> 30 us, 12 x 4096 31 -> 26, 32 x 4096 68 -> 58, 1 x 32768 the same.
+    // Against splits = slots / units rounded up: 8 x 8192 37 -> 30 us, 12 x 4096 31 -> 26, 32 x 4096 68 -> 58, 1 x 32768
+    // the same.
     const long long units = static_cast<long long>(batch > 0 ? batch : 1) * d->num_kv_heads;
     const long long slots = 3LL * num_sms(), most = (pages + 4 * kWarps - 1) / (4 * kWarps);
     const long long least = (pages + 127) / 128;

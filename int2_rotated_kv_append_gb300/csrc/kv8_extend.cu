@@ -33,8 +33,8 @@
 // row's other pages.
 //
 // Measured (GB300, 2070 MHz): 8192 rows over 16384 positions, 32 query heads, 8 KV heads, D = 128, e4m3: 1.21 ms,
-// 1360 TFLOP/s, 71% of a cuBLAS bf16 product's rate (6.3 ms where the V scales of all pages are 2^20 apart).  A block takes 3300 clocks where the products alone would
-// take 2050: the softmax of a row tile (1900: 512 of them exponentials, the rest the latencies of its waits and
+// 1360 TFLOP/s, 71% of a cuBLAS bf16 product's rate (6.3 ms where the V scales of all pages are up to 2^20 apart).  A
+// block takes 3300 clocks where the products alone would take 2050: the softmax of a row tile (1900: 512 of them exponentials, the rest the latencies of its waits and
 // loads) and the expansion (about 2000 for K and V) run beside them on the same schedulers and the same
 // shared-memory port.  One to eight rows of 8 sequences of up to 32768 positions (bound by 274 MB of codes): 87 us,
 // 3.1 TB/s: a block takes about 1700 clocks where

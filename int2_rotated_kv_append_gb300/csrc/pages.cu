@@ -4,9 +4,9 @@
 // lowest id first in the order of the requests: ranks by prefix sums, no atomics whose order
 // matters.  Each operation is a planning kernel over counts and lengths and, where bytes move,
 // a second kernel that copies pages and table rows, launched as its programmatic dependent.
-// Planning is latency (a few dependent passes over 4 bytes per page: a token more for each of 64 sequences 3.4 us, a trim 2.3, a
-// fork of 24 sequences 11 with the free before it); the copies are bound by 2 x page bytes (11.5 thousand pages of 32 KB moved: 122 us, 6.2 TB/s, 92% of a plain
-// copy's rate).
+// Planning is latency (a few dependent passes over 4 bytes per page: a token more for each of 64 sequences 3.4 us, a
+// trim 2.3, a fork of 24 sequences 11 with the free before it); the copies are bound by 2 x page bytes (11.5 thousand
+// pages of 32 KB moved: 124 us, 6.1 TB/s, 90% of a plain copy's rate).
 #include "kv8.cuh"
 
 namespace {
