@@ -444,6 +444,74 @@ oscar_status_t oscar_calibrate(const oscar_dims_t* dims, int64_t num_samples, co
                                void* stream);
 
 /*
+ * ---- Rotary positions ------------------------------------------------------------
+ *
+ * Every cache here holds keys that have been rotated by their positions, and takes queries that have been (the OSCAR pages
+ * leave that to the model).  These calls do it: the first rotary_dim channels of a head are pairs, and pair i of a row at
+ * position p is turned by the angle p f_i:
+ *   y_a = magnitude (x_a cos - x_b sin),  y_b = magnitude (x_b cos + x_a sin)
+ *   (a, b) = (i, i + rotary_dim / 2)  half layout (interleaved = 0), or (2 i, 2 i + 1)  (interleaved = 1)
+ * The other channels pass through.  Frequencies are 64-bit fractions of a turn, turns[i] = f_i / (2 pi) 2^64 modulo 2^64, so that
+ * an angle modulo a turn is exact at every 32-bit position (a negative position turns backwards: keys that move towards
+ * the front of a cache).  Cosine and sine are fp32 to about a rounding, the products fp32, rounded once at the end.
+ *   rotary_dim   a multiple of 16, at most head_dim
+ *   magnitude    finite; 1 but for OSCAR_ROPE_YARN
+ *   turns        device uint64 [rotary_dim / 2], from oscar_rope_turns
+ */
+typedef struct {
+  int32_t rotary_dim;
+  int32_t interleaved;
+  float magnitude;
+  const uint64_t* turns;
+} oscar_rope_t;
+
+/*
+ * oscar_rope_turns -- the frequencies of a model, on the host: turns (host uint64 [rotary_dim / 2]) and the magnitude, from
+ * f_i = base^(-2 i / rotary_dim), base > 1, scaled for contexts longer than the model was trained on (scaling NULL: not):
+ *   OSCAR_ROPE_LINEAR    f_i / factor
+ *   OSCAR_ROPE_NTK       base times factor^(rotary_dim / (rotary_dim - 2)): the last pair is slowed by factor, the first not
+ *   OSCAR_ROPE_YARN      slow pairs are divided by factor, fast ones kept, a linear ramp over i between them: from the pair that
+ *                        turns `high` times within original_max_position (rounded down, at least 0) to the one that turns `low`
+ *                        times (rounded up, at most rotary_dim - 1); magnitude = 0.1 ln(factor) + 1 (1 where factor <= 1).
+ *                        Usual: low 1, high 32
+ *   OSCAR_ROPE_BANDS     t = original_max_position f_i / (2 pi) turns within the original length: f_i where t >= high,
+ *                        f_i / factor where t <= low, between them the mean weighted by (t - low) / (high - low)
+ *   OSCAR_ROPE_DIVISORS  f_i / divisors[i] (host double [rotary_dim / 2], > 0)
+ * Computed in double.  Invalid numbers, and frequencies over 10^6 radians a position, return OSCAR_ERR_INVALID_ARG.
+ */
+#define OSCAR_ROPE_PLAIN 0
+#define OSCAR_ROPE_LINEAR 1
+#define OSCAR_ROPE_NTK 2
+#define OSCAR_ROPE_YARN 3
+#define OSCAR_ROPE_BANDS 4
+#define OSCAR_ROPE_DIVISORS 5
+typedef struct {
+  int32_t kind;
+  int32_t original_max_position;
+  double factor, low, high;
+  const double* divisors;
+} oscar_rope_scaling_t;
+
+oscar_status_t oscar_rope_turns(int32_t rotary_dim, double base, const oscar_rope_scaling_t* scaling, uint64_t* turns,
+                                float* magnitude);
+
+/*
+ * oscar_rope -- rotates query rows and key rows, either of which may be NULL (with its output).
+ *   type       OSCAR_TYPE_BF16, _FP16 or _FP32, of q, k and the outputs
+ *   positions  device int32 [num_tokens]
+ *   q, k       device [num_tokens][Hq][D] and [num_tokens][Hkv][D], rows q_stride and k_stride elements apart (slices of one
+ *              projection's output, say), 16-byte aligned, strides multiples of 16 bytes and at least a row
+ *   q_out, k_out  the same; an output may be its input itself with the same stride (in place), and overlaps nothing otherwise
+ * num_tokens == 0 is a no-op.
+ */
+#define OSCAR_TYPE_BF16 0
+#define OSCAR_TYPE_FP16 1
+#define OSCAR_TYPE_FP32 2
+oscar_status_t oscar_rope(const oscar_dims_t* dims, const oscar_rope_t* rope, int32_t type, int64_t num_tokens,
+                          const int32_t* positions, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                          void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream);
+
+/*
  * ---- 8-bit paged cache ---------------------------------------------------------
  *
  * Between the INT2 pool and the BF16 pool: K and V unrotated, one byte per element,
@@ -503,6 +571,24 @@ oscar_status_t oscar_kv8_append_granted(const oscar_dims_t* dims, int32_t kv_for
                                         int32_t max_tokens_per_seq, const void* k, const void* v,
                                         const int32_t* t_start, const int32_t* page_table, const int32_t* seq_lens,
                                         const int32_t* granted, uint8_t* kv8_pages, float* kv8_scales, void* stream);
+
+/*
+ * oscar_kv8_rope_append -- oscar_kv8_append_granted of keys that are rotated on the way (oscar_rope_t above), and the queries of
+ * the same tokens rotated beside them, in one launch.  The rotated keys are quantised from fp32: they are not rounded to
+ * bf16 first; what is said of k at oscar_kv8_append holds for the rotated values.
+ *   q, k, v    device bf16 [num_tokens][Hq or Hkv][D], rows q_stride, k_stride, v_stride elements apart, as oscar_rope; q may be
+ *              NULL (with q_out)
+ *   positions  device int32 [num_tokens], or NULL: every token's position in its sequence
+ *   q_out      device bf16 [num_tokens][Hq][D], rows q_out_stride apart; may be q itself with the same stride
+ * Queries of a sequence that granted refuses become zeros, those of a sequence that is skipped for its numbers are left as they
+ * were; a bad page id costs that page's keys and values alone.
+ */
+oscar_status_t oscar_kv8_rope_append(const oscar_dims_t* dims, const oscar_rope_t* rope, int32_t kv_format, int32_t batch,
+                                     int64_t num_tokens, int32_t max_tokens_per_seq, const void* q, int64_t q_stride,
+                                     const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int32_t* t_start,
+                                     const int32_t* positions, const int32_t* page_table, const int32_t* seq_lens,
+                                     const int32_t* granted, uint8_t* kv8_pages, float* kv8_scales, void* q_out,
+                                     int64_t q_out_stride, void* stream);
 
 /*
  * oscar_kv8_decode -- paged GQA decode attention over the 8-bit cache, with an

@@ -37,6 +37,17 @@ OSCAR_KV8_INT8 = 1
 
 OSCAR_MAX_POOLS = 8
 
+OSCAR_TYPE_BF16 = 0
+OSCAR_TYPE_FP16 = 1
+OSCAR_TYPE_FP32 = 2
+
+OSCAR_ROPE_PLAIN = 0
+OSCAR_ROPE_LINEAR = 1
+OSCAR_ROPE_NTK = 2
+OSCAR_ROPE_YARN = 3
+OSCAR_ROPE_BANDS = 4
+OSCAR_ROPE_DIVISORS = 5
+
 
 class OscarError(RuntimeError):
     def __init__(self, status: int, where: str):
@@ -58,6 +69,16 @@ class oscar_page_pool_t(ctypes.Structure):
     _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
 
 
+class oscar_rope_t(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("turns", ctypes.c_void_p)]
+
+
+class oscar_rope_scaling_t(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("original_max_position", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("divisors", ctypes.POINTER(ctypes.c_double))]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"OSCAR CUDA library not built ({LIB_PATH} missing); run "
@@ -66,6 +87,7 @@ def _load():
     P, I32, I64, F32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
     D = ctypes.POINTER(oscar_dims_t)
     L = ctypes.POINTER(oscar_page_pool_t)
+    R = ctypes.POINTER(oscar_rope_t)
     sigs = {
         "oscar_append": (I32, [D, I64, P, P, P, P, P, P, P, P, P, P, P, P]),
         "oscar_append_mixed": (I32, [D, I64, P, P, P, P, P, P, P, P, P, P, P, P, I32, I32, I32, P, P, P, P, P]),
@@ -87,6 +109,9 @@ def _load():
         "oscar_calibrate_workspace_bytes": (SZ, [D, I64]),
         "oscar_calibrate": (I32, [D, I64, P, P, I32, ctypes.c_double, ctypes.POINTER(oscar_calib_out_t),
                                   ctypes.POINTER(oscar_calib_out_t), P, SZ, P]),
+        "oscar_rope_turns": (I32, [I32, ctypes.c_double, ctypes.POINTER(oscar_rope_scaling_t), P, ctypes.POINTER(F32)]),
+        "oscar_rope": (I32, [D, R, I32, I64, P, P, I64, P, I64, P, I64, P, I64, P]),
+        "oscar_kv8_rope_append": (I32, [D, R, I32, I32, I64, I32, P, I64, P, I64, P, I64, P, P, P, P, P, P, P, P, I64, P]),
         "oscar_kv8_append": (I32, [D, I32, I32, I64, I32, P, P, P, P, P, P, P, P]),
         "oscar_kv8_append_granted": (I32, [D, I32, I32, I64, I32, P, P, P, P, P, P, P, P, P]),
         "oscar_kv8_decode_workspace_bytes": (SZ, [D, I32, I32, I32, I32, I32]),
@@ -327,6 +352,127 @@ def oscar_calibrate(dims, num_samples, k, v, centered, clip_quantile, out_k, out
     _check(lib.oscar_calibrate(ctypes.byref(_dims(dims)), int(num_samples), _ptr(k), _ptr(v), int(centered),
                                float(clip_quantile), _calib_out(out_k), _calib_out(out_v), _ptr(workspace),
                                workspace.numel() * workspace.element_size(), _stream(stream)), "oscar_calibrate")
+
+
+def oscar_rope_turns(rotary_dim, base=10000.0, scaling=None):
+    """The frequencies of a model, on the host: (int64 tensor [rotary_dim / 2] of 64-bit fractions of a turn, magnitude).
+    ``scaling``: None, or a dict with "kind" and that kind's numbers: "linear" and "ntk" (factor), "yarn" (factor,
+    original_max_position, beta_slow = 1, beta_fast = 32), "bands" (factor, original_max_position, low_freq_factor,
+    high_freq_factor), "divisors" (divisors, one per pair)."""
+    c = oscar_rope_scaling_t()
+    if scaling is not None:
+        kinds = {"linear": (OSCAR_ROPE_LINEAR, ("factor",), {}), "ntk": (OSCAR_ROPE_NTK, ("factor",), {}),
+                 "yarn": (OSCAR_ROPE_YARN, ("factor", "original_max_position"), {"beta_slow": 1.0, "beta_fast": 32.0}),
+                 "bands": (OSCAR_ROPE_BANDS, ("factor", "original_max_position", "low_freq_factor", "high_freq_factor"), {}),
+                 "divisors": (OSCAR_ROPE_DIVISORS, ("divisors",), {})}
+        s = dict(scaling)
+        kind = s.pop("kind", None)
+        if kind not in kinds:
+            raise ValueError(f"scaling kinds are {', '.join(kinds)}")
+        c.kind, needed, optional = kinds[kind]
+        if not set(needed) <= s.keys() <= set(needed) | optional.keys():
+            raise ValueError(f"scaling {kind!r} has {', '.join(needed + tuple(optional))}")
+        s = {**optional, **s}
+        if kind == "divisors":
+            if len(s["divisors"]) != rotary_dim // 2:
+                raise ValueError("divisors has one entry per pair")
+            c.divisors = (ctypes.c_double * len(s["divisors"]))(*s["divisors"])
+        c.factor = s.get("factor", 1.0)
+        c.original_max_position = s.get("original_max_position", 0)
+        c.low = s.get("beta_slow", s.get("low_freq_factor", 0.0))
+        c.high = s.get("beta_fast", s.get("high_freq_factor", 0.0))
+    turns = torch.zeros(max(int(rotary_dim) // 2, 1), dtype=torch.int64)
+    magnitude = ctypes.c_float(0.0)
+    _check(lib.oscar_rope_turns(int(rotary_dim), float(base), None if scaling is None else ctypes.byref(c), turns.data_ptr(),
+                                ctypes.byref(magnitude)), "oscar_rope_turns")
+    return turns, magnitude.value
+
+
+class Rope:
+    """A model's rotary positions: the frequencies on the device and what else oscar_rope_t holds (arguments as
+    oscar_rope_turns; ``interleaved``: pairs are neighbours, else halves of the rotated channels; ``magnitude``: in the
+    place of the scaling's own)."""
+
+    def __init__(self, rotary_dim, base=10000.0, interleaved=False, scaling=None, magnitude=None, device="cuda"):
+        turns, own = oscar_rope_turns(rotary_dim, base, scaling)
+        self.turns = turns.to(device)
+        self.rotary_dim, self.interleaved = int(rotary_dim), bool(interleaved)
+        self.magnitude = own if magnitude is None else float(magnitude)
+        self.c = oscar_rope_t(self.rotary_dim, int(self.interleaved), self.magnitude, self.turns.data_ptr())
+
+
+_TYPES = {torch.bfloat16: OSCAR_TYPE_BF16, torch.float16: OSCAR_TYPE_FP16, torch.float32: OSCAR_TYPE_FP32}
+
+
+def _rows(t, heads, dim, what):
+    """Pointer and stride of rows [T][heads][dim] that may be slices of longer rows; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim):
+        raise ValueError(f"{what} is [tokens][{heads}][{dim}]")
+    if t.numel() == 0:
+        return t.data_ptr() or 16, heads * dim
+    if t.stride(2) != 1 or t.stride(1) != dim and heads > 1:
+        raise ValueError(f"{what}: the heads of a row are contiguous")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def _same_device(*tensors):
+    """The tensors of one call are on the current device: its stream and kernels are."""
+    now = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != now:
+            raise ValueError(f"tensors of a call are on the current CUDA device ({now})")
+
+
+def _int32(t, n, what):
+    if t is not None and (t.dtype != torch.int32 or t.numel() < n):
+        raise ValueError(f"{what} is int32 with {n} entries or more")
+
+
+def oscar_rope(dims, rope, positions, q, k, q_out, k_out, stream=None):
+    """Rotate q [T][Hq][D] and k [T][Hkv][D] (bf16, fp16 or fp32; either may be None, with its output) by positions
+    (int32 [T]) into q_out and k_out, which may be q and k themselves.  Rows may be slices of longer ones."""
+    d = _dims(dims)
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("q or k is given")
+    tokens, dtype = some.shape[0], some.dtype
+    if dtype not in _TYPES:
+        raise ValueError("rows are bfloat16, float16 or float32")
+    for t in (q, k, q_out, k_out):
+        if t is not None and (t.dtype != dtype or t.shape[0] != tokens):
+            raise ValueError("rows of q, k and the outputs have one type and number")
+    _int32(positions, tokens, "positions")
+    _same_device(positions, q, k, q_out, k_out, rope.turns)
+    ptrs = [x for t, h, n in ((q, d.num_q_heads, "q"), (k, d.num_kv_heads, "k"), (q_out, d.num_q_heads, "q_out"),
+                              (k_out, d.num_kv_heads, "k_out")) for x in _rows(t, h, d.head_dim, n)]
+    _check(lib.oscar_rope(ctypes.byref(d), ctypes.byref(rope.c), _TYPES[dtype], int(tokens), _ptr(positions), *ptrs,
+                          _stream(stream)), "oscar_rope")
+
+
+def oscar_kv8_rope_append(dims, rope, kv_format, batch, max_tokens_per_seq, q, k, v, t_start, positions, page_table, seq_lens,
+                          kv8_pages, kv8_scales, q_out, stream=None, granted=None):
+    """oscar_kv8_append of keys that are rotated on the way, and the queries q [T][Hq][D] of the same tokens rotated into
+    q_out (both may be None; q_out may be q).  ``positions``: int32 [T], or None for the positions in the sequences.
+    Rows of q, k, v and q_out may be slices of longer ones."""
+    d = _dims(dims)
+    tokens = k.shape[0]
+    for t in (q, k, v, q_out):
+        if t is not None and (t.dtype != torch.bfloat16 or t.shape[0] != tokens):
+            raise ValueError("q, k, v and q_out are bfloat16 rows, one per token")
+    _int32(positions, tokens, "positions")
+    _int32(t_start, batch + 1, "t_start")
+    _int32(seq_lens, batch, "seq_lens")
+    _int32(granted, batch, "granted")
+    _int32(page_table, batch * d.max_pages_per_seq, "page_table")
+    _same_device(q, k, v, t_start, positions, page_table, seq_lens, kv8_pages, kv8_scales, q_out, granted, rope.turns)
+    qp, ks, vp, op = (_rows(t, h, d.head_dim, n) for t, h, n in ((q, d.num_q_heads, "q"), (k, d.num_kv_heads, "k"),
+                                                                 (v, d.num_kv_heads, "v"), (q_out, d.num_q_heads, "q_out")))
+    _check(lib.oscar_kv8_rope_append(ctypes.byref(d), ctypes.byref(rope.c), int(kv_format), int(batch), int(tokens),
+                                     int(max_tokens_per_seq), *qp, *ks, *vp, _ptr(t_start), _ptr(positions),
+                                     _ptr(page_table), _ptr(seq_lens), _ptr(granted), _ptr(kv8_pages), _ptr(kv8_scales), *op,
+                                     _stream(stream)), "oscar_kv8_rope_append")
 
 
 def _nbytes(t) -> int:
