@@ -651,6 +651,37 @@ oscar_status_t oscar_kv8_extend_varlen(const oscar_dims_t* dims, int32_t kv_form
                                        void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * oscar_kv8_decode_shared -- oscar_kv8_decode (without a window) of sequences whose first pages are the same, as
+ * oscar_pages_fork leaves them: each group's prefix is attended once for all its members, on tensor cores, what a member has
+ * behind it by itself, and the two are joined by log-sum-exp.  The result is that of oscar_kv8_decode, but that weights over
+ * the prefix are held in 11 bits (oscar_kv8_extend_varlen); the output has 8.
+ * Arguments beyond oscar_kv8_decode's
+ *   num_members   entries of `members` at most; num_groups: of prefix_lens
+ *   members       device int32 [num_members]: the sequences to decode, group after group
+ *   group_start   device int32 [num_groups + 1], non-decreasing, group_start[0] = 0: group g is members group_start[g] ..
+ *                 group_start[g + 1] - 1; members from group_start[num_groups] <= num_members on are none
+ *   prefix_lens   device int32 [num_groups]: the tokens that all members of the group share, of which whole pages are attended
+ *                 together, read through the page table of the group's first member; 0 for sequences by themselves
+ *   max_prefix_len  host bound: of a longer prefix the first max_prefix_len tokens (whole pages) are attended together, and the
+ *                 rest with each member's own
+ *   max_own_len   host bound on what any member has behind that; longer ones are cut off and flagged (OSCAR_DEVERR_SEQ_LEN)
+ * q and out have a row for every sequence; rows of sequences that are no member are neither read nor written.  A member shorter
+ * than its group's prefix attends what it has.  The work is split for these bounds: the nearer they and num_groups are to what
+ * the lists hold, the quicker.  A sequence is named once: of one named twice, either of the two results is left.  A
+ * member out of [0, batch) is skipped and flagged (OSCAR_DEVERR_POSITION); lists that decrease or leave their range are flagged
+ * and nothing is written.
+ */
+size_t oscar_kv8_decode_shared_workspace_bytes(const oscar_dims_t* dims, int32_t batch, int32_t max_seq_len,
+                                               int32_t max_prefix_len, int32_t max_own_len, int32_t num_members,
+                                               int32_t num_groups);
+oscar_status_t oscar_kv8_decode_shared(const oscar_dims_t* dims, int32_t kv_format, int32_t batch, int32_t max_seq_len,
+                                       int32_t max_prefix_len, int32_t max_own_len, int32_t num_members, int32_t num_groups,
+                                       const void* q, const uint8_t* kv8_pages, const float* kv8_scales,
+                                       const int32_t* page_table, const int32_t* seq_lens, const int32_t* members,
+                                       const int32_t* group_start, const int32_t* prefix_lens, float sm_scale, void* out,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * ---- Pages ----------------------------------------------------------------------
  *
  * Operations on the pages of a paged cache, whatever they hold: the INT2 codes and
@@ -746,6 +777,22 @@ oscar_status_t oscar_pages_trim(const oscar_dims_t* dims, int32_t batch, int32_t
 oscar_status_t oscar_pages_compact(const oscar_dims_t* dims, int32_t num_pools, const oscar_page_pool_t* pools,
                                    int32_t batch, int32_t* page_table, const int32_t* seq_lens, int32_t* page_refs,
                                    int32_t* num_used, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * oscar_pages_groups -- finds the sequences that share their first pages, as oscar_kv8_decode_shared takes them.  Sequences whose
+ * first min_pages >= 1 pages are full and the same (page ids, none negative) are a group; its prefix is the tokens of the
+ * leading full pages that all its members share.  Groups of two members or more are listed in the order of their lowest
+ * members, max_groups - 1 of them at most; then, as the last group with prefix 0, every other sequence (empty ones too).
+ *   members       device int32 [batch], every sequence once, ascending within a group
+ *   group_start   device int32 [max_groups + 1]; groups behind the last one are empty
+ *   prefix_lens   device int32 [max_groups]
+ * A length out of range flags OSCAR_DEVERR_POSITION; that sequence is in the last group.  Nothing is done for batch == 0.
+ * Workspace: oscar_pages_groups_workspace_bytes(dims, batch) bytes, 256-byte aligned, no initialisation.
+ */
+size_t oscar_pages_groups_workspace_bytes(const oscar_dims_t* dims, int32_t batch);
+oscar_status_t oscar_pages_groups(const oscar_dims_t* dims, int32_t batch, int32_t min_pages, int32_t max_groups,
+                                  const int32_t* page_table, const int32_t* seq_lens, int32_t* members, int32_t* group_start,
+                                  int32_t* prefix_lens, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* oscar_status_string(oscar_status_t status);

@@ -118,6 +118,10 @@ def _load():
         "oscar_kv8_decode": (I32, [D, I32, I32, I32, I32, P, P, P, P, P, I32, I32, F32, P, P, SZ, P]),
         "oscar_kv8_extend_varlen_workspace_bytes": (SZ, [D, I32, I32, I32, I32, I32, I32, I32]),
         "oscar_kv8_extend_varlen": (I32, [D, I32, I32, I32, I32, I32, I32, P, P, P, P, P, P, I32, I32, F32, P, P, SZ, P]),
+        "oscar_kv8_decode_shared_workspace_bytes": (SZ, [D, I32, I32, I32, I32, I32, I32]),
+        "oscar_kv8_decode_shared": (I32, [D, I32, I32, I32, I32, I32, I32, I32, P, P, P, P, P, P, P, P, F32, P, P, SZ, P]),
+        "oscar_pages_groups_workspace_bytes": (SZ, [D, I32]),
+        "oscar_pages_groups": (I32, [D, I32, I32, I32, P, P, P, P, P, P, SZ, P]),
         "oscar_pages_workspace_bytes": (SZ, [D, I32, I32]),
         "oscar_pages_copy": (I32, [D, I32, L, I32, P, P, P]),
         "oscar_pages_reserve": (I32, [D, I32, P, P, P, P, P, P, SZ, P]),
@@ -529,6 +533,34 @@ def oscar_kv8_extend_varlen(dims, kv_format, batch, max_seq_len, max_rows_per_se
            "oscar_kv8_extend_varlen")
 
 
+def oscar_kv8_decode_shared_workspace_bytes(dims, batch, max_seq_len, max_prefix_len, max_own_len, num_members,
+                                            num_groups) -> int:
+    return int(lib.oscar_kv8_decode_shared_workspace_bytes(ctypes.byref(_dims(dims)), int(batch), int(max_seq_len),
+                                                           int(max_prefix_len), int(max_own_len), int(num_members),
+                                                           int(num_groups)))
+
+
+def oscar_kv8_decode_shared(dims, kv_format, batch, max_seq_len, max_prefix_len, max_own_len, q, kv8_pages, kv8_scales,
+                            page_table, seq_lens, members, group_start, prefix_lens, sm_scale, out, workspace, stream=None):
+    """One decode step over the 8-bit cache of the sequences ``members``, group after group (group_start [groups + 1]): the
+    first prefix_lens[g] tokens, which group g shares, are attended once for all of it.  Writes the members' rows of bf16
+    out [batch][Hq][D]."""
+    d = _dims(dims)
+    groups = prefix_lens.numel()
+    shape = (batch, d.num_q_heads, d.head_dim)
+    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or q.shape != shape or out.shape != shape:
+        raise ValueError("q and out are bfloat16 [batch][Hq][D]")
+    for t, n, what in ((members, 0, "members"), (group_start, groups + 1, "group_start"), (prefix_lens, 0, "prefix_lens"),
+                       (seq_lens, batch, "seq_lens"), (page_table, batch * d.max_pages_per_seq, "page_table")):
+        _int32(t, n, what)
+    _same_device(q, kv8_pages, kv8_scales, page_table, seq_lens, members, group_start, prefix_lens, out, workspace)
+    _check(lib.oscar_kv8_decode_shared(ctypes.byref(d), int(kv_format), int(batch), int(max_seq_len), int(max_prefix_len),
+                                       int(max_own_len), int(members.numel()), int(groups), _ptr(q), _ptr(kv8_pages),
+                                       _ptr(kv8_scales), _ptr(page_table), _ptr(seq_lens), _ptr(members), _ptr(group_start),
+                                       _ptr(prefix_lens), float(sm_scale), _ptr(out), _ptr(workspace), _nbytes(workspace),
+                                       _stream(stream)), "oscar_kv8_decode_shared")
+
+
 def _pools(pools, num_pages):
     """The pools' tensors, num_pages pages each, as the C array."""
     arr = (oscar_page_pool_t * max(len(pools), 1))()
@@ -593,6 +625,25 @@ def oscar_pages_compact(dims, pools, page_table, seq_lens, page_refs, num_used, 
     _check(lib.oscar_pages_compact(ctypes.byref(d), len(pools), _pools(pools, d.num_pages), int(seq_lens.shape[0]),
                                    _ptr(page_table), _ptr(seq_lens), _ptr(page_refs), _ptr(num_used), _ptr(workspace),
                                    _nbytes(workspace), _stream(stream)), "oscar_pages_compact")
+
+
+def oscar_pages_groups_workspace_bytes(dims, batch) -> int:
+    return int(lib.oscar_pages_groups_workspace_bytes(ctypes.byref(_dims(dims)), int(batch)))
+
+
+def oscar_pages_groups(dims, min_pages, page_table, seq_lens, members, group_start, prefix_lens, workspace, stream=None):
+    """The sequences whose first min_pages pages are full and the same, as groups for oscar_kv8_decode_shared: members
+    (int32 [batch]), group_start (int32 [groups + 1]) and prefix_lens (int32 [groups]) are written; what is in no group of
+    two, or beyond groups - 1 of them, is the last group, without a prefix."""
+    d = _dims(dims)
+    batch, room = seq_lens.shape[0], prefix_lens.numel()
+    for t, n, what in ((members, batch, "members"), (group_start, room + 1, "group_start"), (prefix_lens, 1, "prefix_lens"),
+                       (seq_lens, batch, "seq_lens"), (page_table, batch * d.max_pages_per_seq, "page_table")):
+        _int32(t, n, what)
+    _same_device(page_table, seq_lens, members, group_start, prefix_lens, workspace)
+    _check(lib.oscar_pages_groups(ctypes.byref(d), int(batch), int(min_pages), int(room), _ptr(page_table), _ptr(seq_lens),
+                                  _ptr(members), _ptr(group_start), _ptr(prefix_lens), _ptr(workspace), _nbytes(workspace),
+                                  _stream(stream)), "oscar_pages_groups")
 
 
 def oscar_test_stall_page_waits(cycles: int) -> None:

@@ -3,7 +3,8 @@
 ``Int2Cache`` owns the INT2 code pool, the fp16 scale/zero pool and the BF16
 sink/window buffers of a workload; ``Bf16Cache`` owns the all-BF16 pool of the
 speedup reference; ``Kv8Cache`` owns an 8-bit pool whose pages it manages itself
-(reserve, fork, free, trim, compact).  They only allocate torch memory and call the
+(reserve, fork, free, trim, compact), rotates keys on their way in and attends
+shared prefixes once.  They only allocate torch memory and call the
 library, as does ``calibrate`` (the offline step that produces R and the clipping
 thresholds).
 
@@ -14,15 +15,18 @@ made on one stream at a time.  ``Kv8Cache`` has one per stream.
 from __future__ import annotations
 
 import contextlib
+from typing import NamedTuple
 
 import torch
 
 from . import (OSCAR_KV8_E4M3, make_dims, oscar_append, oscar_append_mixed, oscar_bf16_append, oscar_bf16_decode,
                oscar_bf16_decode_workspace_bytes, oscar_calibrate, oscar_calibrate_workspace_bytes, oscar_decode,
                oscar_decode_workspace_bytes, oscar_extend, oscar_extend_varlen, oscar_extend_varlen_workspace_bytes,
-               oscar_extend_workspace_bytes, oscar_kv8_append, oscar_kv8_decode, oscar_kv8_decode_workspace_bytes,
-               oscar_kv8_extend_varlen, oscar_kv8_extend_varlen_workspace_bytes, oscar_pages_compact, oscar_pages_fork,
-               oscar_pages_free, oscar_pages_reserve, oscar_pages_trim, oscar_pages_workspace_bytes, _stream)
+               oscar_extend_workspace_bytes, oscar_kv8_append, oscar_kv8_decode, oscar_kv8_decode_shared,
+               oscar_kv8_decode_shared_workspace_bytes, oscar_kv8_decode_workspace_bytes, oscar_kv8_extend_varlen,
+               oscar_kv8_extend_varlen_workspace_bytes, oscar_kv8_rope_append, oscar_pages_compact, oscar_pages_fork,
+               oscar_pages_free, oscar_pages_groups, oscar_pages_groups_workspace_bytes, oscar_pages_reserve,
+               oscar_pages_trim, oscar_pages_workspace_bytes, _stream)
 from .synth import Workload
 
 SENTINEL = 0xA5
@@ -166,6 +170,14 @@ class Bf16Cache:
         return out
 
 
+class SharedPrefixes(NamedTuple):
+    """Groups of sequences that share a prefix (int32 device tensors), as ``Kv8Cache.groups`` finds them."""
+
+    members: torch.Tensor      # sequences, group after group
+    group_start: torch.Tensor  # [groups + 1]
+    prefix_lens: torch.Tensor  # [groups] tokens
+
+
 class Kv8Cache:
     """An 8-bit paged cache for up to ``batch`` sequences of max_seq_len tokens (rounded up to whole
     pages of 16), with its page table, lengths and page counts.  With ``window_len`` >= 1 attention
@@ -228,6 +240,17 @@ class Kv8Cache:
         oscar_kv8_append(self.dims, self.kv_format, self.batch, max_tokens_per_seq, k, v, t_start, self.page_table,
                          self.seq_lens, self.pages, self.scales, stream, granted=self.granted)
 
+    def rope_append(self, q, k, v, rope, t_start, max_tokens_per_seq, q_out=None, positions=None, stream=None):
+        """``append`` of keys that ``rope`` (a ``Rope``) rotates on the way, at their positions in the sequences or at
+        ``positions`` (int32 device [T]); returns the rotated queries (``q_out``, which may be q; None where q is None).  q, k
+        and v may be slices of one projection's rows."""
+        if q is not None and q_out is None:
+            with self._allocating(stream):
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        oscar_kv8_rope_append(self.dims, rope, self.kv_format, self.batch, max_tokens_per_seq, q, k, v, t_start, positions,
+                              self.page_table, self.seq_lens, self.pages, self.scales, q_out, stream, granted=self.granted)
+        return q_out
+
     def _bound(self, max_seq_len):
         if max_seq_len is None:
             return self.max_seq_len
@@ -245,6 +268,38 @@ class Kv8Cache:
                                                               self.sink_len, self.window_len), stream)
         oscar_kv8_decode(self.dims, self.kv_format, self.batch, bound, pages_per_split, q, self.pages, self.scales,
                          self.page_table, self.seq_lens, self.sink_len, self.window_len, sm_scale, out, ws, stream)
+        return out
+
+    def groups(self, min_pages=1, max_groups=8, stream=None):
+        """The sequences whose first min_pages pages are full and the same (as ``fork`` leaves them), max_groups - 1 groups of
+        them at most, and the rest.  They hold until a sequence of a group is forked, freed, trimmed or shortened: one call
+        serves every layer of a step, and later steps that only append."""
+        with self._allocating(stream):
+            new = lambda n: torch.empty(n, dtype=torch.int32, device=self.device)  # noqa: E731
+            g = SharedPrefixes(new(self.batch), new(max_groups + 1), new(max_groups))
+        oscar_pages_groups(self.dims, min_pages, self.page_table, self.seq_lens, *g,
+                           self._workspace(oscar_pages_groups_workspace_bytes(self.dims, self.batch), stream), stream)
+        return g
+
+    def decode_shared(self, q, groups, out=None, sm_scale=0.0, stream=None, max_seq_len=None, max_prefix_len=None,
+                      max_own_len=None):
+        """``decode`` that attends what each group (a ``SharedPrefixes``) shares once for all its members, for caches without a
+        window.  The bounds (None: max_seq_len's) size the work: on a group's prefix, of which more is attended by each
+        member, and on what a member has behind it.  Rows of sequences that are no member are left as they are in ``out``,
+        and mean nothing in an output made here."""
+        if self.window_len:
+            raise ValueError("decode_shared is for caches without a window")
+        bound = self._bound(max_seq_len)
+        prefix, own = (bound if x is None else x for x in (max_prefix_len, max_own_len))
+        if not (0 <= prefix <= bound and 0 <= own <= bound):
+            raise ValueError(f"bounds on parts of a sequence are between 0 and {bound}")
+        if out is None:
+            out = self._output(q, stream)
+        ws = self._workspace(oscar_kv8_decode_shared_workspace_bytes(self.dims, self.batch, bound, prefix, own,
+                                                                     groups.members.numel(), groups.prefix_lens.numel()),
+                             stream)
+        oscar_kv8_decode_shared(self.dims, self.kv_format, self.batch, bound, prefix, own, q, self.pages, self.scales,
+                                self.page_table, self.seq_lens, *groups, sm_scale, out, ws, stream)
         return out
 
     def extend(self, q, q_start, max_rows_per_seq, out=None, sm_scale=0.0, pages_per_split=0, stream=None,

@@ -129,4 +129,5 @@ oscar_status_t oscar_internal_kv8_append_errors(uint32_t* flags, int reset);
 oscar_status_t oscar_internal_kv8_rope_append_errors(uint32_t* flags, int reset);
 oscar_status_t oscar_internal_kv8_decode_errors(uint32_t* flags, int reset);
 oscar_status_t oscar_internal_kv8_extend_errors(uint32_t* flags, int reset);
+oscar_status_t oscar_internal_kv8_shared_errors(uint32_t* flags, int reset);
 oscar_status_t oscar_internal_pages_errors(uint32_t* flags, int reset);

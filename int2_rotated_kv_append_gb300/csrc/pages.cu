@@ -1,4 +1,4 @@
-// Operations on the pages of a paged cache: copy, reserve, fork, free, trim, compact.
+// Operations on the pages of a paged cache: copy, reserve, fork, free, trim, compact, and groups of sequences that share pages.
 //
 // A page's reference count is the allocator's whole state (0 = free), and free pages are taken
 // lowest id first in the order of the requests: ranks by prefix sums, no atomics whose order
@@ -502,6 +502,161 @@ int page_parts(const Pools& p) {
 
 oscar_status_t launched() { return cudaGetLastError() == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA; }
 
+// ---- groups of sequences with the same first pages ------------------------------------------
+
+constexpr int kNoMatch = 0x7fffffff;
+
+// One block per sequence b: the lowest sequence whose first k pages are b's (b itself where there is none lower), and how many
+// leading pages the two have in common.  A sequence with fewer than k full pages is its own.
+__global__ void __launch_bounds__(256) groups_find_kernel(Tables t, int k, int32_t* leader, int32_t* depth) {
+  __shared__ int found, differs;
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  auto full_pages = [&](int a) {
+    const int L = __ldg(t.lens + a);
+    return length_ok(t, L) ? L / kPageSize : 0;
+  };
+  auto row = [&](int a) { return t.table + static_cast<size_t>(a) * t.max_pages; };
+  const int full = full_pages(b);
+  if (tid == 0 && !length_ok(t, __ldg(t.lens + b))) record_error(OSCAR_DEVERR_POSITION);
+  const int32_t* mine = row(b);
+  const int last = full >= k ? __ldg(mine + k - 1) : -1;
+  if (tid == 0) found = differs = kNoMatch;
+  __syncthreads();
+  for (int a0 = 0; a0 < b && last >= 0; a0 += blockDim.x) {
+    const int a = a0 + tid;
+    bool hit = false;
+    uint32_t maybe = __ballot_sync(0xffffffffu, a < b && full_pages(min(a, b)) >= k && __ldg(row(min(a, b)) + k - 1) == last);
+    for (; maybe != 0; maybe &= maybe - 1) {  // a warp looks at its own, lowest first
+      const int c = a - lane + __ffs(maybe) - 1;
+      bool same = true;
+      for (int j = lane; j < k && same; j += 32) {
+        const int p = __ldg(mine + j);
+        same = p >= 0 && p == __ldg(row(c) + j);
+      }
+      if (__all_sync(0xffffffffu, same)) {
+        if (lane == 0) atomicMin(&found, c);
+        hit = true;
+        break;
+      }
+    }
+    if (__syncthreads_or(hit)) break;
+  }
+  const int lead = found == kNoMatch ? b : found;
+  if (tid == 0) leader[b] = lead;
+  if (lead == b) {
+    if (tid == 0) depth[b] = full;
+    return;
+  }
+  const int32_t* theirs = row(lead);
+  const int most = min(full, full_pages(lead));
+  constexpr int kEach = 4;
+  for (int j0 = k; j0 < most; j0 += kEach * 256) {
+    int x[kEach], y[kEach], at = kNoMatch;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int j = min(j0 + e * 256 + tid, most - 1);
+      x[e] = __ldg(mine + j);
+      y[e] = __ldg(theirs + j);
+    }
+#pragma unroll
+    for (int e = kEach - 1; e >= 0; --e)
+      if (j0 + e * 256 + tid < most && (x[e] != y[e] || x[e] < 0)) at = j0 + e * 256 + tid;
+    at = __reduce_min_sync(0xffffffffu, at);
+    if (lane == 0 && at != kNoMatch) atomicMin(&differs, at);
+    if (__syncthreads_or(at != kNoMatch)) break;
+  }
+  if (tid == 0) depth[b] = min(differs, most);
+}
+
+// One block: numbers the groups of two members or more in the order of their leaders, `room` - 1 of them at most, and lists
+// their members; then all other sequences as one group without a prefix.
+constexpr int kLeadersHere = 4096;
+__global__ void __launch_bounds__(kPlanThreads) groups_list_kernel(int batch, int room, const int32_t* leaders, const int32_t* depth,
+                                                                   int32_t* kind, int32_t* heads, int32_t* members,
+                                                                   int32_t* start, int32_t* prefix) {
+  __shared__ int part[kPlanWarps];
+  __shared__ int32_t here[kLeadersHere];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dep_wait();
+  for (int b = tid; b < batch; b += kPlanThreads) {
+    if (batch <= kLeadersHere) here[b] = leaders[b];
+    kind[b] = 0;
+  }
+  const int32_t* leader = batch <= kLeadersHere ? here : leaders;
+  __syncthreads();
+  for (int b = tid; b < batch; b += kPlanThreads)
+    if (leader[b] != b) kind[leader[b]] = 1;  // leads others
+  __syncthreads();
+  int count = 0;
+  for (int b0 = 0; b0 < batch; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    const int leads = b < batch && kind[b] == 1;
+    int sum;
+    const int rank = count + block_scan(leads, part, &sum);
+    if (leads && rank < room - 1) {
+      heads[rank] = b;
+      kind[b] = 2;  // leads a group that is listed
+    }
+    count += sum;
+  }
+  count = min(count, room - 1);
+  __syncthreads();
+  // a warp per group: members, and the pages that all of them share
+  for (int g = warp; g < count; g += kPlanWarps) {
+    const int head = heads[g];
+    int n = 0, least = kNoMatch;
+    for (int b0 = head & ~31; b0 < batch; b0 += 32) {
+      const int b = b0 + lane;
+      const bool in = b < batch && leader[min(b, batch - 1)] == head;
+      if (in) least = min(least, depth[b]);
+      n += __popc(__ballot_sync(0xffffffffu, in));
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (lane == 0) {
+      start[g + 1] = n;
+      prefix[g] = least * kPageSize;
+    }
+  }
+  __syncthreads();
+  int before = 0;
+  for (int g0 = 0; g0 < room; g0 += kPlanThreads) {
+    const int g = g0 + tid;
+    int sum;
+    const int n = g < count ? start[g + 1] : 0;
+    const int at = before + block_scan(n, part, &sum) + n;
+    if (g < room) {
+      start[g + 1] = g < count ? at : batch;
+      if (g >= count) prefix[g] = 0;
+    }
+    before += sum;
+  }
+  if (tid == 0) start[0] = 0;
+  __syncthreads();
+  for (int g = warp; g < count; g += kPlanWarps) {
+    const int head = heads[g];
+    int at = start[g];
+    const int end = start[g + 1];
+    for (int b0 = head & ~31; at < end; b0 += 32) {
+      const int b = b0 + lane;
+      const bool in = b < batch && leader[min(b, batch - 1)] == head;
+      const uint32_t all = __ballot_sync(0xffffffffu, in);
+      if (in) members[at + __popc(all & ((1u << lane) - 1))] = b;
+      at += __popc(all);
+    }
+  }
+  int rest = before;
+  for (int b0 = 0; b0 < batch; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    const int alone = b < batch && kind[leader[min(b, batch - 1)]] != 2;
+    int sum;
+    const int at = rest + block_scan(alone, part, &sum);
+    if (alone) members[at] = b;
+    rest += sum;
+  }
+}
+
+size_t groups_bytes(int batch) { return 4 * align_up(static_cast<size_t>(batch) * sizeof(int32_t), 256) + 256; }
+
 }  // namespace
 
 extern "C" size_t oscar_pages_workspace_bytes(const oscar_dims_t* dims, int32_t batch, int32_t num_forks) {
@@ -627,6 +782,34 @@ extern "C" oscar_status_t oscar_pages_compact(const oscar_dims_t* dims, int32_t 
   e = launch_pdl(compact_apply_kernel, dim3(batch + movers), dim3(256), 0, s, t, p,
                  static_cast<const int32_t*>(words(l.from)), static_cast<const int32_t*>(words(l.to)),
                  static_cast<const int32_t*>(words(l.rank)), static_cast<const int32_t*>(words(l.info)));
+  return e == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
+}
+
+extern "C" size_t oscar_pages_groups_workspace_bytes(const oscar_dims_t* dims, int32_t batch) {
+  return check_pages(dims, batch, 0, nullptr) == OSCAR_OK ? groups_bytes(batch) : 0;
+}
+
+extern "C" oscar_status_t oscar_pages_groups(const oscar_dims_t* dims, int32_t batch, int32_t min_pages, int32_t max_groups,
+                                             const int32_t* page_table, const int32_t* seq_lens, int32_t* members,
+                                             int32_t* group_start, int32_t* prefix_lens, void* workspace,
+                                             size_t workspace_bytes, void* stream) {
+  const oscar_status_t st = check_pages(dims, batch, 0, nullptr);
+  if (st != OSCAR_OK) return st;
+  if (min_pages < 1 || max_groups < 1) return OSCAR_ERR_INVALID_ARG;
+  if (batch == 0) return OSCAR_OK;
+  if (!page_table || !seq_lens || !members || !group_start || !prefix_lens || !workspace ||
+      reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+    return OSCAR_ERR_INVALID_ARG;
+  if (workspace_bytes < groups_bytes(batch)) return OSCAR_ERR_WORKSPACE;
+  const Tables t{const_cast<int32_t*>(page_table), const_cast<int32_t*>(seq_lens), nullptr, batch, dims->num_pages,
+                 dims->max_pages_per_seq};
+  const size_t each = align_up(static_cast<size_t>(batch) * sizeof(int32_t), 256);
+  auto words = [&](int i) { return reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + i * each); };
+  groups_find_kernel<<<batch, 256, 0, as_stream(stream)>>>(t, min_pages, words(0), words(1));
+  if (cudaGetLastError() != cudaSuccess) return OSCAR_ERR_CUDA;
+  const cudaError_t e = launch_pdl(groups_list_kernel, dim3(1), dim3(kPlanThreads), 0, as_stream(stream), batch,
+                                   max_groups, static_cast<const int32_t*>(words(0)), static_cast<const int32_t*>(words(1)),
+                                   words(2), words(3), members, group_start, prefix_lens);
   return e == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
