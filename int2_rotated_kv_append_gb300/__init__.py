@@ -403,56 +403,69 @@ class Rope:
         self.rotary_dim, self.interleaved = int(rotary_dim), bool(interleaved)
         self.magnitude = own if magnitude is None else float(magnitude)
         self.c = oscar_rope_t(self.rotary_dim, int(self.interleaved), self.magnitude, self.turns.data_ptr())
+        self.ref = ctypes.byref(self.c)
 
 
 _TYPES = {torch.bfloat16: OSCAR_TYPE_BF16, torch.float16: OSCAR_TYPE_FP16, torch.float32: OSCAR_TYPE_FP32}
 
 
-def _rows(t, heads, dim, what):
+# Checks of a call's tensors, each with one look at the tensor: the host's part of a small call is most of its time.  Tensors of
+# one call are on the current device, whose stream and kernels it uses (`now`).
+
+
+def _rows(t, tokens, heads, dim, dtype, now, what):
     """Pointer and stride of rows [T][heads][dim] that may be slices of longer rows; (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim):
-        raise ValueError(f"{what} is [tokens][{heads}][{dim}]")
-    if t.numel() == 0:
-        return t.data_ptr() or 16, heads * dim
-    if t.stride(2) != 1 or t.stride(1) != dim and heads > 1:
+    if t.dtype is not dtype or t.get_device() != now or t.shape != (tokens, heads, dim):
+        raise ValueError(f"{what} is {dtype} [{tokens}][{heads}][{dim}] on the current CUDA device ({now})")
+    row, head, one = t.stride()
+    if tokens < 2:
+        row = heads * dim
+        if tokens == 0:
+            return t.data_ptr() or 16, row
+    if one != 1 or head != dim and heads > 1:
         raise ValueError(f"{what}: the heads of a row are contiguous")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * dim
+    return t.data_ptr(), row
 
 
-def _same_device(*tensors):
-    """The tensors of one call are on the current device: its stream and kernels are."""
-    now = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != now:
-            raise ValueError(f"tensors of a call are on the current CUDA device ({now})")
+def _ints(t, n, now, what):
+    """Pointer of an int32 array of n entries or more."""
+    if t.dtype is not torch.int32 or t.numel() < n or t.get_device() != now or not t.is_contiguous():
+        raise ValueError(f"{what} is contiguous int32 with {n} entries or more on the current CUDA device ({now})")
+    return t.data_ptr()
 
 
-def _int32(t, n, what):
-    if t is not None and (t.dtype != torch.int32 or t.numel() < n):
-        raise ValueError(f"{what} is int32 with {n} entries or more")
+def _here(t, now, what):
+    """Pointer of a buffer."""
+    if t.get_device() != now or not t.is_contiguous():
+        raise ValueError(f"{what} is contiguous on the current CUDA device ({now})")
+    return t.data_ptr()
+
+
+def _rope(rope, now):
+    if rope.turns.get_device() != now:
+        raise ValueError(f"the Rope is on the current CUDA device ({now})")
+    return rope.ref
 
 
 def oscar_rope(dims, rope, positions, q, k, q_out, k_out, stream=None):
     """Rotate q [T][Hq][D] and k [T][Hkv][D] (bf16, fp16 or fp32; either may be None, with its output) by positions
     (int32 [T]) into q_out and k_out, which may be q and k themselves.  Rows may be slices of longer ones."""
-    d = _dims(dims)
-    some = q if q is not None else k
+    d, now = _dims(dims), torch.cuda.current_device()
+    some = k if q is None else q
     if some is None:
         raise ValueError("q or k is given")
-    tokens, dtype = some.shape[0], some.dtype
-    if dtype not in _TYPES:
+    tokens, dtype, hq, hkv, dim = some.shape[0], some.dtype, d.num_q_heads, d.num_kv_heads, d.head_dim
+    code = _TYPES.get(dtype)
+    if code is None:
         raise ValueError("rows are bfloat16, float16 or float32")
-    for t in (q, k, q_out, k_out):
-        if t is not None and (t.dtype != dtype or t.shape[0] != tokens):
-            raise ValueError("rows of q, k and the outputs have one type and number")
-    _int32(positions, tokens, "positions")
-    _same_device(positions, q, k, q_out, k_out, rope.turns)
-    ptrs = [x for t, h, n in ((q, d.num_q_heads, "q"), (k, d.num_kv_heads, "k"), (q_out, d.num_q_heads, "q_out"),
-                              (k_out, d.num_kv_heads, "k_out")) for x in _rows(t, h, d.head_dim, n)]
-    _check(lib.oscar_rope(ctypes.byref(d), ctypes.byref(rope.c), _TYPES[dtype], int(tokens), _ptr(positions), *ptrs,
-                          _stream(stream)), "oscar_rope")
+    qp, qs = _rows(q, tokens, hq, dim, dtype, now, "q")
+    kp, ks = _rows(k, tokens, hkv, dim, dtype, now, "k")
+    qop, qos = _rows(q_out, tokens, hq, dim, dtype, now, "q_out")
+    kop, kos = _rows(k_out, tokens, hkv, dim, dtype, now, "k_out")
+    _check(lib.oscar_rope(d, _rope(rope, now), code, tokens, _ints(positions, tokens, now, "positions"), qp, qs, kp, ks, qop,
+                          qos, kop, kos, _stream(stream)), "oscar_rope")
 
 
 def oscar_kv8_rope_append(dims, rope, kv_format, batch, max_tokens_per_seq, q, k, v, t_start, positions, page_table, seq_lens,
@@ -460,23 +473,19 @@ def oscar_kv8_rope_append(dims, rope, kv_format, batch, max_tokens_per_seq, q, k
     """oscar_kv8_append of keys that are rotated on the way, and the queries q [T][Hq][D] of the same tokens rotated into
     q_out (both may be None; q_out may be q).  ``positions``: int32 [T], or None for the positions in the sequences.
     Rows of q, k, v and q_out may be slices of longer ones."""
-    d = _dims(dims)
-    tokens = k.shape[0]
-    for t in (q, k, v, q_out):
-        if t is not None and (t.dtype != torch.bfloat16 or t.shape[0] != tokens):
-            raise ValueError("q, k, v and q_out are bfloat16 rows, one per token")
-    _int32(positions, tokens, "positions")
-    _int32(t_start, batch + 1, "t_start")
-    _int32(seq_lens, batch, "seq_lens")
-    _int32(granted, batch, "granted")
-    _int32(page_table, batch * d.max_pages_per_seq, "page_table")
-    _same_device(q, k, v, t_start, positions, page_table, seq_lens, kv8_pages, kv8_scales, q_out, granted, rope.turns)
-    qp, ks, vp, op = (_rows(t, h, d.head_dim, n) for t, h, n in ((q, d.num_q_heads, "q"), (k, d.num_kv_heads, "k"),
-                                                                 (v, d.num_kv_heads, "v"), (q_out, d.num_q_heads, "q_out")))
-    _check(lib.oscar_kv8_rope_append(ctypes.byref(d), ctypes.byref(rope.c), int(kv_format), int(batch), int(tokens),
-                                     int(max_tokens_per_seq), *qp, *ks, *vp, _ptr(t_start), _ptr(positions),
-                                     _ptr(page_table), _ptr(seq_lens), _ptr(granted), _ptr(kv8_pages), _ptr(kv8_scales), *op,
-                                     _stream(stream)), "oscar_kv8_rope_append")
+    d, now = _dims(dims), torch.cuda.current_device()
+    tokens, hq, hkv, dim, bf16 = k.shape[0], d.num_q_heads, d.num_kv_heads, d.head_dim, torch.bfloat16
+    qp, qs = _rows(q, tokens, hq, dim, bf16, now, "q")
+    kp, ks = _rows(k, tokens, hkv, dim, bf16, now, "k")
+    vp, vs = _rows(v, tokens, hkv, dim, bf16, now, "v")
+    op, os_ = _rows(q_out, tokens, hq, dim, bf16, now, "q_out")
+    _check(lib.oscar_kv8_rope_append(
+        d, _rope(rope, now), kv_format, batch, tokens, max_tokens_per_seq, qp, qs, kp, ks, vp, vs,
+        _ints(t_start, batch + 1, now, "t_start"),
+        None if positions is None else _ints(positions, tokens, now, "positions"),
+        _ints(page_table, batch * d.max_pages_per_seq, now, "page_table"), _ints(seq_lens, batch, now, "seq_lens"),
+        None if granted is None else _ints(granted, batch, now, "granted"), _here(kv8_pages, now, "kv8_pages"),
+        _here(kv8_scales, now, "kv8_scales"), op, os_, _stream(stream)), "oscar_kv8_rope_append")
 
 
 def _nbytes(t) -> int:
@@ -545,20 +554,18 @@ def oscar_kv8_decode_shared(dims, kv_format, batch, max_seq_len, max_prefix_len,
     """One decode step over the 8-bit cache of the sequences ``members``, group after group (group_start [groups + 1]): the
     first prefix_lens[g] tokens, which group g shares, are attended once for all of it.  Writes the members' rows of bf16
     out [batch][Hq][D]."""
-    d = _dims(dims)
-    groups = prefix_lens.numel()
-    shape = (batch, d.num_q_heads, d.head_dim)
-    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or q.shape != shape or out.shape != shape:
-        raise ValueError("q and out are bfloat16 [batch][Hq][D]")
-    for t, n, what in ((members, 0, "members"), (group_start, groups + 1, "group_start"), (prefix_lens, 0, "prefix_lens"),
-                       (seq_lens, batch, "seq_lens"), (page_table, batch * d.max_pages_per_seq, "page_table")):
-        _int32(t, n, what)
-    _same_device(q, kv8_pages, kv8_scales, page_table, seq_lens, members, group_start, prefix_lens, out, workspace)
-    _check(lib.oscar_kv8_decode_shared(ctypes.byref(d), int(kv_format), int(batch), int(max_seq_len), int(max_prefix_len),
-                                       int(max_own_len), int(members.numel()), int(groups), _ptr(q), _ptr(kv8_pages),
-                                       _ptr(kv8_scales), _ptr(page_table), _ptr(seq_lens), _ptr(members), _ptr(group_start),
-                                       _ptr(prefix_lens), float(sm_scale), _ptr(out), _ptr(workspace), _nbytes(workspace),
-                                       _stream(stream)), "oscar_kv8_decode_shared")
+    d, now, groups = _dims(dims), torch.cuda.current_device(), prefix_lens.numel()
+    qp, _ = _rows(q, batch, d.num_q_heads, d.head_dim, torch.bfloat16, now, "q")
+    op, _ = _rows(out, batch, d.num_q_heads, d.head_dim, torch.bfloat16, now, "out")
+    if not (q.is_contiguous() and out.is_contiguous()):
+        raise ValueError("q and out are contiguous")
+    _check(lib.oscar_kv8_decode_shared(
+        d, kv_format, batch, max_seq_len, max_prefix_len, max_own_len, members.numel(), groups, qp,
+        _here(kv8_pages, now, "kv8_pages"), _here(kv8_scales, now, "kv8_scales"),
+        _ints(page_table, batch * d.max_pages_per_seq, now, "page_table"), _ints(seq_lens, batch, now, "seq_lens"),
+        _ints(members, 0, now, "members"), _ints(group_start, groups + 1, now, "group_start"),
+        _ints(prefix_lens, 0, now, "prefix_lens"), sm_scale, op, _here(workspace, now, "workspace"), _nbytes(workspace),
+        _stream(stream)), "oscar_kv8_decode_shared")
 
 
 def _pools(pools, num_pages):
@@ -635,15 +642,13 @@ def oscar_pages_groups(dims, min_pages, page_table, seq_lens, members, group_sta
     """The sequences whose first min_pages pages are full and the same, as groups for oscar_kv8_decode_shared: members
     (int32 [batch]), group_start (int32 [groups + 1]) and prefix_lens (int32 [groups]) are written; what is in no group of
     two, or beyond groups - 1 of them, is the last group, without a prefix."""
-    d = _dims(dims)
-    batch, room = seq_lens.shape[0], prefix_lens.numel()
-    for t, n, what in ((members, batch, "members"), (group_start, room + 1, "group_start"), (prefix_lens, 1, "prefix_lens"),
-                       (seq_lens, batch, "seq_lens"), (page_table, batch * d.max_pages_per_seq, "page_table")):
-        _int32(t, n, what)
-    _same_device(page_table, seq_lens, members, group_start, prefix_lens, workspace)
-    _check(lib.oscar_pages_groups(ctypes.byref(d), int(batch), int(min_pages), int(room), _ptr(page_table), _ptr(seq_lens),
-                                  _ptr(members), _ptr(group_start), _ptr(prefix_lens), _ptr(workspace), _nbytes(workspace),
-                                  _stream(stream)), "oscar_pages_groups")
+    d, now = _dims(dims), torch.cuda.current_device()
+    batch, room = seq_lens.numel(), prefix_lens.numel()
+    _check(lib.oscar_pages_groups(
+        d, batch, min_pages, room, _ints(page_table, batch * d.max_pages_per_seq, now, "page_table"),
+        _ints(seq_lens, batch, now, "seq_lens"), _ints(members, batch, now, "members"),
+        _ints(group_start, room + 1, now, "group_start"), _ints(prefix_lens, 1, now, "prefix_lens"),
+        _here(workspace, now, "workspace"), _nbytes(workspace), _stream(stream)), "oscar_pages_groups")
 
 
 def oscar_test_stall_page_waits(cycles: int) -> None:
