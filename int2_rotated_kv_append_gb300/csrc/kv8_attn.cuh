@@ -90,14 +90,14 @@ __device__ __forceinline__ void store_out4(__nv_bfloat16* out, float4 o, float l
       make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
-// One warp: partials first, first + step, ... of n (o_at(i) [D] unnormalised, ml_at(i) = m, l, r, -; -infinity for the units of a
-// partial of nothing): l and four channels r of lane's c4 = lane % (D / 4), in units of the largest m and m + r of all n, the
+// One warp: partials first, first + step, ... of n (o_at(i): the four channels of c4 = lane % (D / 4), unnormalised; ml_at(i) =
+// m, l, r, -; -infinity for the units of a partial of nothing): l and four channels r, in units of the largest m and m + r of all n, the
 // latter e above the former.  Eight partials are in flight at once, the first of them while the maxima are found.
 template <int D, typename OAt, typename MlAt>
 __device__ __forceinline__ void merge_parts(OAt o_at, MlAt ml_at, int n, int first, int step, int lane, float& l, float4& r,
                                             float& e) {
   constexpr int kSub = 128 / D, kFly = 8;  // D = 64: two half warps take every second partial
-  const int sub = lane / (D / 4), c4 = lane % (D / 4);
+  const int sub = lane / (D / 4);
   l = 0.f;
   r = make_float4(0.f, 0.f, 0.f, 0.f);
   float4 x[kFly], p[kFly];
@@ -109,7 +109,7 @@ __device__ __forceinline__ void merge_parts(OAt o_at, MlAt ml_at, int n, int fir
       x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < n) {
         p[k] = *reinterpret_cast<const float4*>(ml_at(i));
-        x[k] = *reinterpret_cast<const float4*>(o_at(i) + 4 * c4);
+        x[k] = *reinterpret_cast<const float4*>(o_at(i));
       }
     }
   };
@@ -160,7 +160,8 @@ __device__ __forceinline__ void merge_parts(OAt o_at, MlAt ml_at, int n, int fir
 template <int D>
 __device__ __forceinline__ void merge_part(const float* o, const float* ml, int n, int first, int step, int lane,
                                            float& l, float4& r, float& e) {
-  merge_parts<D>([&](int i) { return o + static_cast<size_t>(i) * D; }, [&](int i) { return ml + 4 * i; }, n, first, step, lane,
+  const int c4 = lane % (D / 4);
+  merge_parts<D>([&](int i) { return o + static_cast<size_t>(i) * D + 4 * c4; }, [&](int i) { return ml + 4 * i; }, n, first, step, lane,
                  l, r, e);
 }
 

@@ -105,8 +105,8 @@ struct Geo {
   static constexpr uint32_t kBars = kQ + MT * kOp;
   static_assert(!kQStage || kOp == kStage, "Q has the place of a stage");
   // raw full, raw empty | K full, K empty, V full, V empty (2 each) | S full, S free, P full, PV done (2 each) |
-  // info full, info free | Q in TMEM | end
-  static constexpr int kNumBars = 2 * kRing + 8 + 8 + 2 * kInfo + 2;
+  // info full, info free | Q in TMEM | end | Q's rows
+  static constexpr int kNumBars = 2 * kRing + 8 + 8 + 2 * kInfo + 3;
   static constexpr bool kQTmem = MT == 1;
   static constexpr uint32_t kScale = kBars + ((kNumBars * 8 + 15) & ~15);  // [kInfo] BlockInfo
   static constexpr uint32_t kQs = kScale + kInfo * sizeof(BlockInfo);
@@ -124,10 +124,10 @@ struct ExtArgs {
 
 // Kernels over shared prefixes (SHARED): a tile's rows are the queries of one group's members, each at the end of the prefix.
 struct SharedArgs {
-  ExtArgs e;   // part_o, part_ml: [items x KV heads x rows of a tile]; ns, bps, tiles unused
+  ExtArgs e;   // part_o, part_ml: [items x KV heads x rows of a tile], 16-byte chunk q of row r at q ^ (r % 8); ns, bps, tiles unused
   Groups g;
   int4* info;  // [num_members]: first item of the member's group, its tiles and splits, the member's place in it
-  int sms;
+  bool first, last;  // of the two kernels that run beside one another
 };
 
 // A tile's rows and the pages they see.
@@ -167,74 +167,67 @@ __device__ __forceinline__ Tile tile_of(const AttnArgs& a, int b, int tile) {
 
 // What a block of the prefix kernel does: a tile of a group's rows (TM at most) over a range of the prefix's blocks.
 struct Item {
-  int group, start, n, prefix;       // the group
-  int first, tiles, splits, bps;     // its first item, tiles and splits, blocks of a split
+  int start, n, prefix;           // the group: first member, members, tokens
+  int first, tiles, splits, bps;  // its first item, tiles and splits, blocks of a split
   int tile, split;
   bool ok, bad;
 };
 
-// The item of block x, found by every warp for itself.  Every (tile, split) of every group is one, and a split's length is the
-// same for all groups: the shortest with which the items fit into whole waves of one block per SM, as many waves as take least,
-// a wave being as long as its blocks and kExtra more for start and end.
+// The item of block x of `limit` (at least as many as there are tiles).  Every (tile, split) of every group is one, and a split's
+// length is the same for all groups: the shortest, but at least kLeast, with which there are `limit` items at most.  The groups'
+// tiles and blocks go into `table` (shared memory), and every warp finds the length for itself.
+constexpr int kTable = 2048;  // groups; more are read again
 template <int TM>
-__device__ __forceinline__ Item item_of(const SharedArgs& s, int x, int limit, int lane) {
-  constexpr int kExtra = 5, kLeast = 4, kWaves = 4;
+__device__ __forceinline__ Item item_of(const SharedArgs& s, int x, int limit, int2* table) {
+  constexpr int kLeast = 4;
   constexpr uint32_t kAll = 0xffffffffu;
-  const int gqa = s.e.a.Hq / s.e.a.H;
+  const int lane = threadIdx.x & 31, gqa = s.e.a.Hq / s.e.a.H;
   Item it{};
-  // a lane's group of 32: tiles and blocks; nothing where there is no group, no member or no prefix
-  auto look = [&](int g, int& start, int& n, int& prefix, int& tiles, int& blocks) {
-    start = n = prefix = tiles = blocks = 0;
-    bool fine = true;
-    if (g < s.g.num_groups) {
-      fine = group_of(s.g, g, start, n, prefix);
-      blocks = (prefix / kPageSize + kBlkPages - 1) / kBlkPages;
-      tiles = fine && blocks > 0 ? static_cast<int>((static_cast<long long>(n) * gqa + TM - 1) / TM) : 0;
-    }
-    return fine;
+  auto look = [&](int g, bool& fine) {
+    int start, n, prefix;
+    fine = group_of(s.g, g, start, n, prefix);
+    const int blocks = (prefix / kPageSize + kBlkPages - 1) / kBlkPages;
+    const int tiles = fine && blocks > 0 ? static_cast<int>((static_cast<long long>(n) * gqa + TM - 1) / TM) : 0;
+    return make_int2(tiles, tiles > 0 ? blocks : 0);
   };
-  int start, n, prefix, tiles, blocks;
-  it.bad = __any_sync(kAll, !look(lane, start, n, prefix, tiles, blocks));
-  int all_tiles = __reduce_add_sync(kAll, tiles), longest = __reduce_max_sync(kAll, tiles > 0 ? blocks : 0);
-  for (int g = 32; g < s.g.num_groups; g += 32) {
-    int a0, a1, a2, t, b;
-    it.bad = __any_sync(kAll, !look(g + lane, a0, a1, a2, t, b)) || it.bad;
-    all_tiles += __reduce_add_sync(kAll, t);
-    longest = max(longest, __reduce_max_sync(kAll, t > 0 ? b : 0));
+  bool bad = false;
+  for (int g = threadIdx.x; g < s.g.num_groups; g += blockDim.x) {
+    bool fine;
+    const int2 v = look(g, fine);
+    bad = bad || !fine;
+    if (g < kTable) table[g] = v;
   }
-  if (it.bad || all_tiles == 0) return it;
-  auto items = [&](int bps) {
-    int sum = __reduce_add_sync(kAll, tiles > 0 ? tiles * ((blocks + bps - 1) / bps) : 0);
-    for (int g = 32; g < s.g.num_groups; g += 32) {
-      int a0, a1, a2, t, b;
-      look(g + lane, a0, a1, a2, t, b);
-      sum += __reduce_add_sync(kAll, t > 0 ? t * ((b + bps - 1) / bps) : 0);
-    }
-    return sum;
-  };
-  int best = 0;
-  for (int w = 1; w <= kWaves; ++w) {
-    const int room = min(limit, w * s.sms / s.e.a.H);
-    if (room < all_tiles && (w < kWaves || it.bps > 0)) continue;
-    const int use = room < all_tiles ? limit : room;  // (the last: as many waves as it takes)
-    int lo = 1, hi = max(longest, 1);
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (items(mid) <= use) hi = mid;
-      else lo = mid + 1;
-    }
-    const int bps = max(lo, kLeast), cost = w * (bps + kExtra);
-    if (it.bps == 0 || cost < best) {
-      best = cost;
-      it.bps = bps;
-    }
-    if (room == limit) break;
+  it.bad = __syncthreads_or(bad);
+  if (it.bad) return it;
+  bool unused;
+  auto group = [&](int g) { return g < kTable ? table[g] : look(g, unused); };
+  int longest = 0, tiles = 0;
+  long long all = 0;  // blocks
+  for (int g = lane; g < s.g.num_groups; g += 32) {
+    const int2 v = group(g);
+    tiles += v.x;
+    longest = max(longest, v.y);
+    all += static_cast<long long>(v.x) * v.y;
   }
+  tiles = __reduce_add_sync(kAll, tiles);
+  longest = __reduce_max_sync(kAll, longest);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(kAll, all, o);
+  if (tiles == 0) return it;
+  // a lane tries one of the 32 shortest lengths that might do; if none does, one that does for sure
+  const int lo = max(min(kLeast, longest), static_cast<int>((all + limit - 1) / limit)), mine = lo + lane;
+  long long sum = 0;
+  for (int g = 0; g < s.g.num_groups; ++g) {
+    const int2 v = group(g);
+    sum += static_cast<long long>(v.x) * ((v.y + mine - 1) / mine);
+  }
+  const uint32_t fits = __ballot_sync(kAll, sum <= limit);
+  it.bps = fits != 0 ? lo + __ffs(fits) - 1 : tiles < limit ? static_cast<int>((all + limit - tiles - 1) / (limit - tiles)) : longest;
   int before = 0;
-  for (int g = 0; g < s.g.num_groups; g += 32) {
-    if (g > 0) look(g + lane, start, n, prefix, tiles, blocks);
-    const int splits = tiles > 0 ? (blocks + it.bps - 1) / it.bps : 0;
-    int sum = tiles * splits;
+  for (int g0 = 0; g0 < s.g.num_groups; g0 += 32) {
+    const int2 v = g0 + lane < s.g.num_groups ? group(g0 + lane) : make_int2(0, 0);
+    const int splits = (v.y + it.bps - 1) / it.bps;
+    int sum = v.x * splits;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(kAll, sum, o);
@@ -243,11 +236,8 @@ __device__ __forceinline__ Item item_of(const SharedArgs& s, int x, int limit, i
     const uint32_t behind = __ballot_sync(kAll, before + sum > x);
     if (behind != 0) {
       const int at = __ffs(behind) - 1;
-      it.group = g + at;
-      it.start = __shfl_sync(kAll, start, at);
-      it.n = __shfl_sync(kAll, n, at);
-      it.prefix = __shfl_sync(kAll, prefix, at);
-      it.tiles = __shfl_sync(kAll, tiles, at);
+      group_of(s.g, g0 + at, it.start, it.n, it.prefix);
+      it.tiles = __shfl_sync(kAll, v.x, at);
       it.splits = __shfl_sync(kAll, splits, at);
       it.first = before + __shfl_sync(kAll, sum, at) - it.tiles * it.splits;
       it.tile = (x - it.first) % it.tiles;
@@ -271,6 +261,12 @@ __device__ __forceinline__ void reg_dec() {
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w));
+}
+// A copy from shared to global memory (16-byte aligned, a multiple of 16 bytes), to its end.
+__device__ __forceinline__ void bulk_s2g_wait(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -302,19 +298,21 @@ __device__ __forceinline__ void extend_body(const Args& args) {
   const int h = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gqa = a.Hq / a.H;
-  grid_dep_wait();
+  bool waits = true;
+  if constexpr (SHARED) waits = args.first;
+  if (waits) grid_dep_wait();
   grid_dep_launch_dependents();
   constexpr int kRowsOfTile = MT * 128 / PARTS;
   int split, tile, b, bps;
   Tile T;
   if constexpr (SHARED) {
-    const Item it = item_of<kRowsOfTile>(args, blockIdx.x, gridDim.x, lane);
+    const Item it = item_of<kRowsOfTile>(args, blockIdx.x, gridDim.x, reinterpret_cast<int2*>(sm));
     if (it.bad && blockIdx.x == 0 && h == 0 && tid == 0) record_error(OSCAR_DEVERR_POSITION);
     if (!it.ok) return;
     split = it.split;
     tile = it.tile;
     bps = it.bps;
-    b = max(member_of(args.g, a.batch, it.start), 0);  // the sequence whose pages are read
+    b = in_batch(__ldg(args.g.members + it.start), a.batch);  // the sequence whose pages are read
     T.q0 = it.start;
     T.n = it.n;
     T.L = it.prefix;
@@ -350,7 +348,8 @@ __device__ __forceinline__ void extend_body(const Args& args) {
   auto bar = [&](int i) { return smem_u32(bars + i); };
   constexpr int kRawFull = 0, kRawEmpty = G::kRing, kOpFull = 2 * G::kRing, kOpEmpty = kOpFull + 4,
                 kSFull = kOpEmpty + 4, kSFree = kSFull + 2, kPFull = kSFree + 2, kPvDone = kPFull + 2, kInfoFull = kPvDone + 2,
-                kInfoFree = kInfoFull + kInfo, kQFull = kInfoFree + kInfo, kEnd = kQFull + 1;
+                kInfoFree = kInfoFull + kInfo, kQFull = kInfoFree + kInfo, kEnd = kQFull + 1,
+                kQRaw = kEnd + 1;
   // (operand barriers: 2 x side + buffer)
   BlockInfo* infos = reinterpret_cast<BlockInfo*>(sm + G::kScale);
   float* q_scale = reinterpret_cast<float*>(sm + G::kQs);
@@ -378,49 +377,48 @@ __device__ __forceinline__ void extend_body(const Args& args) {
     }
     mbar_init(bar(kQFull), 128 * active);
     mbar_init(bar(kEnd), 2);
+    mbar_init(bar(kQRaw), 1);
     mbar_init_fence();
   }
   __syncthreads();
   const int wg = warp >> 2;
   const bool fetches = warp == kFetchK || warp == kFetchV;  // these start at once; the others get Q and TMEM ready
   if (warp == kQkWarp) umma::tmem_alloc(sb + G::kMisc, 512);
-  // Q as fp16, K-major with the 128-byte swizzle: a lane takes 8 channels of a row, and every load is in flight at once
-  if (wg < 3) {
-    constexpr int kLanes = D / 8, kAtOnce = 12 * 32 / kLanes;  // lanes of a row; rows of one round of the 12 warps
-    constexpr int kRounds = (MT * 128 / PARTS + kAtOnce - 1) / kAtOnce;
-    const int c = lane % kLanes, r0 = tid / kLanes;
-    int x = T.r0 + r0, i = x / gqa, hd = x - i * gqa;
-    const __nv_bfloat16* src = a.q + (static_cast<size_t>(SHARED ? 0 : T.q0) * a.Hq + h * gqa) * D + 8 * c;
-    uint4 v[kRounds];
-    int seq[kRounds];  // SHARED: the rows' sequences (all loaded before the rows)
-    if constexpr (SHARED) {
-#pragma unroll
-      for (int k = 0; k < kRounds; ++k)
-        seq[k] = r0 + k * kAtOnce < T.rows ? max(member_of(args.g, a.batch, T.q0 + (x + k * kAtOnce) / gqa), 0) : 0;
+  // Q as fp16, K-major with the 128-byte swizzle, by the warps of the softmax.  The rows come by copies, one for each position (or
+  // member) and its query heads, into the memory of the V operands; then a lane takes 8 channels of a row, row after row.  (Little
+  // code: what runs once waits for its instructions more than for anything else, all SMs fetching the same ones.  With a register
+  // for every row's load this took 4 us.)
+  if (wg < MT) {
+    constexpr int kLanes = D / 8, kAtOnce = MT * 128 / kLanes;  // lanes of a row; rows of one round
+    constexpr int kRounds = (kRowsOfTile + kAtOnce - 1) / kAtOnce;
+    const uint32_t stage = sb + G::kV;
+    if (tid == 0) mbar_arrive_expect_tx(bar(kQRaw), T.rows * D * 2);
+    if (const int i = T.r0 / gqa + tid; i <= (T.r0 + T.rows - 1) / gqa) {
+      const int x0 = max(i * gqa, T.r0), x1 = min(i * gqa + gqa, T.r0 + T.rows);
+      size_t row = T.q0 + i;
+      if constexpr (SHARED) row = in_batch(__ldg(args.g.members + row), a.batch);
+      bulk_g2s(stage + (x0 - T.r0) * (D * 2), a.q + (row * a.Hq + h * gqa + (x0 - i * gqa)) * D, (x1 - x0) * D * 2, bar(kQRaw));
     }
-#pragma unroll
+    __syncwarp();
+    const bool there = mbar_wait_bounded(bar(kQRaw), 0);
+    if (!there) record_error(OSCAR_DEVERR_TIMEOUT);
+    const int c = lane % kLanes;
+#pragma unroll 4
     for (int k = 0; k < kRounds; ++k) {
-      v[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (r0 + k * kAtOnce < T.rows)
-        v[k] = __ldg(reinterpret_cast<const uint4*>(src + (static_cast<size_t>(SHARED ? seq[k] : i) * a.Hq + hd) * D));
-      i += kAtOnce / gqa;
-      hd += kAtOnce % gqa;
-      if (hd >= gqa) {
-        hd -= gqa;
-        ++i;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kRounds; ++k) {
-      const int r = r0 + k * kAtOnce;
-      uint32_t mx = __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
-                             __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu));
+      const int r = tid / kLanes + k * kAtOnce;
+      uint32_t in[4] = {0u, 0u, 0u, 0u};
+      if (r < T.rows && there)
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(in[0]), "=r"(in[1]), "=r"(in[2]), "=r"(in[3])
+                     : "r"(stage + r * (D * 2) + c * 16)
+                     : "memory");
+      uint32_t mx = __vmaxu2(__vmaxu2(in[0] & 0x7fff7fffu, in[1] & 0x7fff7fffu),
+                             __vmaxu2(in[2] & 0x7fff7fffu, in[3] & 0x7fff7fffu));
 #pragma unroll
       for (int o = 1; o < kLanes; o <<= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       mx = max(mx & 0xffffu, mx >> 16);
       const int e = min(max(static_cast<int>(mx >> 7) - 127, -126), 126);
       const float inv = pow2i(-e);
-      const uint32_t in[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
       uint32_t y[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -436,13 +434,16 @@ __device__ __forceinline__ void extend_body(const Args& args) {
       }
     }
   }
-  if (!fetches) {
+  // Q and TMEM are there: for all but the fetching warps, those that expand codes after a first round (below).
+  auto q_ready = [&]() {
     fence_async();
     umma::fence_before_sync();
     asm volatile("bar.sync 1, %0;" ::"n"(kThreads - 64) : "memory");
     umma::fence_after_sync();
-  }
-  const uint32_t tmem = fetches ? 0u : misc[0];
+  };
+  const bool expands = wg >= MT && wg < 3;
+  if (!fetches && !expands) q_ready();
+  const uint32_t tmem = fetches || expands ? 0u : misc[0];
   // logits, weights, accumulators
   const uint32_t s_tmem[2] = {tmem, MT == 2 ? tmem : tmem + 384};
   const uint32_t p_tmem[2] = {tmem + 128, tmem + 192};
@@ -477,7 +478,7 @@ __device__ __forceinline__ void extend_body(const Args& args) {
       const int last_r = min(T.rows, wg * 128 + 128) - 1;  // rows behind it are zeros and not stored
       const int x_row = (T.r0 + min(r, last_r)) / gqa;
       int pos = T.L - T.n + x_row;
-      if constexpr (SHARED) pos = min(clamped_len(a, max(member_of(args.g, a.batch, T.q0 + x_row), 0)), T.L) - 1;
+      if constexpr (SHARED) pos = min(max(__ldg(a.seq_lens + in_batch(__ldg(args.g.members + T.q0 + x_row), a.batch)), 0), T.L) - 1;
       const int after = a.window > 0 ? max(pos - a.window, -1) : -1;  // visible: behind it, or a sink
       if (PARTS == 2) {  // the other part's weights are 0
         uint32_t z[32];
@@ -676,6 +677,7 @@ __device__ __forceinline__ void extend_body(const Args& args) {
       if (ok) ok = mbar_wait_bounded(bar(kPvDone + (MT == 2 ? wg : 0)), (cnt - 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) record_error(OSCAR_DEVERR_TIMEOUT);
+      if (SHARED && MT == 2 && active == 2) asm volatile("bar.sync 3, 256;" ::: "memory");  // the other row tile's last product too
       umma::fence_after_sync();
       const bool single = !SHARED && T.blocks <= bps;
       const bool store = r < T.rows;
@@ -720,34 +722,57 @@ __device__ __forceinline__ void extend_body(const Args& args) {
       float f, g;
       pow2_pair(u, f, g);
       const float inv = l == 0.f ? 0.f : f / l;
+      if constexpr (SHARED && PARTS == 1) {
+        // Partials, by way of the operands' memory (no product reads it any more): a warp's rows lie one after another there and in the
+        // partials, and go in one copy (a lane's own stores, of 16 bytes of 32 rows at once, took twice as long).
+        // 16-byte chunk q of row r is at q ^ (r % 8), in both.
+        const uint32_t stage = sb + G::kK + static_cast<uint32_t>(r) * (D * 4);
 #pragma unroll 2
-      for (int c = part * (D / 32); c < (PARTS == 2 ? (part + 1) * (D / 32) : D / 16); ++c) {
-        uint32_t o[16];
-        __syncwarp();
-        umma::tmem_ld16(o_tmem[wg] + t_lane + 16 * c, o);
-        umma::tmem_ld_wait();
-        if (PARTS == 2) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            o[e] = __float_as_uint((none0 ? 0.f : __uint_as_float(o[e]) * u0 * u1) +
-                                   (none1 ? 0.f : theirs[16 * (c - part * (D / 32)) + e] * v0 * v1));
-        }
-        if (store && single) {
-          uint32_t y[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            y[e] = l == 0.f ? 0u : bfloat2_bits(__uint_as_float(o[2 * e]) * inv * g, __uint_as_float(o[2 * e + 1]) * inv * g);
-          }
-          uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + 16 * c);
-          dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
-          dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
-        } else if (store) {
-          float4* dst = reinterpret_cast<float4*>(ea.part_o + part_row * D + 16 * c);
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t o[16];
+          __syncwarp();
+          umma::tmem_ld16(o_tmem[wg] + t_lane + 16 * c, o);
+          umma::tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            dst[e] = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                              : make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                            __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+            st_shared_v4(stage + (((4 * c + e) ^ (r & 7)) << 4), l == 0.f ? 0u : o[4 * e], l == 0.f ? 0u : o[4 * e + 1],
+                         l == 0.f ? 0u : o[4 * e + 2], l == 0.f ? 0u : o[4 * e + 3]);
+        }
+        fence_async();
+        __syncwarp();
+        const int rows = min(max(T.rows - (r - lane), 0), 32);
+        if (lane == 0 && rows > 0) bulk_s2g_wait(ea.part_o + part_row * D, stage, rows * D * 4);
+        __syncwarp();
+      } else {
+#pragma unroll 2
+        for (int c = part * (D / 32); c < (PARTS == 2 ? (part + 1) * (D / 32) : D / 16); ++c) {
+          uint32_t o[16];
+          __syncwarp();
+          umma::tmem_ld16(o_tmem[wg] + t_lane + 16 * c, o);
+          umma::tmem_ld_wait();
+          if (PARTS == 2) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              o[e] = __float_as_uint((none0 ? 0.f : __uint_as_float(o[e]) * u0 * u1) +
+                                     (none1 ? 0.f : theirs[16 * (c - part * (D / 32)) + e] * v0 * v1));
+          }
+          if (store && single) {
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              y[e] = l == 0.f ? 0u : bfloat2_bits(__uint_as_float(o[2 * e]) * inv * g, __uint_as_float(o[2 * e + 1]) * inv * g);
+            }
+            uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + 16 * c);
+            dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+            dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+          } else if (store) {
+            float4* dst = reinterpret_cast<float4*>(ea.part_o + part_row * D);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[SHARED ? (4 * c + e) ^ (r & 7) : 4 * c + e] = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                : make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                              __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+          }
         }
       }
       if (store && !single && part == 0)
@@ -771,12 +796,16 @@ __device__ __forceinline__ void extend_body(const Args& args) {
     const uint32_t dst0 = sb + G::kK + (c >> 2) * (kTok * 128) + r0 * 128 + (((2 * (c & 3)) ^ (r0 & 7)) << 4);
     const uint32_t dst1 = sb + G::kK + (c >> 2) * (kTok * 128) + r0 * 128 + (((2 * (c & 3) + 1) ^ (r0 & 7)) << 4);
     bool ok = true;
+    // The first round (y = -1) is for the instruction cache, before any codes are there: it expands whatever lies in the first
+    // stage into the K operands, which the first real rounds overwrite.
 #pragma unroll 1
-    for (int x = 0; x < (MT == 2 ? 2 : 1) * cnt; ++x) {
+    for (int y = -1; y < (MT == 2 ? 2 : 1) * cnt; ++y) {
+      const bool dry = y < 0;
+      const int x = max(y, 0);
       const int j = MT == 2 ? x >> 1 : x, side = MT == 2 ? x & 1 : 2 - wg;
       const int op = 2 * side + (j & 1), rx = G::kWhole ? j : x, st = rx % G::kRing;
-      ok = mbar_wait_bounded(bar(kRawFull + st), (rx / G::kRing) & 1) &&
-           mbar_wait_bounded(bar(kInfoFull + j % kInfo), (j / kInfo) & 1);
+      ok = dry || (mbar_wait_bounded(bar(kRawFull + st), (rx / G::kRing) & 1) &&
+                   mbar_wait_bounded(bar(kInfoFull + j % kInfo), (j / kInfo) & 1));
       if (!ok) break;
       // every load first: the units are independent, and a load waits for nothing but itself
       uint32_t w[kUnits][4];
@@ -786,11 +815,12 @@ __device__ __forceinline__ void extend_body(const Args& args) {
                      : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
                      : "r"(src0 + st * G::kStage + (G::kWhole ? side * (kPageSize * D) : 0) + i * kSrcStep)
                      : "memory");
-      if (MT == 1 || !G::kWhole || side == 1) mbar_arrive(bar(kRawEmpty + st));  // read: the next codes may come
+      if (!dry && (MT == 1 || !G::kWhole || side == 1)) mbar_arrive(bar(kRawEmpty + st));  // read: the next codes may come
       ok = j < 2 || mbar_wait_bounded(bar(kOpEmpty + op), ((j >> 1) - 1) & 1);
       if (!ok) break;
       const BlockInfo& bi = infos[j % kInfo];
-      if (side == 1 && (bi.flags & kTail)) {
+      const uint32_t flags = dry ? 0u : bi.flags;
+      if (side == 1 && (flags & kTail)) {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
           const int r = r0 + i * kStep;
@@ -798,37 +828,41 @@ __device__ __forceinline__ void extend_body(const Args& args) {
             w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;  // any bits: behind the last token, or no page
         }
       }
-      const uint32_t to = (side * 2 + (j & 1)) * G::kOp;  // the K buffers, then the V buffers
+      const uint32_t to = (dry ? side : side * 2 + (j & 1)) * G::kOp;  // the K buffers, then the V buffers
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
         const __half ratio = side == 1 ? bi.v_ratio[(r0 + i * kStep) >> 4] : __ushort_as_half(0x3c00);
         const __half2 f = __half2half2(ratio), f1152 = __hmul2(f, __half2half2(__ushort_as_half(0x6480)));
-        uint32_t y[8];
+        uint32_t v[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) codes_to_f16_scaled<F>(w[i][e], f, f1152, y[2 * e], y[2 * e + 1]);
-        st_shared_v4(dst0 + to + i * (kStep * 128), y[0], y[1], y[2], y[3]);
-        st_shared_v4(dst1 + to + i * (kStep * 128), y[4], y[5], y[6], y[7]);
+        for (int e = 0; e < 4; ++e) codes_to_f16_scaled<F>(w[i][e], f, f1152, v[2 * e], v[2 * e + 1]);
+        st_shared_v4(dst0 + to + i * (kStep * 128), v[0], v[1], v[2], v[3]);
+        st_shared_v4(dst1 + to + i * (kStep * 128), v[4], v[5], v[6], v[7]);
       }
       if (side == 1) {
-        const uint32_t wild = bi.flags & kWild;
+        const uint32_t wild = flags & kWild;
         if (wild) {  // rare: this thread's values once more, as bf16 (exact)
 #pragma unroll 1
           for (int i = 0; i < 2 * kUnits; ++i) {
             const uint32_t at = (i & 1 ? dst1 : dst0) + to + (i >> 1) * (kStep * 128);
-            uint32_t y[4];
+            uint32_t v[4];
             asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                          : "r"(at)
                          : "memory");
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&y[e]));
-              y[e] = bfloat2_bits(x.x, x.y);
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[e]));
+              v[e] = bfloat2_bits(f.x, f.y);
             }
-            st_shared_v4(at, y[0], y[1], y[2], y[3]);
+            st_shared_v4(at, v[0], v[1], v[2], v[3]);
           }
         }
-        if (pt == 0) misc[1 + (j & 1)] = wild;
+        if (pt == 0 && !dry) misc[1 + (j & 1)] = wild;
+      }
+      if (dry) {
+        q_ready();
+        continue;
       }
       fence_async();
       mbar_arrive(bar(kOpFull + op));
@@ -882,23 +916,6 @@ __device__ __forceinline__ void extend_body(const Args& args) {
           pid1 = checked(pid2);
           sc1 = scales(pid1);
           pid2 = look_up((j >> 2) + 2);
-          // of the lane's block (8 lanes): largest so far and smallest V scale
-          v_own = scale_log2_of(sc.y);
-          float hi = v_own, lo = v_own == -INFINITY ? INFINITY : v_own;
-#pragma unroll
-          for (int o = 1; o < kBlkPages; o <<= 1) {
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-          }
-          v_blk = hi;
-#pragma unroll
-          for (int o = kBlkPages; o < 32; o <<= 1) {
-            const float before = __shfl_up_sync(0xffffffffu, hi, o);
-            if (lane >= o) hi = fmaxf(hi, before);
-          }
-          hi = fmaxf(hi, v_top);
-          v_top = __shfl_sync(0xffffffffu, hi, 31);
-          wild = lo < hi - kTame;
         }
         const bool mine = (lane >> 3) == (j & 3);  // this lane holds a page of block j
         const bool copies = mine && pid >= 0 && (!G::kWhole || ((lane >> 2) & 1) == side);
@@ -933,11 +950,30 @@ __device__ __forceinline__ void extend_body(const Args& args) {
           if (j == 0) {  // while the first codes are on their way: a sequence shorter than the prefix sees less of it
             int least = T.L;
             for (int i = T.r0 / gqa + lane; i <= (T.r0 + T.rows - 1) / gqa; i += 32)
-              least = min(least, max(__ldg(a.seq_lens + max(member_of(args.g, a.batch, T.q0 + i), 0)), 0));
+              least = min(least, max(__ldg(a.seq_lens + in_batch(__ldg(args.g.members + T.q0 + i), a.batch)), 0));
             least = __reduce_min_sync(0xffffffffu, least);
 #pragma unroll
             for (int t = 0; t < MT; ++t) p_lo[t] = least - 1;
           }
+        }
+        if ((j & 3) == 0) {
+          // of the lane's block (8 lanes): largest so far and smallest V scale
+          v_own = scale_log2_of(sc.y);
+          float hi = v_own, lo = v_own == -INFINITY ? INFINITY : v_own;
+#pragma unroll
+          for (int o = 1; o < kBlkPages; o <<= 1) {
+            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+          }
+          v_blk = hi;
+#pragma unroll
+          for (int o = kBlkPages; o < 32; o <<= 1) {
+            const float before = __shfl_up_sync(0xffffffffu, hi, o);
+            if (lane >= o) hi = fmaxf(hi, before);
+          }
+          hi = fmaxf(hi, v_top);
+          v_top = __shfl_sync(0xffffffffu, hi, 31);
+          wild = lo < hi - kTame;
         }
         if (side == (G::kWhole ? j & 1 : 0)) {  // (whole pages: the two warps take turns)
           if (j >= kInfo) ok = mbar_wait_bounded(bar(kInfoFree + info), (j / kInfo - 1) & 1);

@@ -1,76 +1,460 @@
 // Decode attention of sequences that share prefixes (oscar_kv8_decode_shared), over the 8-bit paged cache.
 //
-// Three kernels.  The first takes every group's prefix once, for all its members: their queries are the rows of tiles on tcgen05,
-// as in the extend, and the prefix is cut into splits so that the tiles of all groups fill whole waves.  The lists are on the
-// device, so the cut is made there, by every block for itself.  The second is the decode's split kernel over what each member
-// has of its own; it begins while the first ends.  The third joins a row's partials of both.
+// Three kernels, of which the first two run beside one another.  One takes every group's prefix once, for all its members: their
+// queries are the rows of tiles on tcgen05, as in the extend, and the prefix is cut into splits so that the tiles of all groups
+// fill whole waves.  The lists are on the device, so the cut is made there, by every block for itself.  The other attends what
+// each member has of its own, as the decode does.  The former is bound by products and the latter by memory, and either fills an
+// SM, so the SMs are divided among them.  The third joins a row's partials of both.
 //
 // Against reading every member's whole sequence this trades the prefix's bytes, once instead of once a member, for products
 // at the tensor cores' rate.
-#include "kv8_decode_body.cuh"
 #include "kv8_extend_body.cuh"
+#include "kv8_mma.cuh"
 
 namespace {
 
 template <int F, int D, int MT, int PARTS>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_constant__ SharedArgs args) {
   extend_body<F, D, MT, PARTS, true>(args);
+  // The kernel after the two that run beside one another waits for the second of them alone: its last block ends after the first.
+  // (The blocks of the first have all waited for what comes before both, so the second waits for nothing.)
+  if (args.last && blockIdx.x + 1 == gridDim.x && blockIdx.y + 1 == gridDim.y) grid_dep_wait();
+}
+
+// What the members have of their own, behind their groups' prefixes.  The (member, KV head) units' pages lie one after another, in
+// the order of the list, and every warp of the grid takes the same number of them, wherever units begin and end: uneven lengths
+// balance, and a block finds out once what is where.  A unit's share of a warp is a piece; piece (unit u, warp w) is stored at
+// u + w (no two are at one place, as along the pages one of the two always grows).  Lists of more than kChunk members are cut into
+// chunks with a row of blocks each.
+//
+// A page (16 tokens, K then V, D bytes each) is one tensor copy into a stage of the warp's ring, swizzled so that every
+// shared-memory read is free of bank conflicts.  Per page, with the GQA group's queries as the 8 columns:
+//   S^T = K Q^T     ldmatrix rows of 16 codes -> fp16 pairs (exact) as A: all 16 tokens in one product;
+//   P^T             weights 2^(s - m) times 2^kOwnBoost as fp16, m the running maximum less kOwnLazy at most, so that it seldom
+//                   moves: 11 bits, a step of 2^-30 of the largest; two 8 x 8 transposes make it B;
+//   O^T += f V^T P^T  f = the page's V scale, in fp32 (with a scale over 2^80, infinite V elements saturated, O counts 2^40).
+// That is half the products and half the instructions of the decode's form, whose tokens are the columns and whose weights have 22
+// bits: a page takes an SM @ clocks, where that takes 235.
+constexpr int kChunk = 384;
+constexpr int kOwnWarps = 12;  // as many as an SM holds
+constexpr int kOwnThreads = kOwnWarps * 32;
+static_assert(kChunk == kOwnThreads, "a member a thread");
+constexpr int kLeastPages = 4;  // of a warp
+constexpr float kOwnLazy = 8.f;  // log2
+constexpr int kOwnBoost = 6;     // 2^(kOwnLazy + kOwnBoost) < 65504
+constexpr float kBigScale = 0x1p80f;  // up to here 2^80 times a code (2^9) times 2^kOwnLazy times 2^27 tokens is within fp32
+constexpr int kBigUnit = 40;
+
+// Pages of a warp's ring, 16 KB.
+template <int D>
+struct Ring {
+  static constexpr int kPage = 2 * kPageSize * D;  // bytes of one page and head
+  static constexpr int kStages = 16384 / kPage;
+  static constexpr size_t kBytes = static_cast<size_t>(kStages) * kPage;
+};
+
+struct OwnArgs {
+  AttnArgs a;
+  Groups g;
+  int4* info;     // [num_members]: as the prefix kernel leaves it for members with a prefix; x < 0: not a member
+  int2* own;      // [num_members][H]: first piece of the unit, pieces
+  float* part_o;  // [chunks x warps + num_members x KV heads][GQA][D], and [4]
+  float* part_ml;
+  int max_own;    // tokens
+  bool first, last;  // of the two kernels that run beside one another
+};
+
+template <int D>
+struct OwnGeo {
+  static constexpr size_t kSmem = 1024 + kOwnWarps * (Ring<D>::kBytes + Ring<D>::kStages * 8);
+};
+
+// What a lane (g, t) = (lane / 4, lane % 4) has of a unit: queries 2t and 2t + 1 (x, y), channels D / 8 g + c.
+template <int D>
+struct Sums {
+  float2 o[D / 8];
+  float2 m, l;  // l: of the lane's tokens
+};
+
+// The page in stage `st`, its first position pos0, of a sequence of length L; scales sc (K, V), qs: what a query's logits are to be
+// multiplied with.
+template <int F, int D>
+__device__ __forceinline__ void attend_own(uint32_t st, int pos0, int L, float2 sc, float2 qs, const uint32_t (&qa)[D / 16][2],
+                                           int lane, Sums<D>& u) {
+  constexpr int kKs = D / 16, kNt = D / 8;
+  const int g = lane >> 2, t = lane & 3;
+  float acc[2][4];  // two chains of products
+#pragma unroll
+  for (int c4 = 0; c4 < kKs; c4 += 4) {
+    uint32_t w0[4], w1[4];  // tokens g and g + 8
+    ldmatrix_x4(st + chunk_at<D>(lane & 7, c4 + (lane >> 3)), w0);
+    ldmatrix_x4(st + chunk_at<D>(8 + (lane & 7), c4 + (lane >> 3)), w1);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t a0, a1, a2, a3;
+      codes_to_f16<F>(w0[c], a0, a2);
+      codes_to_f16<F>(w1[c], a1, a3);
+      if (c4 + c < 2) mma_f16_first(acc[c & 1], a0, a1, a2, a3, qa[c4 + c][0], qa[c4 + c][1]);
+      else mma_f16(acc[c & 1], a0, a1, a2, a3, qa[c4 + c][0], qa[c4 + c][1]);
+    }
+  }
+  // (the scales first: a logit may be within fp32 where its product with one of them is not; towards 0: never infinite, so that
+  // logits of 0 stay 0)
+  const float2 ks = make_float2(__fmul_rz(sc.x, qs.x), __fmul_rz(sc.x, qs.y));
+  float2 s0 = make_float2((acc[0][0] + acc[1][0]) * ks.x, (acc[0][1] + acc[1][1]) * ks.y);  // token g
+  float2 s1 = make_float2((acc[0][2] + acc[1][2]) * ks.x, (acc[0][3] + acc[1][3]) * ks.y);  // token g + 8
+  const bool tail = pos0 + kPageSize > L;
+  if (tail) {
+    if (pos0 + g >= L) s0 = make_float2(-INFINITY, -INFINITY);
+    if (pos0 + g + 8 >= L) s1 = make_float2(-INFINITY, -INFINITY);
+  }
+  float2 mx = make_float2(fmaxf(s0.x, s1.x), fmaxf(s0.y, s1.y));
+  // (-infinity + kOwnLazy is that: the first logits move it)
+  if (__any_sync(0xffffffffu, mx.x > u.m.x + kOwnLazy || mx.y > u.m.y + kOwnLazy)) {
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+      mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, x));
+      mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, x));
+    }
+    const float2 m = make_float2(fmaxf(u.m.x, mx.x), fmaxf(u.m.y, mx.y));
+    const float2 alpha = make_float2(u.m.x == -INFINITY ? 0.f : fast_exp2(u.m.x - m.x), u.m.y == -INFINITY ? 0.f : fast_exp2(u.m.y - m.y));
+    u.l = f2mul(u.l, alpha);
+#pragma unroll
+    for (int c = 0; c < kNt; ++c) u.o[c] = f2mul(u.o[c], alpha);
+    u.m = m;
+  }
+  const float2 m = make_float2(u.m.x == -INFINITY ? 0.f : u.m.x, u.m.y == -INFINITY ? 0.f : u.m.y);
+  const float2 p0 = make_float2(fast_exp2(s0.x - m.x), fast_exp2(s0.y - m.y));
+  const float2 p1 = make_float2(fast_exp2(s1.x - m.x), fast_exp2(s1.y - m.y));
+  u.l.x += p0.x + p1.x;
+  u.l.y += p0.y + p1.y;
+  const float boost = 1 << kOwnBoost;
+  const uint32_t b0 = movmatrix_trans(pack_half2(p0.x * boost, p0.y * boost));
+  const uint32_t b1 = movmatrix_trans(pack_half2(p1.x * boost, p1.y * boost));
+  // V: tokens 2t, 2t+1, 2t+8, 2t+9, channels kNt g .. kNt g + kNt - 1
+  uint32_t w[4][kNt / 4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int r = 2 * t + (c & 1) + 8 * (c >> 1);
+    if constexpr (D == 128) {
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3])
+                   : "r"(st + chunk_at<D>(kPageSize + r, g))
+                   : "memory");
+    } else {
+      asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
+                   : "=r"(w[c][0]), "=r"(w[c][1])
+                   : "r"(st + chunk_at<D>(kPageSize + r, g >> 1) + 8 * (g & 1))
+                   : "memory");
+    }
+    if (tail && pos0 + r >= L) {  // behind the last token: any bits, NaN included
+#pragma unroll
+      for (int q = 0; q < kNt / 4; ++q) w[c][q] = 0u;
+    }
+  }
+  const float f = sc.y * (1.f / (1 << kOwnBoost));
+#pragma unroll
+  for (int q = 0; q < kNt / 4; ++q) {
+    uint32_t lo[4], hi[4];  // channels 4 q + e: token pairs (2t, 2t+1) and (2t+8, 2t+9)
+    codes_to_f16<F>(__byte_perm(w[0][q], w[1][q], 0x5140), lo[0], lo[1]);
+    codes_to_f16<F>(__byte_perm(w[0][q], w[1][q], 0x7362), lo[2], lo[3]);
+    codes_to_f16<F>(__byte_perm(w[2][q], w[3][q], 0x5140), hi[0], hi[1]);
+    codes_to_f16<F>(__byte_perm(w[2][q], w[3][q], 0x7362), hi[2], hi[3]);
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {  // rows g and g + 8 of a product: channels 4 q + e and + 1
+      float d[4];
+      mma_f16_first(d, lo[e], lo[e + 1], hi[e], hi[e + 1], b0, b1);
+      u.o[4 * q + e] = f2fma(make_float2(d[0], d[1]), make_float2(f, f), u.o[4 * q + e]);
+      u.o[4 * q + e + 1] = f2fma(make_float2(d[2], d[3]), make_float2(f, f), u.o[4 * q + e + 1]);
+    }
+  }
 }
 
 template <int F, int D>
-__global__ void __launch_bounds__(kWarps * 32, 3) kv8_own_kernel(const __grid_constant__ CUtensorMap map,
+__global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_constant__ CUtensorMap map,
                                                                  const __grid_constant__ OwnArgs args) {
-  split_body<F, D, true>(map, args);
-  // Nothing here waits for the prefix kernel beside it (whose blocks have all waited for what comes before both), but the merge
-  // waits for this kernel alone: its last block ends after the prefix kernel.
-  if (args.beside_prefix && blockIdx.x + 1 == gridDim.x && blockIdx.y + 1 == gridDim.y && blockIdx.z + 1 == gridDim.z)
-    grid_dep_wait();
+  constexpr int kStages = Ring<D>::kStages, kPage = Ring<D>::kPage, kNt = D / 8;  // kNt: channels of a lane
+  extern __shared__ uint8_t raw[];
+  __shared__ long long begins[kChunk + 1];  // pages of one head before member i
+  __shared__ int from_s[kChunk], seq_s[kChunk], len_s[kChunk];
+  __shared__ long long sums[kOwnWarps];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  const AttnArgs& a = args.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int gqa = a.Hq / a.H;
+  const int m0 = blockIdx.y * kChunk, mc = min(kChunk, args.g.num_members - m0);
+  const bool tells = blockIdx.x == 0;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOwnWarps * Ring<D>::kBytes) + warp * kStages;
+  if (tid == 0) umma::prefetch_map(&map);
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(bars + i), 1);
+    mbar_init_fence();
+  }
+  if (args.first) grid_dep_wait();
+  grid_dep_launch_dependents();
+  // ---- the lists ----------------------------------------------------------------------------
+  const int b = tid < mc ? __ldg(args.g.members + m0 + tid) : -1;
+  from_s[tid] = -1;
+  __syncthreads();
+  bool bad = false;
+  for (int g0 = warp * 32; g0 < args.g.num_groups; g0 += kOwnThreads) {
+    int start = 0, n = 0, prefix = 0;
+    if (g0 + lane < args.g.num_groups && !group_of(args.g, g0 + lane, start, n, prefix)) bad = true;
+    const int lo = max(start, m0), hi = bad ? lo : min(start + n, m0 + mc);
+    for (uint32_t some = __ballot_sync(0xffffffffu, lo < hi); some != 0; some &= some - 1) {
+      const int at = __ffs(some) - 1, end = __shfl_sync(0xffffffffu, hi, at), p = __shfl_sync(0xffffffffu, prefix, at);
+      for (int i = __shfl_sync(0xffffffffu, lo, at) + lane; i < end; i += 32) from_s[i - m0] = p;
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && tells && tid == 0) record_error(OSCAR_DEVERR_POSITION);
+  const int from = from_s[tid];
+  const bool in = !bad && from >= 0, good = b >= 0 && b < a.batch;
+  int L = 0, pages = 0;
+  if (in && good) {
+    L = clamped_len(a, b);
+    if (L - from > args.max_own) {
+      record_error(OSCAR_DEVERR_SEQ_LEN);
+      L = from + args.max_own;
+    }
+    pages = max((L + kPageSize - 1) / kPageSize - from / kPageSize, 0);
+  } else if (tells && in) {
+    record_error(OSCAR_DEVERR_POSITION);
+  }
+  seq_s[tid] = b;
+  len_s[tid] = L;
+  if (tells && tid < mc && (!in || from == 0)) args.info[m0 + tid] = make_int4(in && good ? 0 : -1, 0, 0, 0);
+  if (in && good && from == 0 && L == 0 && tid % gridDim.x == blockIdx.x)  // nothing to attend
+    for (int c = 0; c < a.Hq * (D / 8); ++c)
+      reinterpret_cast<uint4*>(a.out + static_cast<size_t>(b) * a.Hq * D)[c] = make_uint4(0, 0, 0, 0);
+  long long up = pages;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up += x;
+  }
+  if (lane == 31) sums[warp] = up;
+  __syncthreads();
+  long long total = 0;
+  up -= pages;
+#pragma unroll
+  for (int w = 0; w < kOwnWarps; ++w) {
+    if (w < warp) up += sums[w];
+    total += sums[w];
+  }
+  const long long warps = static_cast<long long>(gridDim.x) * kOwnWarps, all = total * a.H;
+  const int each = static_cast<int>(max((all + warps - 1) / warps, static_cast<long long>(kLeastPages)));
+  begins[tid] = up;
+  if (tid < mc && tid % gridDim.x == blockIdx.x)
+    for (int h = 0; h < a.H; ++h) {
+      const long long at = up * a.H + static_cast<long long>(h) * pages, w0 = at / each;
+      const int unit = (m0 + tid) * a.H + h;
+      args.own[unit] = make_int2(static_cast<int>(blockIdx.y * warps + unit + w0),
+                                 pages > 0 ? static_cast<int>((at + pages - 1) / each - w0) + 1 : 0);
+    }
+  if (tid == 0) begins[kChunk] = total;
+  __syncthreads();
+  // ---- the warp's pages ----------------------------------------------------------------------
+  const long long w = static_cast<long long>(blockIdx.x) * kOwnWarps + warp;
+  const long long f0 = w * each, f1 = min(f0 + each, all);
+  const uint32_t ring = smem_u32(smem) + warp * kStages * kPage;
+  const bool issuer = umma::elect_one();
+  uint32_t qa[D / 16][2];
+  Sums<D> sums_u;
+  float2 qs = make_float2(0.f, 0.f);
+  int unit = -1, len = 0, exponent = 0;  // the unit at hand, its sequence's length; what its O counts
+  bool aborted = false;
+  // the piece of `unit`, to the output if it is all of it
+  auto flush = [&]() {
+    const int i = unit / a.H, h = unit - i * a.H;
+    const int n = static_cast<int>(begins[i + 1] - begins[i]);
+    const long long at = begins[i] * a.H + static_cast<long long>(h) * n;
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+      sums_u.l.x += __shfl_xor_sync(0xffffffffu, sums_u.l.x, x);
+      sums_u.l.y += __shfl_xor_sync(0xffffffffu, sums_u.l.y, x);
+    }
+    const bool whole = from_s[i] == 0 && at >= f0 && at + n <= f1;
+    const size_t piece = blockIdx.y * warps + static_cast<long long>(m0) * a.H + unit + w;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int q = 2 * t + e;
+      const float m = e ? sums_u.m.y : sums_u.m.x, l = e ? sums_u.l.y : sums_u.l.x;
+      if (q >= gqa) continue;
+      __nv_bfloat16* out = a.out + (static_cast<size_t>(seq_s[i]) * a.Hq + h * gqa + q) * D + kNt * g;
+      float* part = args.part_o + (piece * gqa + q) * D + kNt * g;
+#pragma unroll
+      for (int j = 0; j < kNt; j += 4) {
+        float4 x;
+        x.x = e ? sums_u.o[j].y : sums_u.o[j].x;
+        x.y = e ? sums_u.o[j + 1].y : sums_u.o[j + 1].x;
+        x.z = e ? sums_u.o[j + 2].y : sums_u.o[j + 2].x;
+        x.w = e ? sums_u.o[j + 3].y : sums_u.o[j + 3].x;
+        if (whole) store_out4(out + j, x, l, exponent);
+        else *reinterpret_cast<float4*>(part + j) = x;
+      }
+      if (!whole && g == 0)
+        *reinterpret_cast<float4*>(args.part_ml + (piece * gqa + q) * 4) =
+            make_float4(m, l, m == -INFINITY ? m : static_cast<float>(exponent), 0.f);
+    }
+  };
+  int done = 0;  // pages of this warp before the batch at hand
+  for (long long f = f0; f < f1; f += 32) {
+    // 32 pages, a lane each: unit, position, page, scales
+    const int n = static_cast<int>(min(f1 - f, 32LL));
+    int key = -1, pos0 = 0, row = -1;
+    float2 sc = make_float2(0.f, 0.f);
+    if (lane < n) {
+      const long long q = (f + lane) / a.H;
+      int lo = 0, hi = mc;  // the last member that begins at q or before
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (begins[mid] <= q) lo = mid;
+        else hi = mid;
+      }
+      const int np = static_cast<int>(begins[lo + 1] - begins[lo]);
+      const long long rem = f + lane - begins[lo] * a.H;
+      const int h = static_cast<int>(rem / np), page = from_s[lo] / kPageSize + static_cast<int>(rem - static_cast<long long>(h) * np);
+      key = lo * a.H + h;
+      pos0 = page * kPageSize;
+      const int id = __ldg(a.page_table + static_cast<size_t>(seq_s[lo]) * a.max_pages + page);
+      if (id < 0 || id >= a.num_pages) {
+        record_error(OSCAR_DEVERR_PAGE_ID);
+      } else {
+        row = id * a.H + h;
+        sc = __ldg(reinterpret_cast<const float2*>(a.scales) + row);
+      }
+    }
+    auto issue = [&](int k) {
+      const int r = __shfl_sync(0xffffffffu, row, k);
+      if (issuer) {
+        const int c = done + k;
+        const uint32_t bar = smem_u32(bars + c % kStages);
+        if (r < 0) {
+          mbar_arrive(bar);
+        } else {
+          mbar_arrive_expect_tx(bar, kPage);
+          umma::tma_load_3d(ring + (c % kStages) * kPage, &map, 0, 0, r, bar);
+        }
+      }
+      __syncwarp();
+    };
+    if (!aborted)
+      for (int k = 0; k < min(n, kStages); ++k) issue(k);
+    for (int k = 0; k < n; ++k) {
+      const int u = __shfl_sync(0xffffffffu, key, k);
+      if (u != unit) {
+        if (unit >= 0) flush();
+        unit = u;
+        const int i = u / a.H, h = u - i * a.H;
+        len = len_s[i];
+        const float x =
+            load_q<D>(a.q + (static_cast<size_t>(seq_s[i]) * a.Hq + h * gqa + min(g, gqa - 1)) * D, g < gqa, t, a.scale_log2, qa);
+        qs = make_float2(__shfl_sync(0xffffffffu, x, 8 * t), __shfl_sync(0xffffffffu, x, 8 * t + 4));  // queries 2t, 2t + 1
+        sums_u.m = make_float2(-INFINITY, -INFINITY);
+        sums_u.l = make_float2(0.f, 0.f);
+        exponent = 0;
+#pragma unroll
+        for (int j = 0; j < kNt; ++j) sums_u.o[j] = make_float2(0.f, 0.f);
+      }
+      if (aborted) continue;
+      const int c = done + k;
+      const bool ok = mbar_wait_bounded(smem_u32(bars + c % kStages), (c / kStages) & 1);
+      if (__any_sync(0xffffffffu, !ok)) {
+        // a copy did not land: the rest of this warp's pages are dropped, once the copies in flight are over
+        aborted = true;
+        if (lane == 0) record_error(OSCAR_DEVERR_TIMEOUT);
+        for (int x = k; x < min(n, k + kStages); ++x)
+          mbar_wait_bounded(smem_u32(bars + (done + x) % kStages), ((done + x) / kStages) & 1);
+        continue;
+      }
+      const int r = __shfl_sync(0xffffffffu, row, k), p = __shfl_sync(0xffffffffu, pos0, k);
+      float2 s = make_float2(__shfl_sync(0xffffffffu, sc.x, k), __shfl_sync(0xffffffffu, sc.y, k));
+      if (r >= 0) {
+        if (exponent == 0 && s.y > kBigScale) {  // rare
+          exponent = kBigUnit;
+#pragma unroll
+          for (int j = 0; j < kNt; ++j) sums_u.o[j] = f2mul(sums_u.o[j], make_float2(pow2i(-kBigUnit), pow2i(-kBigUnit)));
+        }
+        if (exponent != 0) s.y *= pow2i(-kBigUnit);
+        attend_own<F, D>(ring + (c % kStages) * kPage, p, len, s, qs, qa, lane, sums_u);
+      }
+      __syncwarp();
+      if (k + kStages < n) issue(k + kStages);
+    }
+    done += n;
+  }
+  if (unit >= 0) flush();
+  // The kernel after the two waits for the second of them alone: its last block ends after the first.
+  if (args.last && blockIdx.x + 1 == gridDim.x && blockIdx.y + 1 == gridDim.y) grid_dep_wait();
 }
 
 struct MergeArgs {
   AttnArgs a;
   const int32_t* members;
   const int4* info;
-  const int* own;
-  const float* own_o;  // [num_members][Hq][ns][D], and [4]
+  const int2* own;
+  const float* own_o;  // as OwnArgs
   const float* own_ml;
   const float* pre_o;  // [items][H][tm][D], and [4]
   const float* pre_ml;
-  int num_members, ns, tm;
+  int num_members, tm;
 };
 
-// One warp per (member, query head).
-constexpr int kMergeRows = 4;
-template <int D>
-__global__ void __launch_bounds__(kMergeRows * 32) kv8_shared_merge_kernel(MergeArgs m) {
+// WARPS warps per (member, query head), of four in a block.
+constexpr int kMergeWarps = 4;
+template <int D, int WARPS>
+__global__ void __launch_bounds__(kMergeWarps * 32) kv8_shared_merge_kernel(MergeArgs m) {
+  __shared__ float4 part[kMergeWarps][D / 4];
+  __shared__ float sums[kMergeWarps];
   const AttnArgs& a = m.a;
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * kMergeRows + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c4 = lane % (D / 4);
+  const long long row = static_cast<long long>(blockIdx.x) * (kMergeWarps / WARPS) + warp / WARPS;
   grid_dep_wait();
   if (row >= static_cast<long long>(m.num_members) * a.Hq) return;
-  const int i = static_cast<int>(row / a.Hq), hq = static_cast<int>(row % a.Hq);
+  const int i = static_cast<int>(row / a.Hq), hq = static_cast<int>(row - static_cast<long long>(i) * a.Hq);
   const int4 info = m.info[i];
-  if (info.x < 0) return;  // not a member
   const int b = __ldg(m.members + i);
-  if (b < 0 || b >= a.batch) return;
-  const int n_own = m.own[i], n = n_own + info.z;
+  const int gqa = a.Hq / a.H, h = hq / gqa, hd = hq - h * gqa, x = info.w * gqa + hd;
+  const int2 own = m.own[static_cast<size_t>(i) * a.H + h];
+  if (info.x < 0 || b < 0 || b >= a.batch) return;  // not a member
+  const int n_own = own.y, n = n_own + info.z;
   if (info.z == 0 && n_own <= 1) return;  // written by the kernel before
-  const int gqa = a.Hq / a.H, h = hq / gqa, x = info.w * gqa + hq % gqa;
-  const float* own_o = m.own_o + row * m.ns * D;
-  const float* own_ml = m.own_ml + row * m.ns * 4;
-  const size_t at = (static_cast<size_t>(info.x + x / m.tm) * a.H + h) * m.tm + x % m.tm;
+  const size_t piece = own.x;
+  const float* own_o = m.own_o + (piece * gqa + hd) * D + 4 * c4;
+  const float* own_ml = m.own_ml + (piece * gqa + hd) * 4;
+  const size_t pre = (static_cast<size_t>(info.x + x / m.tm) * a.H + h) * m.tm + x % m.tm;
   const size_t step = static_cast<size_t>(info.y) * a.H * m.tm;  // from one split to the next
+  const float* pre_o = m.pre_o + pre * D + 4 * (c4 ^ (x % m.tm & 7));
   float l, e;
   float4 r;
-  merge_parts<D>([&](int k) { return k < n_own ? own_o + static_cast<size_t>(k) * D : m.pre_o + (at + (k - n_own) * step) * D; },
-                 [&](int k) { return k < n_own ? own_ml + 4 * k : m.pre_ml + (at + (k - n_own) * step) * 4; }, n, 0, 1, lane,
-                 l, r, e);
-  if (lane < D / 4) store_out4(a.out + (static_cast<size_t>(b) * a.Hq + hq) * D + 4 * lane, r, l, e);
+  merge_parts<D>([&](int k) { return k < n_own ? own_o + static_cast<size_t>(k) * gqa * D : pre_o + (k - n_own) * step * D; },
+                 [&](int k) {
+                   return k < n_own ? own_ml + static_cast<size_t>(k) * gqa * 4 : m.pre_ml + (pre + (k - n_own) * step) * 4;
+                 },
+                 n, warp % WARPS, WARPS, lane, l, r, e);
+  __nv_bfloat16* out = a.out + (static_cast<size_t>(b) * a.Hq + hq) * D + 4 * c4;
+  if (WARPS == 1) {
+    if (lane < D / 4) store_out4(out, r, l, e);
+    return;
+  }
+  if (lane < D / 4) part[warp][lane] = r;
+  if (lane == 0) sums[warp] = l;
+  __syncthreads();
+  if (threadIdx.x < D / 4) {
+    for (int w = 1; w < WARPS; ++w) {
+      const float4 y = part[w][lane];
+      l += sums[w];
+      r.x += y.x; r.y += y.y; r.z += y.z; r.w += y.w;
+    }
+    store_out4(out, r, l, e);
+  }
 }
 
 struct Plan {
   int mt, parts, tm, items;  // of the prefix kernel; items 0: no prefix
-  int ns, pps;               // of what is the members' own
+  bool prefix_first;         // of the two kernels
+  int chunks, blocks;        // of what is the members' own: rows of blocks, blocks of a row
   size_t off_ml, off_pre_o, off_pre_ml, off_info, off_own, total;
 };
 
@@ -82,46 +466,64 @@ bool make_plan(const oscar_dims_t* d, int batch, int max_seq_len, int max_prefix
   if (d->num_kv_heads > 65535) return false;
   const int H = d->num_kv_heads, gqa = d->num_q_heads / H;
   // the prefixes: tiles of 256 rows, smaller ones where a group has fewer rows
-  const long long rows = static_cast<long long>(members) * gqa, each = groups > 0 ? (rows + groups - 1) / groups : 0;
+  // (of several groups one holds, as a rule, the sequences by themselves)
+  const long long rows = static_cast<long long>(members) * gqa, likely = groups > 1 ? groups - 1 : 1;
+  const long long each = (rows + likely - 1) / likely;
   p->mt = each > 128 ? 2 : 1;
   p->parts = each > 64 ? 1 : 2;
   p->tm = p->mt * 128 / p->parts;
   const long long most_tiles = rows / p->tm + groups;  // of one KV head: ragged ones, one a group, beyond the even ones
   const long long blocks = (max_prefix / kPageSize + kBlkPages - 1) / kBlkPages;
+  // SMs for what is the members' own (k) beside waves of prefix blocks on the others, or one after the other (k = 0), whichever
+  // should take least by these times (us): of a prefix block (128 tokens), of a CTA's start and end, of the bytes of the members'
+  // own tokens, of which half the bound is taken as likely.
+  const int sms = num_sms();
+  const double block_us = p->mt == 2 ? 1.7 : p->parts == 1 ? 1.15 : 0.95, start_us = p->mt == 2 ? 13 : 10, own_start_us = 6;
+  const double own_bytes = static_cast<double>(members) * H * max_own * d->head_dim;
+  auto own_us = [&](int n) { return own_start_us + own_bytes / fmin(n * 40e3, 5.7e6); };  // 40 KB a us and SM, 5.7 TB/s in all
+  const long long chunk = members < kChunk ? members : kChunk, pages = (static_cast<long long>(max_own) + kPageSize - 1) / kPageSize;
+  p->chunks = (members + kChunk - 1) / kChunk;
   p->items = 0;
+  p->prefix_first = false;
+  int own_sms = sms;
   if (blocks > 0 && rows > 0 && groups > 0) {
-    // Blocks of the grid, for each KV head: those of the waves that take least for as many tiles as are likely (the kernel
-    // looks again, with the tiles that there are), and at least one for each tile.
-    const long long tiles = rows / p->tm > groups ? rows / p->tm : groups;
-    long long best = 0, items = 0;
-    for (long long w = 1; w <= 4; ++w) {
-      const long long n = w * num_sms() / H;
-      if (n < tiles) continue;
-      const long long splits = n / tiles, cost = w * ((blocks + splits - 1) / splits + 5);
-      if (best == 0 || cost < best) {
-        best = cost;
-        items = n;
+    const long long tiles = rows / p->tm > likely ? rows / p->tm : likely;
+    double best = 0;
+    long long items = 0;
+    for (int k = 0; k < sms; k += 4) {
+      for (int w = 1; w <= 4; ++w) {
+        const long long n = static_cast<long long>(w) * (sms - k) / H;
+        if (n < tiles) continue;
+        const double prefix = w * (static_cast<double>((blocks + n / tiles - 1) / (n / tiles)) * block_us + start_us);
+        const double us = k == 0 ? prefix + own_us(sms) : fmax(prefix, own_us(k));
+        if (items == 0 || us < best) {
+          best = us;
+          items = n;
+          own_sms = k == 0 ? sms : k;
+        }
       }
     }
     if (items < most_tiles) items = most_tiles;
     if (items > 0x7fffffffLL) return false;
     p->items = static_cast<int>(items);
+    // what takes longer goes first, if it leaves room for the other
+    p->prefix_first = items * H <= sms - own_sms;
   }
-  // the rest, as in the decode
-  const long long pages = (static_cast<long long>(max_own) + kPageSize - 1) / kPageSize;
-  p->pps = split_pages(pages, (members > 0 ? members : 1LL) * H);
-  if (p->pps > kMaxPps) p->pps = kMaxPps;
-  const long long ns = pages > 0 ? (pages + p->pps - 1) / p->pps : 1;
-  if (ns > 65535) return false;
-  p->ns = static_cast<int>(ns);
-  const size_t own = ns > 1 || p->items > 0 ? static_cast<size_t>(members) * d->num_q_heads * ns : 0;
+  // blocks of a chunk, fewer where their warps would have nothing
+  const long long use = (chunk * H * pages + kOwnWarps * kLeastPages - 1) / (kOwnWarps * kLeastPages);
+  long long most = p->chunks > 0 ? own_sms / p->chunks : 1;
+  if (most > use) most = use;
+  p->blocks = static_cast<int>(most < 1 ? 1 : most);
+  const long long pieces = static_cast<long long>(p->chunks) * p->blocks * kOwnWarps + static_cast<long long>(members) * H;
+  if (pieces > 0x7fffffffLL) return false;
+  const size_t own = static_cast<size_t>(pieces) * gqa;
   const size_t pre = static_cast<size_t>(p->items) * H * p->tm;
   p->off_ml = align_up(own * d->head_dim * sizeof(float), 256);
   p->off_pre_o = p->off_ml + align_up(own * 4 * sizeof(float), 256);
   p->off_pre_ml = p->off_pre_o + align_up(pre * d->head_dim * sizeof(float), 256);
   p->off_info = p->off_pre_ml + align_up(pre * 4 * sizeof(float), 256);
   p->off_own = p->off_info + align_up(static_cast<size_t>(members) * sizeof(int4), 256);
-  p->total = p->off_own + align_up(static_cast<size_t>(members) * sizeof(int), 256) + 256;
+  p->total = p->off_own + align_up(static_cast<size_t>(members) * sizeof(int2) * H, 256) + 256;
   return true;
 }
 
@@ -138,20 +540,24 @@ cudaError_t launch_prefix(const Plan& p, const SharedArgs& sh, cudaStream_t stre
 template <int F, int D>
 cudaError_t launch(const Plan& p, const SharedArgs& sh, const OwnArgs& ow, const MergeArgs& me, const CUtensorMap& map,
                    cudaStream_t stream) {
-  cudaError_t e = cudaSuccess;
-  if (p.items > 0)
-    e = p.mt == 2      ? launch_prefix<F, D, 2, 1>(p, sh, stream)
-        : p.parts == 2 ? launch_prefix<F, D, 1, 2>(p, sh, stream)
-                       : launch_prefix<F, D, 1, 1>(p, sh, stream);
-  if (e != cudaSuccess) return e;
   auto k = kv8_own_kernel<F, D>;
-  e = set_smem_limit_once(reinterpret_cast<const void*>(k), DecodeGeo<D>::kSmem);
+  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(k), OwnGeo<D>::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k, dim3(p.ns, ow.s.a.H, me.num_members), dim3(kWarps * 32), DecodeGeo<D>::kSmem, stream, map, ow);
-  if (e != cudaSuccess || (p.items == 0 && p.ns == 1)) return e;
+  for (const bool prefix : {p.prefix_first, !p.prefix_first}) {
+    if (!prefix) e = launch_pdl(k, dim3(p.blocks, p.chunks), dim3(kOwnThreads), OwnGeo<D>::kSmem, stream, map, ow);
+    else if (p.items > 0)
+      e = p.mt == 2      ? launch_prefix<F, D, 2, 1>(p, sh, stream)
+          : p.parts == 2 ? launch_prefix<F, D, 1, 2>(p, sh, stream)
+                         : launch_prefix<F, D, 1, 1>(p, sh, stream);
+    if (e != cudaSuccess) return e;
+  }
   const long long rows = static_cast<long long>(me.num_members) * me.a.Hq;
-  return launch_pdl(kv8_shared_merge_kernel<D>, dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows)),
-                    dim3(kMergeRows * 32), 0, stream, me);
+  // Few rows have many partials each: a row a block, its partials all in flight at once.
+  if (rows <= 2LL * num_sms())
+    return launch_pdl(kv8_shared_merge_kernel<D, kMergeWarps>, dim3(static_cast<unsigned>(rows)), dim3(kMergeWarps * 32), 0, stream,
+                      me);
+  return launch_pdl(kv8_shared_merge_kernel<D, 1>, dim3(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps)),
+                    dim3(kMergeWarps * 32), 0, stream, me);
 }
 
 }  // namespace
@@ -191,11 +597,11 @@ extern "C" oscar_status_t oscar_kv8_decode_shared(const oscar_dims_t* dims, int3
   auto floats = [&](size_t off) { return reinterpret_cast<float*>(w + off); };
   const Groups g{members, group_start, prefix_lens, num_members, num_groups, max_prefix_len};
   int4* info = reinterpret_cast<int4*>(w + plan.off_info);
-  int* own = reinterpret_cast<int*>(w + plan.off_own);
-  const SharedArgs sh{{a, floats(plan.off_pre_o), floats(plan.off_pre_ml), 0, 0, 0}, g, info, num_sms()};
-  const OwnArgs ow{{a, floats(0), floats(plan.off_ml), plan.ns, plan.pps}, g, info, own, max_own_len, plan.items > 0};
+  int2* own = reinterpret_cast<int2*>(w + plan.off_own);
+  const SharedArgs sh{{a, floats(plan.off_pre_o), floats(plan.off_pre_ml), 0, 0, 0}, g, info, plan.prefix_first, !plan.prefix_first};
+  const OwnArgs ow{a, g, info, own, floats(0), floats(plan.off_ml), max_own_len, !plan.prefix_first, plan.prefix_first && plan.items > 0};
   const MergeArgs me{a, members, info, own, floats(0), floats(plan.off_ml), floats(plan.off_pre_o), floats(plan.off_pre_ml),
-                     num_members, plan.ns, plan.tm};
+                     num_members, plan.tm};
   cudaStream_t s = as_stream(stream);
   const bool d128 = dims->head_dim == 128;
   const cudaError_t e = kv_format == OSCAR_KV8_E4M3
