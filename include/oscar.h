@@ -653,8 +653,9 @@ oscar_status_t oscar_kv8_extend_varlen(const oscar_dims_t* dims, int32_t kv_form
 /*
  * oscar_kv8_decode_shared -- oscar_kv8_decode (without a window) of sequences whose first pages are the same, as
  * oscar_pages_fork leaves them: each group's prefix is attended once for all its members, on tensor cores, what a member has
- * behind it by itself, and the two are joined by log-sum-exp.  The result is that of oscar_kv8_decode, but that weights over
- * the prefix are held in 11 bits (oscar_kv8_extend_varlen); the output has 8.
+ * behind it by itself, and the two are joined by log-sum-exp.  The result is that of oscar_kv8_decode, but that weights are
+ * held in 11 bits (as oscar_kv8_extend_varlen's over the prefixes, and with a step of 2^-30 of the row's largest elsewhere); the
+ * output has 8.
  * Arguments beyond oscar_kv8_decode's
  *   num_members   entries of `members` at most; num_groups: of prefix_lens
  *   members       device int32 [num_members]: the sequences to decode, group after group
@@ -680,6 +681,18 @@ oscar_status_t oscar_kv8_decode_shared(const oscar_dims_t* dims, int32_t kv_form
                                        const int32_t* page_table, const int32_t* seq_lens, const int32_t* members,
                                        const int32_t* group_start, const int32_t* prefix_lens, float sm_scale, void* out,
                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * oscar_kv8_decode_shared_plan -- how oscar_kv8_decode_shared runs a decode of these bounds (the arguments of its workspace call);
+ * it reports the library's own schedule:
+ *   *tile_rows      query rows of a prefix tile (64, 128 or 256); 0: members attend their prefixes by themselves, which is quicker
+ *                   where calls are small
+ *   *prefix_blocks  blocks of the kernel over the prefixes; *own_blocks: of that over what members have of their own, beside it
+ * Any output pointer may be NULL.  Invalid sizes return OSCAR_ERR_INVALID_ARG.
+ */
+oscar_status_t oscar_kv8_decode_shared_plan(const oscar_dims_t* dims, int32_t batch, int32_t max_seq_len, int32_t max_prefix_len,
+                                            int32_t max_own_len, int32_t num_members, int32_t num_groups, int32_t* tile_rows,
+                                            int32_t* prefix_blocks, int32_t* own_blocks);
 
 /*
  * ---- Pages ----------------------------------------------------------------------

@@ -119,6 +119,8 @@ def _load():
         "oscar_kv8_extend_varlen_workspace_bytes": (SZ, [D, I32, I32, I32, I32, I32, I32, I32]),
         "oscar_kv8_extend_varlen": (I32, [D, I32, I32, I32, I32, I32, I32, P, P, P, P, P, P, I32, I32, F32, P, P, SZ, P]),
         "oscar_kv8_decode_shared_workspace_bytes": (SZ, [D, I32, I32, I32, I32, I32, I32]),
+        "oscar_kv8_decode_shared_plan": (I32, [D, I32, I32, I32, I32, I32, I32, ctypes.POINTER(I32), ctypes.POINTER(I32),
+                                               ctypes.POINTER(I32)]),
         "oscar_kv8_decode_shared": (I32, [D, I32, I32, I32, I32, I32, I32, I32, P, P, P, P, P, P, P, P, F32, P, P, SZ, P]),
         "oscar_pages_groups_workspace_bytes": (SZ, [D, I32]),
         "oscar_pages_groups": (I32, [D, I32, I32, I32, P, P, P, P, P, P, SZ, P]),
@@ -547,6 +549,16 @@ def oscar_kv8_decode_shared_workspace_bytes(dims, batch, max_seq_len, max_prefix
     return int(lib.oscar_kv8_decode_shared_workspace_bytes(ctypes.byref(_dims(dims)), int(batch), int(max_seq_len),
                                                            int(max_prefix_len), int(max_own_len), int(num_members),
                                                            int(num_groups)))
+
+
+def oscar_kv8_decode_shared_plan(dims, batch, max_seq_len, max_prefix_len, max_own_len, num_members, num_groups) -> dict:
+    """The schedule for these bounds: {"tile_rows": query rows of a prefix tile (0: members attend their prefixes by
+    themselves), "prefix_blocks", "own_blocks": blocks of the two kernels}."""
+    t, p, o = ctypes.c_int32(0), ctypes.c_int32(0), ctypes.c_int32(0)
+    _check(lib.oscar_kv8_decode_shared_plan(_dims(dims), int(batch), int(max_seq_len), int(max_prefix_len), int(max_own_len),
+                                            int(num_members), int(num_groups), ctypes.byref(t), ctypes.byref(p), ctypes.byref(o)),
+           "oscar_kv8_decode_shared_plan")
+    return {"tile_rows": t.value, "prefix_blocks": p.value, "own_blocks": o.value}
 
 
 def oscar_kv8_decode_shared(dims, kv_format, batch, max_seq_len, max_prefix_len, max_own_len, q, kv8_pages, kv8_scales,

@@ -90,14 +90,14 @@ __device__ __forceinline__ void store_out4(__nv_bfloat16* out, float4 o, float l
       make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
-// One warp: partials first, first + step, ... of n (o_at(i): the four channels of c4 = lane % (D / 4), unnormalised; ml_at(i) =
-// m, l, r, -; -infinity for the units of a partial of nothing): l and four channels r, in units of the largest m and m + r of all n, the
+// One warp: partials first, first + step, ... of n (o [n][D] unnormalised, ml [n][4] = m, l, r, -; -infinity for the units of a
+// partial of nothing): l and four channels r of lane's c4 = lane % (D / 4), in units of the largest m and m + r of all n, the
 // latter e above the former.  Eight partials are in flight at once, the first of them while the maxima are found.
-template <int D, typename OAt, typename MlAt>
-__device__ __forceinline__ void merge_parts(OAt o_at, MlAt ml_at, int n, int first, int step, int lane, float& l, float4& r,
-                                            float& e) {
+template <int D>
+__device__ __forceinline__ void merge_part(const float* o, const float* ml, int n, int first, int step, int lane,
+                                           float& l, float4& r, float& e) {
   constexpr int kSub = 128 / D, kFly = 8;  // D = 64: two half warps take every second partial
-  const int sub = lane / (D / 4);
+  const int sub = lane / (D / 4), c4 = lane % (D / 4);
   l = 0.f;
   r = make_float4(0.f, 0.f, 0.f, 0.f);
   float4 x[kFly], p[kFly];
@@ -108,8 +108,8 @@ __device__ __forceinline__ void merge_parts(OAt o_at, MlAt ml_at, int n, int fir
       p[k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
       x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < n) {
-        p[k] = *reinterpret_cast<const float4*>(ml_at(i));
-        x[k] = *reinterpret_cast<const float4*>(o_at(i));
+        p[k] = *reinterpret_cast<const float4*>(ml + 4 * i);
+        x[k] = *reinterpret_cast<const float4*>(o + static_cast<size_t>(i) * D + 4 * c4);
       }
     }
   };
@@ -117,7 +117,7 @@ __device__ __forceinline__ void merge_parts(OAt o_at, MlAt ml_at, int n, int fir
   load(i0);
   float M = -INFINITY, R = -INFINITY;  // a lane's own, then all lanes'
   for (int i = lane; i < n; i += 32) {
-    const float4 v = *reinterpret_cast<const float4*>(ml_at(i));
+    const float4 v = *reinterpret_cast<const float4*>(ml + 4 * i);
     if (v.x > -INFINITY) {
       const float m = fmaxf(M, v.x);
       R = fmaxf(R + (M - m), v.z + (v.x - m));
@@ -154,15 +154,6 @@ __device__ __forceinline__ void merge_parts(OAt o_at, MlAt ml_at, int n, int fir
     r.z += __shfl_xor_sync(0xffffffffu, r.z, 16);
     r.w += __shfl_xor_sync(0xffffffffu, r.w, 16);
   }
-}
-
-// The same of partials one after another (o [n][D], ml [n][4]).
-template <int D>
-__device__ __forceinline__ void merge_part(const float* o, const float* ml, int n, int first, int step, int lane,
-                                           float& l, float4& r, float& e) {
-  const int c4 = lane % (D / 4);
-  merge_parts<D>([&](int i) { return o + static_cast<size_t>(i) * D + 4 * c4; }, [&](int i) { return ml + 4 * i; }, n, first, step, lane,
-                 l, r, e);
 }
 
 // One warp: the merge of n partials into a row of the output.

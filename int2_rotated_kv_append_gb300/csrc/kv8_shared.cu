@@ -22,8 +22,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
 }
 
 // What the members have of their own, behind their groups' prefixes.  The (member, KV head) units' pages lie one after another, in
-// the order of the list, and every warp of the grid takes the same number of them, wherever units begin and end: uneven lengths
-// balance, and a block finds out once what is where.  A unit's share of a warp is a piece; piece (unit u, warp w) is stored at
+// the order of the list and kUnitCost empty places behind each unit's, and every warp of the grid takes the same number of places,
+// wherever units begin and end: uneven lengths balance, and a block finds out once what is where.  A unit's share of a warp is a piece; piece (unit u, warp w) is stored at
 // u + w (no two are at one place, as along the pages one of the two always grows).  Lists of more than kChunk members are cut into
 // chunks with a row of blocks each.
 //
@@ -40,6 +40,7 @@ constexpr int kOwnWarps = 12;  // as many as an SM holds
 constexpr int kOwnThreads = kOwnWarps * 32;
 static_assert(kChunk == kOwnThreads, "a member a thread");
 constexpr int kLeastPages = 4;  // of a warp
+constexpr int kUnitCost = 2;    // pages in whose time a warp goes from one unit to the next: as many places without a page
 constexpr float kOwnLazy = 8.f;  // log2
 constexpr int kOwnBoost = 6;     // 2^(kOwnLazy + kOwnBoost) < 65504
 constexpr float kBigScale = 0x1p80f;  // up to here 2^80 times a code (2^9) times 2^kOwnLazy times 2^27 tokens is within fp32
@@ -62,6 +63,7 @@ struct OwnArgs {
   float* part_ml;
   int max_own;    // tokens
   bool first, last;  // of the two kernels that run beside one another
+  bool all;          // every member attends its prefix by itself too (there is no prefix kernel)
 };
 
 template <int D>
@@ -175,8 +177,9 @@ __global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_co
                                                                  const __grid_constant__ OwnArgs args) {
   constexpr int kStages = Ring<D>::kStages, kPage = Ring<D>::kPage, kNt = D / 8;  // kNt: channels of a lane
   extern __shared__ uint8_t raw[];
-  __shared__ long long begins[kChunk + 1];  // pages of one head before member i
-  __shared__ int from_s[kChunk], seq_s[kChunk], len_s[kChunk];
+  __shared__ long long begins[kChunk + 1];  // places of one head before member i
+  __shared__ int from_s[kChunk], seq_s[kChunk], len_s[kChunk];  // member i: its group's prefix, sequence, length
+  __shared__ int lead_s[kChunk];                                // its group's first member, whose pages the prefix is read from
   __shared__ long long sums[kOwnWarps];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const AttnArgs& a = args.a;
@@ -203,7 +206,11 @@ __global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_co
     const int lo = max(start, m0), hi = bad ? lo : min(start + n, m0 + mc);
     for (uint32_t some = __ballot_sync(0xffffffffu, lo < hi); some != 0; some &= some - 1) {
       const int at = __ffs(some) - 1, end = __shfl_sync(0xffffffffu, hi, at), p = __shfl_sync(0xffffffffu, prefix, at);
-      for (int i = __shfl_sync(0xffffffffu, lo, at) + lane; i < end; i += 32) from_s[i - m0] = p;
+      const int lead = __shfl_sync(0xffffffffu, start, at);
+      for (int i = __shfl_sync(0xffffffffu, lo, at) + lane; i < end; i += 32) {
+        from_s[i - m0] = p;
+        lead_s[i - m0] = lead;
+      }
     }
   }
   bad = __syncthreads_or(bad);
@@ -217,17 +224,20 @@ __global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_co
       record_error(OSCAR_DEVERR_SEQ_LEN);
       L = from + args.max_own;
     }
-    pages = max((L + kPageSize - 1) / kPageSize - from / kPageSize, 0);
+    pages = max((L + kPageSize - 1) / kPageSize - (args.all ? 0 : from / kPageSize), 0);
+    if (args.all && from > 0) lead_s[tid] = in_batch(__ldg(args.g.members + lead_s[tid]), a.batch);
   } else if (tells && in) {
     record_error(OSCAR_DEVERR_POSITION);
   }
   seq_s[tid] = b;
   len_s[tid] = L;
-  if (tells && tid < mc && (!in || from == 0)) args.info[m0 + tid] = make_int4(in && good ? 0 : -1, 0, 0, 0);
-  if (in && good && from == 0 && L == 0 && tid % gridDim.x == blockIdx.x)  // nothing to attend
+  const bool alone = from == 0 || args.all;  // no part of the member is the prefix kernel's
+  if (tells && tid < mc && (!in || alone)) args.info[m0 + tid] = make_int4(in && good ? 0 : -1, 0, 0, 0);
+  if (in && good && alone && L == 0 && tid % gridDim.x == blockIdx.x)  // nothing to attend
     for (int c = 0; c < a.Hq * (D / 8); ++c)
       reinterpret_cast<uint4*>(a.out + static_cast<size_t>(b) * a.Hq * D)[c] = make_uint4(0, 0, 0, 0);
-  long long up = pages;
+  const int places = pages > 0 ? pages + kUnitCost : 0;
+  long long up = places;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long x = __shfl_up_sync(0xffffffffu, up, o);
@@ -236,7 +246,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_co
   if (lane == 31) sums[warp] = up;
   __syncthreads();
   long long total = 0;
-  up -= pages;
+  up -= places;
 #pragma unroll
   for (int w = 0; w < kOwnWarps; ++w) {
     if (w < warp) up += sums[w];
@@ -247,7 +257,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_co
   begins[tid] = up;
   if (tid < mc && tid % gridDim.x == blockIdx.x)
     for (int h = 0; h < a.H; ++h) {
-      const long long at = up * a.H + static_cast<long long>(h) * pages, w0 = at / each;
+      const long long at = up * a.H + static_cast<long long>(h) * places, w0 = at / each;
       const int unit = (m0 + tid) * a.H + h;
       args.own[unit] = make_int2(static_cast<int>(blockIdx.y * warps + unit + w0),
                                  pages > 0 ? static_cast<int>((at + pages - 1) / each - w0) + 1 : 0);
@@ -267,14 +277,14 @@ __global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_co
   // the piece of `unit`, to the output if it is all of it
   auto flush = [&]() {
     const int i = unit / a.H, h = unit - i * a.H;
-    const int n = static_cast<int>(begins[i + 1] - begins[i]);
-    const long long at = begins[i] * a.H + static_cast<long long>(h) * n;
+    const int places = static_cast<int>(begins[i + 1] - begins[i]);
+    const long long at = begins[i] * a.H + static_cast<long long>(h) * places;
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1) {
       sums_u.l.x += __shfl_xor_sync(0xffffffffu, sums_u.l.x, x);
       sums_u.l.y += __shfl_xor_sync(0xffffffffu, sums_u.l.y, x);
     }
-    const bool whole = from_s[i] == 0 && at >= f0 && at + n <= f1;
+    const bool whole = (from_s[i] == 0 || args.all) && at >= f0 && at + places - kUnitCost <= f1;
     const size_t piece = blockIdx.y * warps + static_cast<long long>(m0) * a.H + unit + w;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -298,31 +308,36 @@ __global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_co
             make_float4(m, l, m == -INFINITY ? m : static_cast<float>(exponent), 0.f);
     }
   };
-  int done = 0;  // pages of this warp before the batch at hand
+  const bool small = all < 0x7fffffff;
+  int done = 0;  // places of this warp before the batch at hand
   for (long long f = f0; f < f1; f += 32) {
-    // 32 pages, a lane each: unit, position, page, scales
+    // 32 places, a lane each: unit (-1: an empty place), position, page, scales
     const int n = static_cast<int>(min(f1 - f, 32LL));
     int key = -1, pos0 = 0, row = -1;
     float2 sc = make_float2(0.f, 0.f);
     if (lane < n) {
-      const long long q = (f + lane) / a.H;
+      const long long q = small ? static_cast<int>(f + lane) / a.H : (f + lane) / a.H;
       int lo = 0, hi = mc;  // the last member that begins at q or before
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
         if (begins[mid] <= q) lo = mid;
         else hi = mid;
       }
-      const int np = static_cast<int>(begins[lo + 1] - begins[lo]);
+      const int places = static_cast<int>(begins[lo + 1] - begins[lo]);
       const long long rem = f + lane - begins[lo] * a.H;
-      const int h = static_cast<int>(rem / np), page = from_s[lo] / kPageSize + static_cast<int>(rem - static_cast<long long>(h) * np);
-      key = lo * a.H + h;
-      pos0 = page * kPageSize;
-      const int id = __ldg(a.page_table + static_cast<size_t>(seq_s[lo]) * a.max_pages + page);
-      if (id < 0 || id >= a.num_pages) {
-        record_error(OSCAR_DEVERR_PAGE_ID);
-      } else {
-        row = id * a.H + h;
-        sc = __ldg(reinterpret_cast<const float2*>(a.scales) + row);
+      const int h = small ? static_cast<int>(rem) / places : static_cast<int>(rem / places);
+      const int place = static_cast<int>(rem - static_cast<long long>(h) * places);
+      if (place < places - kUnitCost) {
+        const int behind = from_s[lo] / kPageSize, page = place + (args.all ? 0 : behind);
+        key = lo * a.H + h;
+        pos0 = page * kPageSize;
+        const int id = __ldg(a.page_table + static_cast<size_t>(page < behind ? lead_s[lo] : seq_s[lo]) * a.max_pages + page);
+        if (id < 0 || id >= a.num_pages) {
+          record_error(OSCAR_DEVERR_PAGE_ID);
+        } else {
+          row = id * a.H + h;
+          sc = __ldg(reinterpret_cast<const float2*>(a.scales) + row);
+        }
       }
     }
     auto issue = [&](int k) {
@@ -343,7 +358,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_co
       for (int k = 0; k < min(n, kStages); ++k) issue(k);
     for (int k = 0; k < n; ++k) {
       const int u = __shfl_sync(0xffffffffu, key, k);
-      if (u != unit) {
+      if (u != unit && u >= 0) {
         if (unit >= 0) flush();
         unit = u;
         const int i = u / a.H, h = u - i * a.H;
@@ -401,54 +416,87 @@ struct MergeArgs {
   int num_members, tm;
 };
 
-// WARPS warps per (member, query head), of four in a block.
-constexpr int kMergeWarps = 4;
-template <int D, int WARPS>
-__global__ void __launch_bounds__(kMergeWarps * 32) kv8_shared_merge_kernel(MergeArgs m) {
-  __shared__ float4 part[kMergeWarps][D / 4];
-  __shared__ float sums[kMergeWarps];
+// One warp per (member, query head), its partials 32 at a time: a lane has the units of one, and all their rows are in flight at
+// once with those (15 partials: 1.8 us behind the lists, where eight in flight and a pass over the units before took 4.4).
+constexpr int kMergeRows = 4;
+template <int D>
+__global__ void __launch_bounds__(kMergeRows * 32, 6) kv8_shared_merge_kernel(MergeArgs m) {
+  constexpr int kSub = 128 / D, kFly = 8;  // D = 64: two half warps take every second partial
   const AttnArgs& a = m.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c4 = lane % (D / 4);
-  const long long row = static_cast<long long>(blockIdx.x) * (kMergeWarps / WARPS) + warp / WARPS;
+  const int lane = threadIdx.x & 31, c4 = lane % (D / 4), sub = lane / (D / 4);
+  const long long row = static_cast<long long>(blockIdx.x) * kMergeRows + (threadIdx.x >> 5);
   grid_dep_wait();
   if (row >= static_cast<long long>(m.num_members) * a.Hq) return;
   const int i = static_cast<int>(row / a.Hq), hq = static_cast<int>(row - static_cast<long long>(i) * a.Hq);
+  const int gqa = a.Hq / a.H, h = hq / gqa, hd = hq - h * gqa;
   const int4 info = m.info[i];
   const int b = __ldg(m.members + i);
-  const int gqa = a.Hq / a.H, h = hq / gqa, hd = hq - h * gqa, x = info.w * gqa + hd;
   const int2 own = m.own[static_cast<size_t>(i) * a.H + h];
   if (info.x < 0 || b < 0 || b >= a.batch) return;  // not a member
   const int n_own = own.y, n = n_own + info.z;
   if (info.z == 0 && n_own <= 1) return;  // written by the kernel before
-  const size_t piece = own.x;
-  const float* own_o = m.own_o + (piece * gqa + hd) * D + 4 * c4;
-  const float* own_ml = m.own_ml + (piece * gqa + hd) * 4;
+  const int x = info.w * gqa + hd;
+  const float* own_o = m.own_o + (static_cast<size_t>(own.x) * gqa + hd) * D + 4 * c4;
+  const float* own_ml = m.own_ml + (static_cast<size_t>(own.x) * gqa + hd) * 4;
   const size_t pre = (static_cast<size_t>(info.x + x / m.tm) * a.H + h) * m.tm + x % m.tm;
   const size_t step = static_cast<size_t>(info.y) * a.H * m.tm;  // from one split to the next
   const float* pre_o = m.pre_o + pre * D + 4 * (c4 ^ (x % m.tm & 7));
-  float l, e;
-  float4 r;
-  merge_parts<D>([&](int k) { return k < n_own ? own_o + static_cast<size_t>(k) * gqa * D : pre_o + (k - n_own) * step * D; },
-                 [&](int k) {
-                   return k < n_own ? own_ml + static_cast<size_t>(k) * gqa * 4 : m.pre_ml + (pre + (k - n_own) * step) * 4;
-                 },
-                 n, warp % WARPS, WARPS, lane, l, r, e);
-  __nv_bfloat16* out = a.out + (static_cast<size_t>(b) * a.Hq + hq) * D + 4 * c4;
-  if (WARPS == 1) {
-    if (lane < D / 4) store_out4(out, r, l, e);
-    return;
-  }
-  if (lane < D / 4) part[warp][lane] = r;
-  if (lane == 0) sums[warp] = l;
-  __syncthreads();
-  if (threadIdx.x < D / 4) {
-    for (int w = 1; w < WARPS; ++w) {
-      const float4 y = part[w][lane];
-      l += sums[w];
-      r.x += y.x; r.y += y.y; r.z += y.z; r.w += y.w;
+  float M = -INFINITY, R = -INFINITY, l = 0.f;  // units of l (2^M) and r (2^(M + R)); l: the lane's part
+  float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    const int cnt = min(n - k0, 32), k = k0 + lane;
+    float4 v = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    if (lane < cnt)
+      v = *reinterpret_cast<const float4*>(k < n_own ? own_ml + static_cast<size_t>(k) * gqa * 4 : m.pre_ml + (pre + (k - n_own) * step) * 4);
+    float4 y[kFly];
+    auto load = [&](int j0) {
+#pragma unroll
+      for (int e = 0; e < kFly; ++e) {
+        const int j = j0 + e * kSub + sub, kk = k0 + j;
+        y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < cnt)
+          y[e] = *reinterpret_cast<const float4*>(kk < n_own ? own_o + static_cast<size_t>(kk) * gqa * D : pre_o + (kk - n_own) * step * D);
+      }
+    };
+    load(0);
+    float m1 = v.x, r1 = v.z;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m1, o), r2 = __shfl_xor_sync(0xffffffffu, r1, o);
+      const float top = fmaxf(m1, m2);
+      if (top > -INFINITY) r1 = fmaxf(r1 + (m1 - top), r2 + (m2 - top));
+      m1 = top;
     }
-    store_out4(out, r, l, e);
+    // onto what there is
+    const float top = fmaxf(M, m1), base = top == -INFINITY ? 0.f : top;
+    const float unit = fmaxf(R + (M - base), r1 + (m1 - base)), base_r = unit == -INFINITY ? 0.f : unit;
+    float f, g;
+    pow2_pair(M - base + R - base_r, f, g);
+    r.x = r.x * f * g; r.y = r.y * f * g; r.z = r.z * f * g; r.w = r.w * f * g;
+    l = l * fast_exp2(M - base) + fast_exp2(v.x - base) * v.y;
+    M = top;
+    R = unit;
+    pow2_pair(v.x - base + v.z - base_r, f, g);
+    for (int j0 = 0; j0 < cnt; j0 += kFly * kSub) {
+      if (j0 > 0) load(j0);
+#pragma unroll
+      for (int e = 0; e < kFly; ++e) {
+        const int j = min(j0 + e * kSub + sub, 31);
+        const float fj = __shfl_sync(0xffffffffu, f, j), gj = __shfl_sync(0xffffffffu, g, j);
+        r.x = fmaf(fj, y[e].x * gj, r.x); r.y = fmaf(fj, y[e].y * gj, r.y);
+        r.z = fmaf(fj, y[e].z * gj, r.z); r.w = fmaf(fj, y[e].w * gj, r.w);
+      }
+    }
   }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (kSub == 2) {
+    r.x += __shfl_xor_sync(0xffffffffu, r.x, 16);
+    r.y += __shfl_xor_sync(0xffffffffu, r.y, 16);
+    r.z += __shfl_xor_sync(0xffffffffu, r.z, 16);
+    r.w += __shfl_xor_sync(0xffffffffu, r.w, 16);
+  }
+  if (lane < D / 4) store_out4(a.out + (static_cast<size_t>(b) * a.Hq + hq) * D + 4 * c4, r, l, R);
 }
 
 struct Plan {
@@ -478,10 +526,10 @@ bool make_plan(const oscar_dims_t* d, int batch, int max_seq_len, int max_prefix
   // should take least by these times (us): of a prefix block (128 tokens), of a CTA's start and end, of the bytes of the members'
   // own tokens, of which half the bound is taken as likely.
   const int sms = num_sms();
-  const double block_us = p->mt == 2 ? 1.7 : p->parts == 1 ? 1.15 : 0.95, start_us = p->mt == 2 ? 13 : 10, own_start_us = 6;
+  const double block_us = p->mt == 2 ? 1.7 : p->parts == 1 ? 1.15 : 0.95, start_us = p->mt == 2 ? 13 : 10, own_start_us = 8;
   const double own_bytes = static_cast<double>(members) * H * max_own * d->head_dim;
   auto own_us = [&](int n) { return own_start_us + own_bytes / fmin(n * 40e3, 5.7e6); };  // 40 KB a us and SM, 5.7 TB/s in all
-  const long long chunk = members < kChunk ? members : kChunk, pages = (static_cast<long long>(max_own) + kPageSize - 1) / kPageSize;
+  const long long chunk = members < kChunk ? members : kChunk;
   p->chunks = (members + kChunk - 1) / kChunk;
   p->items = 0;
   p->prefix_first = false;
@@ -505,12 +553,19 @@ bool make_plan(const oscar_dims_t* d, int batch, int max_seq_len, int max_prefix
     }
     if (items < most_tiles) items = most_tiles;
     if (items > 0x7fffffffLL) return false;
+    // every member by itself, where that should take no longer: small calls, and prefixes that hardly anyone shares
+    const double all_us = own_start_us + (own_bytes + 2.0 * members * H * max_prefix * d->head_dim) / 5.7e6;
+    if (best > 0 && all_us <= best) {
+      items = 0;
+      own_sms = sms;
+    }
     p->items = static_cast<int>(items);
     // what takes longer goes first, if it leaves room for the other
-    p->prefix_first = items * H <= sms - own_sms;
+    p->prefix_first = items > 0 && items * H <= sms - own_sms;
   }
   // blocks of a chunk, fewer where their warps would have nothing
-  const long long use = (chunk * H * pages + kOwnWarps * kLeastPages - 1) / (kOwnWarps * kLeastPages);
+  const long long own_most = static_cast<long long>(max_own) + (p->items == 0 ? max_prefix : 0), pages = (own_most + kPageSize - 1) / kPageSize;
+  const long long use = (chunk * H * (pages + kUnitCost) + kOwnWarps * kLeastPages - 1) / (kOwnWarps * kLeastPages);
   long long most = p->chunks > 0 ? own_sms / p->chunks : 1;
   if (most > use) most = use;
   p->blocks = static_cast<int>(most < 1 ? 1 : most);
@@ -552,12 +607,8 @@ cudaError_t launch(const Plan& p, const SharedArgs& sh, const OwnArgs& ow, const
     if (e != cudaSuccess) return e;
   }
   const long long rows = static_cast<long long>(me.num_members) * me.a.Hq;
-  // Few rows have many partials each: a row a block, its partials all in flight at once.
-  if (rows <= 2LL * num_sms())
-    return launch_pdl(kv8_shared_merge_kernel<D, kMergeWarps>, dim3(static_cast<unsigned>(rows)), dim3(kMergeWarps * 32), 0, stream,
-                      me);
-  return launch_pdl(kv8_shared_merge_kernel<D, 1>, dim3(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps)),
-                    dim3(kMergeWarps * 32), 0, stream, me);
+  return launch_pdl(kv8_shared_merge_kernel<D>, dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows)),
+                    dim3(kMergeRows * 32), 0, stream, me);
 }
 
 }  // namespace
@@ -567,6 +618,20 @@ extern "C" size_t oscar_kv8_decode_shared_workspace_bytes(const oscar_dims_t* di
                                                           int32_t num_groups) {
   Plan p;
   return make_plan(dims, batch, max_seq_len, max_prefix_len, max_own_len, num_members, num_groups, &p) ? p.total : 0;
+}
+
+extern "C" oscar_status_t oscar_kv8_decode_shared_plan(const oscar_dims_t* dims, int32_t batch, int32_t max_seq_len,
+                                                       int32_t max_prefix_len, int32_t max_own_len, int32_t num_members,
+                                                       int32_t num_groups, int32_t* tile_rows, int32_t* prefix_blocks,
+                                                       int32_t* own_blocks) {
+  const oscar_status_t st = check_dims(dims);
+  if (st != OSCAR_OK) return st;
+  Plan p;
+  if (!make_plan(dims, batch, max_seq_len, max_prefix_len, max_own_len, num_members, num_groups, &p)) return OSCAR_ERR_INVALID_ARG;
+  if (tile_rows) *tile_rows = p.items > 0 ? p.tm : 0;
+  if (prefix_blocks) *prefix_blocks = p.items * dims->num_kv_heads;
+  if (own_blocks) *own_blocks = p.blocks * p.chunks;
+  return OSCAR_OK;
 }
 
 extern "C" oscar_status_t oscar_kv8_decode_shared(const oscar_dims_t* dims, int32_t kv_format, int32_t batch,
@@ -599,7 +664,7 @@ extern "C" oscar_status_t oscar_kv8_decode_shared(const oscar_dims_t* dims, int3
   int4* info = reinterpret_cast<int4*>(w + plan.off_info);
   int2* own = reinterpret_cast<int2*>(w + plan.off_own);
   const SharedArgs sh{{a, floats(plan.off_pre_o), floats(plan.off_pre_ml), 0, 0, 0}, g, info, plan.prefix_first, !plan.prefix_first};
-  const OwnArgs ow{a, g, info, own, floats(0), floats(plan.off_ml), max_own_len, !plan.prefix_first, plan.prefix_first && plan.items > 0};
+  const OwnArgs ow{a, g, info, own, floats(0), floats(plan.off_ml), max_own_len, !plan.prefix_first, plan.prefix_first && plan.items > 0, plan.items == 0 && max_prefix_len >= kPageSize};
   const MergeArgs me{a, members, info, own, floats(0), floats(plan.off_ml), floats(plan.off_pre_o), floats(plan.off_pre_ml),
                      num_members, plan.tm};
   cudaStream_t s = as_stream(stream);

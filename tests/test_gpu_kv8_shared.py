@@ -78,6 +78,12 @@ class Case:
                                    self.t_lens if lens is None else lens, members, start, prefix, 0.0, out, work, stream)
         return out
 
+    def tile_rows(self):
+        """Of the prefix kernel's tiles; 0 where members attend their prefixes by themselves."""
+        own = max(int(self.lens[b]) - p for g, p in enumerate(self.prefix) for b in self.members[self.start[g]:self.start[g + 1]])
+        return ok.oscar_kv8_decode_shared_plan(self.dims, self.batch, int(self.lens.max()), max(self.prefix), own, len(self.members),
+                                               len(self.prefix))["tile_rows"]
+
     def check(self, out, members=None, lens=None):
         members = self.members if members is None else members
         lens = self.lens if lens is None else lens
@@ -111,6 +117,26 @@ def test_shared(hq, H, D, fmt, groups):
     c.check(c.run())
 
 
+# large enough for the kernel over prefixes: tiles of 64, 128 and 256 rows, ragged ones, queries of a member in two tiles, groups of
+# one, prefixes of fewer blocks than a split
+TILED = [((8, 8, 128), 64, [(16000, [5, 0, 300, 16] * 9)] + [(48 * 16, [9])] * 4 + [(0, [700, 0])]),
+         ((32, 8, 128), 64, [(8192, list(range(11))), (8016, [0, 1000]), (12000, [90] * 13), (4000, [2, 3]), (11104, [1] * 15)]),
+         ((5, 1, 64), 128, [(40000, [7 * i for i in range(24)])]),
+         ((24, 8, 128), 128, [(9600, [40] * 41), (9008, [17])]),
+         ((7, 1, 128), 256, [(30000, [3] * 90), (16, [40, 1])]),
+         ((20, 4, 64), 256, [(20000, [100, 0, 33] * 40), (0, [64, 1]), (15888, [5] * 77)]),
+         ((64, 8, 128), 256, [(4096, [50] * 37), (100, [1, 2])])]
+
+
+@pytest.mark.parametrize("fmt", [R.E4M3, R.INT8])
+@pytest.mark.parametrize("shape,rows,groups", TILED, ids=lambda x: str(x)[:24])
+def test_shared_over_tiles(shape, rows, groups, fmt):
+    groups = [(p // 16 * 16, m) for p, m in groups]
+    c = Case(*shape, fmt, groups, seed=rows + shape[0])
+    assert c.tile_rows() == rows
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("fmt", [R.E4M3, R.INT8])
 def test_more_groups_than_a_warp_has_lanes(fmt):
     rng = np.random.default_rng(1)
@@ -119,9 +145,27 @@ def test_more_groups_than_a_warp_has_lanes(fmt):
     c.check(c.run())
 
 
+def test_more_groups_than_a_warp_has_lanes_over_tiles():
+    rng = np.random.default_rng(1)
+    groups = [(int(rng.integers(0, 200)) * 16, rng.integers(0, 90, rng.integers(0, 9)).tolist()) for _ in range(75)] + [(8000, [5] * 99)]
+    c = Case(8, 2, 128, R.E4M3, groups, seed=5)
+    assert c.tile_rows() > 0
+    c.check(c.run())
+
+
+def test_more_groups_than_the_table_of_their_tiles_and_members_than_a_chunk():
+    # 2048 groups' tiles are kept in shared memory, and 384 members' pages are dealt out together
+    c = Case(4, 1, 64, R.INT8, [(32, [3])] * 2100 + [(6400, list(range(60)) * 10), (48, [1, 2])], seed=14)
+    assert c.tile_rows() > 0
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("heads", [1, 40, 200])
 def test_heads_fewer_and_more_than_fit_a_wave(heads):
     c = Case(heads, heads, 64, R.INT8, [(1600, [9] * 5), (800, [40, 0, 3])], seed=heads)
+    c.check(c.run())
+    c = Case(heads, heads, 64, R.INT8, [(16000, [9] * 70), (800, [40, 0, 3])], seed=heads)
+    assert c.tile_rows() > 0
     c.check(c.run())
 
 
@@ -135,6 +179,11 @@ def test_bounds_below_the_prefixes_leave_the_rest_to_the_members():
     for bound in (0, 15, 16, 100, 511):
         c.check(c.run(max_prefix=bound))
     c.check(c.run(max_own=532, max_len=544))  # far above what there is
+    c = Case(6, 2, 128, R.INT8, [(20000, [20, 0] * 30), (96, [1, 5, 9])], seed=4)
+    assert c.tile_rows() > 0
+    for bound in (15000, 19999):
+        c.check(c.run(max_prefix=bound))
+    c.check(c.run(max_own=20016, max_len=20032))
 
 
 def test_prefixes_that_are_not_whole_pages():
@@ -145,33 +194,43 @@ def test_prefixes_that_are_not_whole_pages():
 
 def test_v_scales_far_apart():
     for spread in (9, 40):
-        c = Case(8, 2, 128, R.E4M3, [(512, [20] * 33), (256, [50] * 3)], seed=7, spread=spread)
-        c.check(c.run())
+        for prefix in (512, 12000):
+            c = Case(8, 2, 128, R.E4M3, [(prefix, [20] * 99), (256, [50] * 3)], seed=7, spread=spread)
+            assert (c.tile_rows() > 0) == (prefix > 512)
+            c.check(c.run())
 
 
-def test_members_shorter_than_the_prefix_and_empty_ones():
-    c = Case(4, 2, 128, R.INT8, [(512, [20, 30, 40, 50]), (256, [0, 4])], seed=8)
+# the same cases small (every member by itself) and over tiles
+SMALL, LARGE = [(512, [20, 30, 40, 50]), (256, [0, 4])], [(20000, [20, 30, 40, 50] * 20), (256, [0, 4])]
+
+
+@pytest.mark.parametrize("groups", [SMALL, LARGE], ids=["small", "tiles"])
+def test_members_shorter_than_the_prefix_and_empty_ones(groups):
+    c = Case(4, 2, 128, R.INT8, groups, seed=8)
+    assert (c.tile_rows() > 0) == (groups is LARGE)
     lens = c.lens.copy()
-    lens[c.members[0]], lens[c.members[2]], lens[c.members[4]] = 300, 0, 17
+    lens[c.members[0]], lens[c.members[2]], lens[c.members[-2]] = 300, 0, 17
     c.check(c.run(lens=torch.from_numpy(lens).cuda()), lens=lens)
     lens[:] = 0
     out = c.run(lens=torch.from_numpy(lens).cuda())
     assert (out[c.members] == 0).all() and ok.oscar_device_errors(reset=True) == 0
 
 
-def test_some_of_the_sequences_in_any_order():
-    c = Case(4, 2, 128, R.E4M3, [(512, [20, 30, 40, 50]), (256, [0, 4])], seed=9)
-    m = c.members
-    some = [m[3], m[0], m[5]]
-    c.check(c.run(lists=(some, [0, 2, 3], [512, 0]), max_own=300), members=some)
+@pytest.mark.parametrize("groups", [SMALL, LARGE], ids=["small", "tiles"])
+def test_some_of_the_sequences_in_any_order(groups):
+    c = Case(4, 2, 128, R.E4M3, groups, seed=9)
+    m, p = c.members, groups[0][0]
+    some = [m[3], m[0], m[-1]]
+    c.check(c.run(lists=(some, [0, 2, 3], [p, 0]), max_own=300), members=some)
     # fewer members than entries: those behind the last group are none
-    c.check(c.run(lists=(m, [0, 2, 2], [512, 0])), members=m[:2])
+    c.check(c.run(lists=(m, [0, 2, 2], [p, 0])), members=m[:2])
 
 
-def test_bad_numbers_are_flagged_and_nothing_else_is_touched():
-    c = Case(4, 2, 128, R.INT8, [(512, [20, 30, 40, 50]), (256, [0, 4])], seed=10)
-    m, P = c.members, ok.OSCAR_DEVERR_POSITION
-    for start in ([0, 4, 3], [0, 4, 7], [1, 4, 6], [0, -1, 6], [0, 7, 6], [0, 2 ** 31 - 1, 6]):
+@pytest.mark.parametrize("groups", [SMALL, LARGE], ids=["small", "tiles"])
+def test_bad_numbers_are_flagged_and_nothing_else_is_touched(groups):
+    c = Case(4, 2, 128, R.INT8, groups, seed=10)
+    m, P, n, t, p = c.members, ok.OSCAR_DEVERR_POSITION, len(groups[0][1]), len(c.members), groups[0][0]
+    for start in ([0, n, n - 1], [0, n, t + 1], [1, n, t], [0, -1, t], [0, t + 1, t], [0, 2 ** 31 - 1, t]):
         out = c.run(lists=(m, start, c.prefix))
         assert (out == 7).all() and ok.oscar_device_errors(reset=True) == P, start
     for bad in (-1, c.batch, 2 ** 31 - 1):
@@ -184,13 +243,13 @@ def test_bad_numbers_are_flagged_and_nothing_else_is_touched():
     assert ok.oscar_device_errors(reset=True) & ok.OSCAR_DEVERR_SEQ_LEN
     out = c.run(max_own=32)  # 40 and 50 tokens are cut off
     assert ok.oscar_device_errors(reset=True) == ok.OSCAR_DEVERR_SEQ_LEN
-    cut = np.minimum(c.lens, [544 if b in m[:4] else 10 ** 6 for b in range(c.batch)])
+    cut = np.minimum(c.lens, [p + 32 if b in m[:n] else 10 ** 6 for b in range(c.batch)])
     c.check(out, lens=cut)
     keep = c.t_table.clone()
     c.t_table[m[0], 3] = c.dims.num_pages
-    c.t_table[m[4], 16:] = -1
+    c.t_table[m[-2], 16:] = -1
     c.table = c.t_table.cpu().numpy()
-    for b in m[1:4]:  # the prefix is read through the first member's pages
+    for b in m[1:n]:  # the prefix is read through the first member's pages
         c.table[b, 3] = -1
     out = c.run()
     assert ok.oscar_device_errors(reset=True) == ok.OSCAR_DEVERR_PAGE_ID
@@ -198,8 +257,9 @@ def test_bad_numbers_are_flagged_and_nothing_else_is_touched():
     c.t_table = keep
 
 
-def test_nan_queries_and_pages_behind_the_tokens():
-    c = Case(4, 2, 128, R.E4M3, [(512, [20, 30, 40])], seed=11)
+@pytest.mark.parametrize("groups", [SMALL, LARGE], ids=["small", "tiles"])
+def test_nan_queries_and_pages_behind_the_tokens(groups):
+    c = Case(4, 2, 128, R.E4M3, groups, seed=11)
     clean = c.run()
     for b in range(c.batch):  # NaN codes behind every last token
         n = int(c.lens[b])
@@ -214,8 +274,9 @@ def test_nan_queries_and_pages_behind_the_tokens():
 
 
 def test_the_same_call_twice_on_two_streams_and_captured():
-    a = Case(8, 2, 128, R.E4M3, [(2048, [100] * 20), (512, [9, 700])], seed=12)
-    b = Case(8, 2, 128, R.E4M3, [(1024, [10] * 70)], seed=13)
+    a = Case(8, 2, 128, R.E4M3, [(20000, [100] * 40), (512, [9, 700])], seed=12)
+    b = Case(8, 2, 128, R.E4M3, [(10240, [10] * 70)], seed=13)
+    assert a.tile_rows() > 0 and b.tile_rows() > 0
     want = a.run(), b.run()
     a.check(want[0])
     streams = torch.cuda.Stream(), torch.cuda.Stream()

@@ -47,8 +47,15 @@ def test_decode_shared_refusals(lib):
 def test_decode_shared_workspaces(lib, kw):
     a = {**dict(max_len=300, prefix=200, own=100, members=4, groups=2), **kw}
     for heads in ((32, 8), (1, 1), (200, 200), (1600, 200)):
-        n = lib.oscar_kv8_decode_shared_workspace_bytes(dims(num_q_heads=heads[0], num_kv_heads=heads[1]), 4, *a.values())
+        d = dims(num_q_heads=heads[0], num_kv_heads=heads[1])
+        n = lib.oscar_kv8_decode_shared_workspace_bytes(d, 4, *a.values())
         assert 0 < n < 1 << 40
+        t, p, o = (ctypes.c_int32(-1) for _ in range(3))
+        assert lib.oscar_kv8_decode_shared_plan(d, 4, *a.values(), ctypes.byref(t), ctypes.byref(p), ctypes.byref(o)) == OK
+        assert t.value in (0, 64, 128, 256) and (t.value > 0) == (p.value > 0) and o.value > 0
+        assert lib.oscar_kv8_decode_shared_plan(d, 4, *a.values(), None, None, None) == OK
+    assert lib.oscar_kv8_decode_shared_plan(d, 4, 300, 301, 0, 4, 2, None, None, None) == BAD
+    assert lib.oscar_kv8_decode_shared_plan(None, 4, 300, 300, 0, 4, 2, None, None, None) == BAD
 
 
 def test_groups_refusals(lib):
