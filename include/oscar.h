@@ -655,14 +655,15 @@ oscar_status_t oscar_kv8_extend_varlen(const oscar_dims_t* dims, int32_t kv_form
  * oscar_pages_fork leaves them: each group's prefix is attended once for all its members, on tensor cores, what a member has
  * behind it by itself, and the two are joined by log-sum-exp.  The result is that of oscar_kv8_decode, but that weights are
  * held in 11 bits (as oscar_kv8_extend_varlen's over the prefixes, and with a step of 2^-30 of the row's largest elsewhere); the
- * output has 8.
+ * output has 8.  Where that would take longer than each member by itself (small calls, short prefixes), each attends all of its
+ * own.
  * Arguments beyond oscar_kv8_decode's
  *   num_members   entries of `members` at most; num_groups: of prefix_lens
  *   members       device int32 [num_members]: the sequences to decode, group after group
  *   group_start   device int32 [num_groups + 1], non-decreasing, group_start[0] = 0: group g is members group_start[g] ..
  *                 group_start[g + 1] - 1; members from group_start[num_groups] <= num_members on are none
  *   prefix_lens   device int32 [num_groups]: the tokens that all members of the group share, of which whole pages are attended
- *                 together, read through the page table of the group's first member; 0 for sequences by themselves
+ *                 together, read through any member's page table; 0 for sequences by themselves
  *   max_prefix_len  host bound: of a longer prefix the first max_prefix_len tokens (whole pages) are attended together, and the
  *                 rest with each member's own
  *   max_own_len   host bound on what any member has behind that; longer ones are cut off and flagged (OSCAR_DEVERR_SEQ_LEN)

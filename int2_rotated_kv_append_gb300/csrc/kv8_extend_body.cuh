@@ -176,35 +176,28 @@ struct Item {
 // The item of block x of `limit` (at least as many as there are tiles).  Every (tile, split) of every group is one, and a split's
 // length is the same for all groups: the shortest, but at least kLeast, with which there are `limit` items at most.  The groups'
 // tiles and blocks go into `table` (shared memory), and every warp finds the length for itself.
-constexpr int kTable = 2048;  // groups; more are read again
+constexpr int kTable = 1024;  // groups at most: lists of more have more tiles than there are items
 template <int TM>
 __device__ __forceinline__ Item item_of(const SharedArgs& s, int x, int limit, int2* table) {
   constexpr int kLeast = 4;
   constexpr uint32_t kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31, gqa = s.e.a.Hq / s.e.a.H;
   Item it{};
-  auto look = [&](int g, bool& fine) {
-    int start, n, prefix;
-    fine = group_of(s.g, g, start, n, prefix);
-    const int blocks = (prefix / kPageSize + kBlkPages - 1) / kBlkPages;
-    const int tiles = fine && blocks > 0 ? static_cast<int>((static_cast<long long>(n) * gqa + TM - 1) / TM) : 0;
-    return make_int2(tiles, tiles > 0 ? blocks : 0);
-  };
   bool bad = false;
   for (int g = threadIdx.x; g < s.g.num_groups; g += blockDim.x) {
-    bool fine;
-    const int2 v = look(g, fine);
+    int start, n, prefix;
+    const bool fine = group_of(s.g, g, start, n, prefix);
     bad = bad || !fine;
-    if (g < kTable) table[g] = v;
+    const int blocks = (prefix / kPageSize + kBlkPages - 1) / kBlkPages;
+    const int tiles = fine && blocks > 0 ? static_cast<int>((static_cast<long long>(n) * gqa + TM - 1) / TM) : 0;
+    table[g] = make_int2(tiles, tiles > 0 ? blocks : 0);
   }
   it.bad = __syncthreads_or(bad);
   if (it.bad) return it;
-  bool unused;
-  auto group = [&](int g) { return g < kTable ? table[g] : look(g, unused); };
   int longest = 0, tiles = 0;
   long long all = 0;  // blocks
   for (int g = lane; g < s.g.num_groups; g += 32) {
-    const int2 v = group(g);
+    const int2 v = table[g];
     tiles += v.x;
     longest = max(longest, v.y);
     all += static_cast<long long>(v.x) * v.y;
@@ -218,14 +211,14 @@ __device__ __forceinline__ Item item_of(const SharedArgs& s, int x, int limit, i
   const int lo = max(min(kLeast, longest), static_cast<int>((all + limit - 1) / limit)), mine = lo + lane;
   long long sum = 0;
   for (int g = 0; g < s.g.num_groups; ++g) {
-    const int2 v = group(g);
+    const int2 v = table[g];
     sum += static_cast<long long>(v.x) * ((v.y + mine - 1) / mine);
   }
   const uint32_t fits = __ballot_sync(kAll, sum <= limit);
   it.bps = fits != 0 ? lo + __ffs(fits) - 1 : tiles < limit ? static_cast<int>((all + limit - tiles - 1) / (limit - tiles)) : longest;
   int before = 0;
   for (int g0 = 0; g0 < s.g.num_groups; g0 += 32) {
-    const int2 v = g0 + lane < s.g.num_groups ? group(g0 + lane) : make_int2(0, 0);
+    const int2 v = g0 + lane < s.g.num_groups ? table[g0 + lane] : make_int2(0, 0);
     const int splits = (v.y + it.bps - 1) / it.bps;
     int sum = v.x * splits;
 #pragma unroll
@@ -384,19 +377,65 @@ __device__ __forceinline__ void extend_body(const Args& args) {
   const int wg = warp >> 2;
   const bool fetches = warp == kFetchK || warp == kFetchV;  // these start at once; the others get Q and TMEM ready
   if (warp == kQkWarp) umma::tmem_alloc(sb + G::kMisc, 512);
-  // Q as fp16, K-major with the 128-byte swizzle, by the warps of the softmax.  The rows come by copies, one for each position (or
-  // member) and its query heads, into the memory of the V operands; then a lane takes 8 channels of a row, row after row.  (Little
-  // code: what runs once waits for its instructions more than for anything else, all SMs fetching the same ones.  With a register
-  // for every row's load this took 4 us.)
-  if (wg < MT) {
+  // Q as fp16, K-major with the 128-byte swizzle: a lane takes 8 channels of a row, and every load is in flight at once
+  if (!SHARED && wg < 3) {
+    constexpr int kLanes = D / 8, kAtOnce = 12 * 32 / kLanes;  // lanes of a row; rows of one round of the 12 warps
+    constexpr int kRounds = (MT * 128 / PARTS + kAtOnce - 1) / kAtOnce;
+    const int c = lane % kLanes, r0 = tid / kLanes;
+    int x = T.r0 + r0, i = x / gqa, hd = x - i * gqa;
+    const __nv_bfloat16* src = a.q + (static_cast<size_t>(T.q0) * a.Hq + h * gqa) * D + 8 * c;
+    uint4 v[kRounds];
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+      v[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (r0 + k * kAtOnce < T.rows)
+        v[k] = __ldg(reinterpret_cast<const uint4*>(src + (static_cast<size_t>(i) * a.Hq + hd) * D));
+      i += kAtOnce / gqa;
+      hd += kAtOnce % gqa;
+      if (hd >= gqa) {
+        hd -= gqa;
+        ++i;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+      const int r = r0 + k * kAtOnce;
+      uint32_t mx = __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
+                             __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu));
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      mx = max(mx & 0xffffu, mx >> 16);
+      const int e = min(max(static_cast<int>(mx >> 7) - 127, -126), 126);
+      const float inv = pow2i(-e);
+      const uint32_t in[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      uint32_t y[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        y[q] = half2_bits(__uint_as_float(in[q] << 16) * inv, __uint_as_float(in[q] & 0xffff0000u) * inv);
+      if (r < active * 128 / PARTS) {
+#pragma unroll
+        for (int copy = 0; copy < PARTS; ++copy) {
+          const int rr = r + copy * (128 / PARTS);
+          st_shared_v4(sb + G::kQ + (rr >> 7) * G::kOp + umma::sw128_offset(rr & 127, 8 * c, 128), y[0], y[1], y[2],
+                       y[3]);
+          if (c == 0) q_scale[rr] = pow2i(e) * a.scale_log2;
+        }
+      }
+    }
+  }
+  // SHARED: by the warps of the softmax alone, so that the others begin.  The rows come by copies, one for each member and its query
+  // heads, into the memory of the V operands; then a lane takes 8 channels of a row, row after row.  (Little code: in a short run
+  // what runs once waits for its instructions more than for anything else, all SMs fetching the same ones; the form above,
+  // with the members' numbers before the rows, took 5 us.)
+  if (SHARED && wg < MT) {
     constexpr int kLanes = D / 8, kAtOnce = MT * 128 / kLanes;  // lanes of a row; rows of one round
     constexpr int kRounds = (kRowsOfTile + kAtOnce - 1) / kAtOnce;
     const uint32_t stage = sb + G::kV;
     if (tid == 0) mbar_arrive_expect_tx(bar(kQRaw), T.rows * D * 2);
     if (const int i = T.r0 / gqa + tid; i <= (T.r0 + T.rows - 1) / gqa) {
       const int x0 = max(i * gqa, T.r0), x1 = min(i * gqa + gqa, T.r0 + T.rows);
-      size_t row = T.q0 + i;
-      if constexpr (SHARED) row = in_batch(__ldg(args.g.members + row), a.batch);
+      size_t row = 0;
+      if constexpr (SHARED) row = in_batch(__ldg(args.g.members + T.q0 + i), a.batch);
       bulk_g2s(stage + (x0 - T.r0) * (D * 2), a.q + (row * a.Hq + h * gqa + (x0 - i * gqa)) * D, (x1 - x0) * D * 2, bar(kQRaw));
     }
     __syncwarp();
@@ -434,14 +473,14 @@ __device__ __forceinline__ void extend_body(const Args& args) {
       }
     }
   }
-  // Q and TMEM are there: for all but the fetching warps, those that expand codes after a first round (below).
+  // Q and TMEM are there: for all but the fetching warps (SHARED: for those that expand codes after a first round, below).
   auto q_ready = [&]() {
     fence_async();
     umma::fence_before_sync();
     asm volatile("bar.sync 1, %0;" ::"n"(kThreads - 64) : "memory");
     umma::fence_after_sync();
   };
-  const bool expands = wg >= MT && wg < 3;
+  const bool expands = SHARED && wg >= MT && wg < 3;
   if (!fetches && !expands) q_ready();
   const uint32_t tmem = fetches || expands ? 0u : misc[0];
   // logits, weights, accumulators
@@ -796,12 +835,12 @@ __device__ __forceinline__ void extend_body(const Args& args) {
     const uint32_t dst0 = sb + G::kK + (c >> 2) * (kTok * 128) + r0 * 128 + (((2 * (c & 3)) ^ (r0 & 7)) << 4);
     const uint32_t dst1 = sb + G::kK + (c >> 2) * (kTok * 128) + r0 * 128 + (((2 * (c & 3) + 1) ^ (r0 & 7)) << 4);
     bool ok = true;
-    // The first round (y = -1) is for the instruction cache, before any codes are there: it expands whatever lies in the first
+    // SHARED: the first round (y = -1) is for the instruction cache, before any codes are there: it expands whatever lies in the first
     // stage into the K operands, which the first real rounds overwrite.
 #pragma unroll 1
-    for (int y = -1; y < (MT == 2 ? 2 : 1) * cnt; ++y) {
-      const bool dry = y < 0;
-      const int x = max(y, 0);
+    for (int y = SHARED ? -1 : 0; y < (MT == 2 ? 2 : 1) * cnt; ++y) {
+      const bool dry = SHARED && y < 0;
+      const int x = SHARED ? max(y, 0) : y;
       const int j = MT == 2 ? x >> 1 : x, side = MT == 2 ? x & 1 : 2 - wg;
       const int op = 2 * side + (j & 1), rx = G::kWhole ? j : x, st = rx % G::kRing;
       ok = dry || (mbar_wait_bounded(bar(kRawFull + st), (rx / G::kRing) & 1) &&

@@ -25,5 +25,19 @@ __device__ __forceinline__ bool group_of(const Groups& s, int g, int& start, int
 // A member's sequence, in range: one that is not is flagged, and left without a result, where members' own parts are attended.
 __device__ __forceinline__ int in_batch(int b, int batch) { return min(max(b, 0), batch - 1); }
 
+// One warp: the prefix of member i's group; kBadLists, or kNoGroup where i is behind the last group's members.
+constexpr int kBadLists = -1, kNoGroup = -2;
+__device__ __forceinline__ int prefix_of_member(const Groups& s, int i, int lane) {
+  int got = kNoGroup;
+  for (int g0 = 0; g0 < s.num_groups; g0 += 32) {
+    int start = 0, n = 0, prefix = 0;
+    const bool fine = g0 + lane >= s.num_groups || group_of(s, g0 + lane, start, n, prefix);
+    if (__any_sync(0xffffffffu, !fine)) return kBadLists;
+    const uint32_t mine = __ballot_sync(0xffffffffu, i >= start && i < start + n);
+    if (mine != 0) got = __shfl_sync(0xffffffffu, prefix, __ffs(mine) - 1);  // (the rest of the list is looked at as well)
+  }
+  return got;
+}
+
 }  // namespace kv8
 }  // namespace oscar

@@ -1,6 +1,7 @@
 // Decode attention of sequences that share prefixes (oscar_kv8_decode_shared), over the 8-bit paged cache.
 //
-// Three kernels, of which the first two run beside one another.  One takes every group's prefix once, for all its members: their
+// Where that would take longer than each member by itself, as in small calls, it is the decode's split kernel over the list, and a
+// merge.  Else three kernels, of which the first two run beside one another.  One takes every group's prefix once, for all its members: their
 // queries are the rows of tiles on tcgen05, as in the extend, and the prefix is cut into splits so that the tiles of all groups
 // fill whole waves.  The lists are on the device, so the cut is made there, by every block for itself.  The other attends what
 // each member has of its own, as the decode does.  The former is bound by products and the latter by memory, and either fills an
@@ -8,8 +9,8 @@
 //
 // Against reading every member's whole sequence this trades the prefix's bytes, once instead of once a member, for products
 // at the tensor cores' rate.
+#include "kv8_decode_body.cuh"
 #include "kv8_extend_body.cuh"
-#include "kv8_mma.cuh"
 
 namespace {
 
@@ -43,8 +44,7 @@ constexpr int kLeastPages = 4;  // of a warp
 constexpr int kUnitCost = 2;    // pages in whose time a warp goes from one unit to the next: as many places without a page
 constexpr float kOwnLazy = 8.f;  // log2
 constexpr int kOwnBoost = 6;     // 2^(kOwnLazy + kOwnBoost) < 65504
-constexpr float kBigScale = 0x1p80f;  // up to here 2^80 times a code (2^9) times 2^kOwnLazy times 2^27 tokens is within fp32
-constexpr int kBigUnit = 40;
+constexpr float kOwnBigScale = 0x1p80f;  // up to here 2^80 times a code (2^9) times 2^kOwnLazy times 2^27 tokens is within fp32
 
 // Pages of a warp's ring, 16 KB.
 template <int D>
@@ -63,7 +63,6 @@ struct OwnArgs {
   float* part_ml;
   int max_own;    // tokens
   bool first, last;  // of the two kernels that run beside one another
-  bool all;          // every member attends its prefix by itself too (there is no prefix kernel)
 };
 
 template <int D>
@@ -179,7 +178,6 @@ __global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_co
   extern __shared__ uint8_t raw[];
   __shared__ long long begins[kChunk + 1];  // places of one head before member i
   __shared__ int from_s[kChunk], seq_s[kChunk], len_s[kChunk];  // member i: its group's prefix, sequence, length
-  __shared__ int lead_s[kChunk];                                // its group's first member, whose pages the prefix is read from
   __shared__ long long sums[kOwnWarps];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const AttnArgs& a = args.a;
@@ -206,11 +204,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_co
     const int lo = max(start, m0), hi = bad ? lo : min(start + n, m0 + mc);
     for (uint32_t some = __ballot_sync(0xffffffffu, lo < hi); some != 0; some &= some - 1) {
       const int at = __ffs(some) - 1, end = __shfl_sync(0xffffffffu, hi, at), p = __shfl_sync(0xffffffffu, prefix, at);
-      const int lead = __shfl_sync(0xffffffffu, start, at);
-      for (int i = __shfl_sync(0xffffffffu, lo, at) + lane; i < end; i += 32) {
-        from_s[i - m0] = p;
-        lead_s[i - m0] = lead;
-      }
+      for (int i = __shfl_sync(0xffffffffu, lo, at) + lane; i < end; i += 32) from_s[i - m0] = p;
     }
   }
   bad = __syncthreads_or(bad);
@@ -224,16 +218,14 @@ __global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_co
       record_error(OSCAR_DEVERR_SEQ_LEN);
       L = from + args.max_own;
     }
-    pages = max((L + kPageSize - 1) / kPageSize - (args.all ? 0 : from / kPageSize), 0);
-    if (args.all && from > 0) lead_s[tid] = in_batch(__ldg(args.g.members + lead_s[tid]), a.batch);
+    pages = max((L + kPageSize - 1) / kPageSize - from / kPageSize, 0);
   } else if (tells && in) {
     record_error(OSCAR_DEVERR_POSITION);
   }
   seq_s[tid] = b;
   len_s[tid] = L;
-  const bool alone = from == 0 || args.all;  // no part of the member is the prefix kernel's
-  if (tells && tid < mc && (!in || alone)) args.info[m0 + tid] = make_int4(in && good ? 0 : -1, 0, 0, 0);
-  if (in && good && alone && L == 0 && tid % gridDim.x == blockIdx.x)  // nothing to attend
+  if (tells && tid < mc && (!in || from == 0)) args.info[m0 + tid] = make_int4(in && good ? 0 : -1, 0, 0, 0);
+  if (in && good && from == 0 && L == 0 && tid % gridDim.x == blockIdx.x)  // nothing to attend
     for (int c = 0; c < a.Hq * (D / 8); ++c)
       reinterpret_cast<uint4*>(a.out + static_cast<size_t>(b) * a.Hq * D)[c] = make_uint4(0, 0, 0, 0);
   const int places = pages > 0 ? pages + kUnitCost : 0;
@@ -284,7 +276,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_co
       sums_u.l.x += __shfl_xor_sync(0xffffffffu, sums_u.l.x, x);
       sums_u.l.y += __shfl_xor_sync(0xffffffffu, sums_u.l.y, x);
     }
-    const bool whole = (from_s[i] == 0 || args.all) && at >= f0 && at + places - kUnitCost <= f1;
+    const bool whole = from_s[i] == 0 && at >= f0 && at + places - kUnitCost <= f1;
     const size_t piece = blockIdx.y * warps + static_cast<long long>(m0) * a.H + unit + w;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -328,10 +320,10 @@ __global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_co
       const int h = small ? static_cast<int>(rem) / places : static_cast<int>(rem / places);
       const int place = static_cast<int>(rem - static_cast<long long>(h) * places);
       if (place < places - kUnitCost) {
-        const int behind = from_s[lo] / kPageSize, page = place + (args.all ? 0 : behind);
+        const int page = from_s[lo] / kPageSize + place;
         key = lo * a.H + h;
         pos0 = page * kPageSize;
-        const int id = __ldg(a.page_table + static_cast<size_t>(page < behind ? lead_s[lo] : seq_s[lo]) * a.max_pages + page);
+        const int id = __ldg(a.page_table + static_cast<size_t>(seq_s[lo]) * a.max_pages + page);
         if (id < 0 || id >= a.num_pages) {
           record_error(OSCAR_DEVERR_PAGE_ID);
         } else {
@@ -386,7 +378,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_co
       const int r = __shfl_sync(0xffffffffu, row, k), p = __shfl_sync(0xffffffffu, pos0, k);
       float2 s = make_float2(__shfl_sync(0xffffffffu, sc.x, k), __shfl_sync(0xffffffffu, sc.y, k));
       if (r >= 0) {
-        if (exponent == 0 && s.y > kBigScale) {  // rare
+        if (exponent == 0 && s.y > kOwnBigScale) {  // rare
           exponent = kBigUnit;
 #pragma unroll
           for (int j = 0; j < kNt; ++j) sums_u.o[j] = f2mul(sums_u.o[j], make_float2(pow2i(-kBigUnit), pow2i(-kBigUnit)));
@@ -404,6 +396,12 @@ __global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_co
   if (args.last && blockIdx.x + 1 == gridDim.x && blockIdx.y + 1 == gridDim.y) grid_dep_wait();
 }
 
+template <int F, int D>
+__global__ void __launch_bounds__(kWarps * 32, 3) kv8_list_kernel(const __grid_constant__ CUtensorMap map,
+                                                                  const __grid_constant__ ListArgs args) {
+  split_body<F, D, true>(map, args);
+}
+
 struct MergeArgs {
   AttnArgs a;
   const int32_t* members;
@@ -416,15 +414,17 @@ struct MergeArgs {
   int num_members, tm;
 };
 
-// One warp per (member, query head), its partials 32 at a time: a lane has the units of one, and all their rows are in flight at
-// once with those (15 partials: 1.8 us behind the lists, where eight in flight and a pass over the units before took 4.4).
-constexpr int kMergeRows = 4;
-template <int D>
-__global__ void __launch_bounds__(kMergeRows * 32, 6) kv8_shared_merge_kernel(MergeArgs m) {
-  constexpr int kSub = 128 / D, kFly = 8;  // D = 64: two half warps take every second partial
+// WARPS of a block's four warps per (member, query head), 32 / WARPS partials at a time: a lane has the units of one.
+constexpr int kMergeWarps = 4;
+template <int D, int WARPS>
+__global__ void __launch_bounds__(kMergeWarps * 32, 6) kv8_shared_merge_kernel(MergeArgs m) {
+  __shared__ float4 part[kMergeWarps][D / 4];
+  __shared__ float4 units[kMergeWarps];
+  constexpr int kPass = 32 / WARPS, kSub = 128 / D, kFly = 8;  // D = 64: two half warps take every second partial
   const AttnArgs& a = m.a;
   const int lane = threadIdx.x & 31, c4 = lane % (D / 4), sub = lane / (D / 4);
-  const long long row = static_cast<long long>(blockIdx.x) * kMergeRows + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5;
+  const long long row = static_cast<long long>(blockIdx.x) * (kMergeWarps / WARPS) + warp / WARPS;
   grid_dep_wait();
   if (row >= static_cast<long long>(m.num_members) * a.Hq) return;
   const int i = static_cast<int>(row / a.Hq), hq = static_cast<int>(row - static_cast<long long>(i) * a.Hq);
@@ -443,8 +443,8 @@ __global__ void __launch_bounds__(kMergeRows * 32, 6) kv8_shared_merge_kernel(Me
   const float* pre_o = m.pre_o + pre * D + 4 * (c4 ^ (x % m.tm & 7));
   float M = -INFINITY, R = -INFINITY, l = 0.f;  // units of l (2^M) and r (2^(M + R)); l: the lane's part
   float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < n; k0 += 32) {
-    const int cnt = min(n - k0, 32), k = k0 + lane;
+  for (int k0 = warp % WARPS * kPass; k0 < n; k0 += 32) {
+    const int cnt = min(n - k0, kPass), k = k0 + lane;
     float4 v = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
     if (lane < cnt)
       v = *reinterpret_cast<const float4*>(k < n_own ? own_ml + static_cast<size_t>(k) * gqa * 4 : m.pre_ml + (pre + (k - n_own) * step) * 4);
@@ -496,10 +496,34 @@ __global__ void __launch_bounds__(kMergeRows * 32, 6) kv8_shared_merge_kernel(Me
     r.z += __shfl_xor_sync(0xffffffffu, r.z, 16);
     r.w += __shfl_xor_sync(0xffffffffu, r.w, 16);
   }
+  if (WARPS > 1) {  // (a block has one row: all of it is here)
+    if (lane < D / 4) part[warp][lane] = r;
+    if (lane == 0) units[warp] = make_float4(M, l, R, 0.f);
+    __syncthreads();
+    if (warp > 0) return;
+    float top = M;
+    for (int w = 1; w < WARPS; ++w) top = fmaxf(top, units[w].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    float unit = -INFINITY;
+    for (int w = 0; w < WARPS; ++w) unit = fmaxf(unit, units[w].z + (units[w].x - base));
+    const float base_r = unit == -INFINITY ? 0.f : unit;
+    l = 0.f;
+    r = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < WARPS; ++w) {
+      const float4 y = part[w][c4], v = units[w];
+      float f, g;
+      pow2_pair(v.x - base + v.z - base_r, f, g);
+      l = fmaf(fast_exp2(v.x - base), v.y, l);
+      r.x = fmaf(f, y.x * g, r.x); r.y = fmaf(f, y.y * g, r.y); r.z = fmaf(f, y.z * g, r.z); r.w = fmaf(f, y.w * g, r.w);
+    }
+    R = unit;
+  }
   if (lane < D / 4) store_out4(a.out + (static_cast<size_t>(b) * a.Hq + hq) * D + 4 * c4, r, l, R);
 }
 
 struct Plan {
+  bool list;                 // every member by itself: ns splits of pps pages
+  int ns, pps;
   int mt, parts, tm, items;  // of the prefix kernel; items 0: no prefix
   bool prefix_first;         // of the two kernels
   int chunks, blocks;        // of what is the members' own: rows of blocks, blocks of a row
@@ -512,9 +536,10 @@ bool make_plan(const oscar_dims_t* d, int batch, int max_seq_len, int max_prefix
     return false;
   if (max_seq_len > kMaxLen || max_seq_len > static_cast<long long>(d->max_pages_per_seq) * kPageSize) return false;
   if (d->num_kv_heads > 65535) return false;
-  const int H = d->num_kv_heads, gqa = d->num_q_heads / H;
-  // the prefixes: tiles of 256 rows, smaller ones where a group has fewer rows
-  // (of several groups one holds, as a rule, the sequences by themselves)
+  const int H = d->num_kv_heads, gqa = d->num_q_heads / H, sms = num_sms();
+  *p = Plan{};
+  // ---- prefixes once: tiles of 256 rows, smaller ones where a group has fewer rows (of several groups one holds, as a rule, the
+  // sequences by themselves)
   const long long rows = static_cast<long long>(members) * gqa, likely = groups > 1 ? groups - 1 : 1;
   const long long each = (rows + likely - 1) / likely;
   p->mt = each > 128 ? 2 : 1;
@@ -523,27 +548,22 @@ bool make_plan(const oscar_dims_t* d, int batch, int max_seq_len, int max_prefix
   const long long most_tiles = rows / p->tm + groups;  // of one KV head: ragged ones, one a group, beyond the even ones
   const long long blocks = (max_prefix / kPageSize + kBlkPages - 1) / kBlkPages;
   // SMs for what is the members' own (k) beside waves of prefix blocks on the others, or one after the other (k = 0), whichever
-  // should take least by these times (us): of a prefix block (128 tokens), of a CTA's start and end, of the bytes of the members'
-  // own tokens, of which half the bound is taken as likely.
-  const int sms = num_sms();
-  const double block_us = p->mt == 2 ? 1.7 : p->parts == 1 ? 1.15 : 0.95, start_us = p->mt == 2 ? 13 : 10, own_start_us = 8;
+  // should take least by these times (us): of a prefix block (128 tokens), of a CTA's start and end, of the merge with its launch,
+  // of the bytes of the members' own tokens, of which half the bound is taken as likely.
+  const double block_us = p->mt == 2 ? 2.0 : p->parts == 1 ? 1.3 : 0.95, start_us = p->mt == 2 ? 13 : 10, merge_us = 8;
   const double own_bytes = static_cast<double>(members) * H * max_own * d->head_dim;
-  auto own_us = [&](int n) { return own_start_us + own_bytes / fmin(n * 40e3, 5.7e6); };  // 40 KB a us and SM, 5.7 TB/s in all
-  const long long chunk = members < kChunk ? members : kChunk;
-  p->chunks = (members + kChunk - 1) / kChunk;
-  p->items = 0;
-  p->prefix_first = false;
+  auto own_us = [&](int n) { return 8 + own_bytes / fmin(n * 40e3, 5.7e6); };  // 40 KB a us and SM, 5.7 TB/s in all
   int own_sms = sms;
-  if (blocks > 0 && rows > 0 && groups > 0) {
+  double best = 0;
+  long long items = 0;
+  if (blocks > 0 && rows > 0 && groups > 0 && groups <= kTable) {
     const long long tiles = rows / p->tm > likely ? rows / p->tm : likely;
-    double best = 0;
-    long long items = 0;
     for (int k = 0; k < sms; k += 4) {
       for (int w = 1; w <= 4; ++w) {
         const long long n = static_cast<long long>(w) * (sms - k) / H;
         if (n < tiles) continue;
         const double prefix = w * (static_cast<double>((blocks + n / tiles - 1) / (n / tiles)) * block_us + start_us);
-        const double us = k == 0 ? prefix + own_us(sms) : fmax(prefix, own_us(k));
+        const double us = (k == 0 ? prefix + own_us(sms) : fmax(prefix, own_us(k))) + merge_us;
         if (items == 0 || us < best) {
           best = us;
           items = n;
@@ -551,27 +571,36 @@ bool make_plan(const oscar_dims_t* d, int batch, int max_seq_len, int max_prefix
         }
       }
     }
-    if (items < most_tiles) items = most_tiles;
+    if (items > 0 && items < most_tiles) items = most_tiles;  // (0: more tiles than four waves have blocks)
     if (items > 0x7fffffffLL) return false;
-    // every member by itself, where that should take no longer: small calls, and prefixes that hardly anyone shares
-    const double all_us = own_start_us + (own_bytes + 2.0 * members * H * max_prefix * d->head_dim) / 5.7e6;
-    if (best > 0 && all_us <= best) {
-      items = 0;
-      own_sms = sms;
-    }
+  }
+  // ---- or every member by itself, by the decode's times: 8 x 2048 12.8 us (19 over tiles), 16 x 2048 18.9 (20), 32 x 2048 33 (22)
+  const double list_us = 7 + (own_bytes + 2.0 * members * H * max_prefix * d->head_dim) / (d->head_dim == 128 ? 6.2e6 : 5e6);
+  p->list = items == 0 || list_us < best;
+  size_t own;  // rows of partials
+  if (p->list) {
+    const long long most = static_cast<long long>(max_prefix) + max_own;
+    const long long pages = ((most < max_seq_len ? most : max_seq_len) + kPageSize - 1) / kPageSize;
+    p->pps = split_pages(pages, (members > 0 ? members : 1LL) * H);
+    if (p->pps > kMaxPps) p->pps = kMaxPps;
+    const long long ns = pages > 0 ? (pages + p->pps - 1) / p->pps : 1;
+    if (ns > 65535 || ns * members * H > 0x7fffffffLL) return false;
+    p->ns = static_cast<int>(ns);
+    own = ns > 1 ? static_cast<size_t>(ns) * rows * H : 0;
+  } else {
     p->items = static_cast<int>(items);
     // what takes longer goes first, if it leaves room for the other
-    p->prefix_first = items > 0 && items * H <= sms - own_sms;
+    p->prefix_first = items * H <= sms - own_sms;
+    // blocks of a chunk, fewer where their warps would have nothing
+    p->chunks = (members + kChunk - 1) / kChunk;
+    const long long chunk = members < kChunk ? members : kChunk, pages = (static_cast<long long>(max_own) + kPageSize - 1) / kPageSize;
+    const long long use = (chunk * H * (pages + kUnitCost) + kOwnWarps * kLeastPages - 1) / (kOwnWarps * kLeastPages);
+    const long long most = own_sms / p->chunks < use ? own_sms / p->chunks : use;
+    p->blocks = static_cast<int>(most < 1 ? 1 : most);
+    const long long pieces = static_cast<long long>(p->chunks) * p->blocks * kOwnWarps + static_cast<long long>(members) * H;
+    if (pieces > 0x7fffffffLL) return false;
+    own = static_cast<size_t>(pieces) * gqa;
   }
-  // blocks of a chunk, fewer where their warps would have nothing
-  const long long own_most = static_cast<long long>(max_own) + (p->items == 0 ? max_prefix : 0), pages = (own_most + kPageSize - 1) / kPageSize;
-  const long long use = (chunk * H * (pages + kUnitCost) + kOwnWarps * kLeastPages - 1) / (kOwnWarps * kLeastPages);
-  long long most = p->chunks > 0 ? own_sms / p->chunks : 1;
-  if (most > use) most = use;
-  p->blocks = static_cast<int>(most < 1 ? 1 : most);
-  const long long pieces = static_cast<long long>(p->chunks) * p->blocks * kOwnWarps + static_cast<long long>(members) * H;
-  if (pieces > 0x7fffffffLL) return false;
-  const size_t own = static_cast<size_t>(pieces) * gqa;
   const size_t pre = static_cast<size_t>(p->items) * H * p->tm;
   p->off_ml = align_up(own * d->head_dim * sizeof(float), 256);
   p->off_pre_o = p->off_ml + align_up(own * 4 * sizeof(float), 256);
@@ -593,22 +622,33 @@ cudaError_t launch_prefix(const Plan& p, const SharedArgs& sh, cudaStream_t stre
 }
 
 template <int F, int D>
-cudaError_t launch(const Plan& p, const SharedArgs& sh, const OwnArgs& ow, const MergeArgs& me, const CUtensorMap& map,
-                   cudaStream_t stream) {
-  auto k = kv8_own_kernel<F, D>;
-  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(k), OwnGeo<D>::kSmem);
-  if (e != cudaSuccess) return e;
-  for (const bool prefix : {p.prefix_first, !p.prefix_first}) {
-    if (!prefix) e = launch_pdl(k, dim3(p.blocks, p.chunks), dim3(kOwnThreads), OwnGeo<D>::kSmem, stream, map, ow);
-    else if (p.items > 0)
-      e = p.mt == 2      ? launch_prefix<F, D, 2, 1>(p, sh, stream)
-          : p.parts == 2 ? launch_prefix<F, D, 1, 2>(p, sh, stream)
-                         : launch_prefix<F, D, 1, 1>(p, sh, stream);
+cudaError_t launch(const Plan& p, const ListArgs& li, const SharedArgs& sh, const OwnArgs& ow, const MergeArgs& me,
+                   const CUtensorMap& map, cudaStream_t stream) {
+  cudaError_t e;
+  if (p.list) {
+    auto k = kv8_list_kernel<F, D>;
+    e = set_smem_limit_once(reinterpret_cast<const void*>(k), DecodeGeo<D>::kSmem);
     if (e != cudaSuccess) return e;
+    e = launch_pdl(k, dim3(p.ns, me.a.H, me.num_members), dim3(kWarps * 32), DecodeGeo<D>::kSmem, stream, map, li);
+    if (e != cudaSuccess || p.ns == 1) return e;
+  } else {
+    auto k = kv8_own_kernel<F, D>;
+    e = set_smem_limit_once(reinterpret_cast<const void*>(k), OwnGeo<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    for (const bool prefix : {p.prefix_first, !p.prefix_first}) {
+      if (!prefix) e = launch_pdl(k, dim3(p.blocks, p.chunks), dim3(kOwnThreads), OwnGeo<D>::kSmem, stream, map, ow);
+      else if (p.mt == 2) e = launch_prefix<F, D, 2, 1>(p, sh, stream);
+      else if (p.parts == 2) e = launch_prefix<F, D, 1, 2>(p, sh, stream);
+      else e = launch_prefix<F, D, 1, 1>(p, sh, stream);
+      if (e != cudaSuccess) return e;
+    }
   }
   const long long rows = static_cast<long long>(me.num_members) * me.a.Hq;
-  return launch_pdl(kv8_shared_merge_kernel<D>, dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows)),
-                    dim3(kMergeRows * 32), 0, stream, me);
+  if (p.list && p.ns > 8)  // few rows of many partials
+    return launch_pdl(kv8_shared_merge_kernel<D, kMergeWarps>, dim3(static_cast<unsigned>(rows)), dim3(kMergeWarps * 32), 0, stream,
+                      me);
+  return launch_pdl(kv8_shared_merge_kernel<D, 1>, dim3(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps)),
+                    dim3(kMergeWarps * 32), 0, stream, me);
 }
 
 }  // namespace
@@ -628,9 +668,9 @@ extern "C" oscar_status_t oscar_kv8_decode_shared_plan(const oscar_dims_t* dims,
   if (st != OSCAR_OK) return st;
   Plan p;
   if (!make_plan(dims, batch, max_seq_len, max_prefix_len, max_own_len, num_members, num_groups, &p)) return OSCAR_ERR_INVALID_ARG;
-  if (tile_rows) *tile_rows = p.items > 0 ? p.tm : 0;
+  if (tile_rows) *tile_rows = p.list ? 0 : p.tm;
   if (prefix_blocks) *prefix_blocks = p.items * dims->num_kv_heads;
-  if (own_blocks) *own_blocks = p.blocks * p.chunks;
+  if (own_blocks) *own_blocks = p.list ? p.ns * dims->num_kv_heads * num_members : p.blocks * p.chunks;
   return OSCAR_OK;
 }
 
@@ -663,15 +703,19 @@ extern "C" oscar_status_t oscar_kv8_decode_shared(const oscar_dims_t* dims, int3
   const Groups g{members, group_start, prefix_lens, num_members, num_groups, max_prefix_len};
   int4* info = reinterpret_cast<int4*>(w + plan.off_info);
   int2* own = reinterpret_cast<int2*>(w + plan.off_own);
+  const ListArgs li{{a, floats(0), floats(plan.off_ml), plan.ns, plan.pps}, g, info, own, max_own_len};
   const SharedArgs sh{{a, floats(plan.off_pre_o), floats(plan.off_pre_ml), 0, 0, 0}, g, info, plan.prefix_first, !plan.prefix_first};
-  const OwnArgs ow{a, g, info, own, floats(0), floats(plan.off_ml), max_own_len, !plan.prefix_first, plan.prefix_first && plan.items > 0, plan.items == 0 && max_prefix_len >= kPageSize};
+  const OwnArgs ow{a, g, info, own, floats(0), floats(plan.off_ml), max_own_len, !plan.prefix_first, plan.prefix_first};
   const MergeArgs me{a, members, info, own, floats(0), floats(plan.off_ml), floats(plan.off_pre_o), floats(plan.off_pre_ml),
                      num_members, plan.tm};
   cudaStream_t s = as_stream(stream);
   const bool d128 = dims->head_dim == 128;
-  const cudaError_t e = kv_format == OSCAR_KV8_E4M3
-                            ? (d128 ? launch<kE4M3, 128>(plan, sh, ow, me, map, s) : launch<kE4M3, 64>(plan, sh, ow, me, map, s))
-                            : (d128 ? launch<kInt8, 128>(plan, sh, ow, me, map, s) : launch<kInt8, 64>(plan, sh, ow, me, map, s));
+  auto go = [&](auto f) {
+    constexpr int F = decltype(f)::value;
+    return d128 ? launch<F, 128>(plan, li, sh, ow, me, map, s) : launch<F, 64>(plan, li, sh, ow, me, map, s);
+  };
+  const cudaError_t e = kv_format == OSCAR_KV8_E4M3 ? go(std::integral_constant<int, kE4M3>{})
+                                                    : go(std::integral_constant<int, kInt8>{});
   return e == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 

@@ -153,10 +153,13 @@ def test_more_groups_than_a_warp_has_lanes_over_tiles():
     c.check(c.run())
 
 
-def test_more_groups_than_the_table_of_their_tiles_and_members_than_a_chunk():
-    # 2048 groups' tiles are kept in shared memory, and 384 members' pages are dealt out together
-    c = Case(4, 1, 64, R.INT8, [(32, [3])] * 2100 + [(6400, list(range(60)) * 10), (48, [1, 2])], seed=14)
+def test_more_groups_than_tiles_may_be_and_more_members_than_a_chunk():
+    # 384 members' pages are dealt out together
+    c = Case(4, 1, 64, R.INT8, [(6400, list(range(60)) * 10), (48, [1, 2])] + [(32, [3])] * 5, seed=14)
     assert c.tile_rows() > 0
+    c.check(c.run())
+    c = Case(4, 1, 64, R.INT8, [(32, [3])] * 1100 + [(6400, list(range(60))), (48, [1, 2])], seed=14)
+    assert c.tile_rows() == 0
     c.check(c.run())
 
 
@@ -170,8 +173,12 @@ def test_heads_fewer_and_more_than_fit_a_wave(heads):
 
 
 def test_long_prefix_over_many_splits_and_own_parts_in_splits():
-    c = Case(8, 1, 128, R.E4M3, [(20000 // 16 * 16, [9000, 1, 16, 0, 333])], seed=3)
-    c.check(c.run())
+    for hq, D in ((8, 128), (3, 64)):  # few rows of many partials, and one of few
+        c = Case(hq, 1, D, R.E4M3, [(20000 // 16 * 16, [9000, 1, 16, 0, 333])], seed=3)
+        c.check(c.run())
+        c = Case(hq, 1, D, R.INT8, [(20000 // 16 * 16, [0])], seed=4)
+        assert c.tile_rows() == 0
+        c.check(c.run())
 
 
 def test_bounds_below_the_prefixes_leave_the_rest_to_the_members():
@@ -249,7 +256,7 @@ def test_bad_numbers_are_flagged_and_nothing_else_is_touched(groups):
     c.t_table[m[0], 3] = c.dims.num_pages
     c.t_table[m[-2], 16:] = -1
     c.table = c.t_table.cpu().numpy()
-    for b in m[1:n]:  # the prefix is read through the first member's pages
+    for b in m[1:n] if groups is LARGE else ():  # over tiles the prefix is read through the first member's pages
         c.table[b, 3] = -1
     out = c.run()
     assert ok.oscar_device_errors(reset=True) == ok.OSCAR_DEVERR_PAGE_ID
