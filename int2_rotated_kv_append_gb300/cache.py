@@ -26,10 +26,20 @@ from . import (OSCAR_KV8_E4M3, make_dims, oscar_append, oscar_append_mixed, osca
                oscar_kv8_decode_shared_workspace_bytes, oscar_kv8_decode_workspace_bytes, oscar_kv8_extend_varlen,
                oscar_kv8_extend_varlen_workspace_bytes, oscar_kv8_rope_append, oscar_pages_compact, oscar_pages_fork,
                oscar_pages_free, oscar_pages_groups, oscar_pages_groups_workspace_bytes, oscar_pages_reserve,
-               oscar_pages_trim, oscar_pages_workspace_bytes, _stream)
+               oscar_pages_trim, oscar_pages_workspace_bytes, oscar_rope, _stream)
 from .synth import Workload
 
 SENTINEL = 0xA5
+
+
+def _allocating(device, stream):
+    """The context in which what a call on ``stream`` uses is allocated."""
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 class Int2Cache:
@@ -54,7 +64,13 @@ class Int2Cache:
         self.window = None
         self._ws = None
 
-    def append(self, k, v, slot_mapping, stream=None):
+    def append(self, k, v, slot_mapping, stream=None, rope=None, positions=None):
+        """With ``rope`` (a ``Rope``) the keys come without positions and are rotated by ``positions`` (int32 device [T])
+        first; k may then be a slice of longer rows."""
+        if rope is not None:
+            with _allocating(self.device, stream):
+                plain, k = k, torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            oscar_rope(self.dims, rope, positions, None, plain, None, k, stream)
         oscar_append(self.dims, k, v, self.R_k, self.R_v, self.clip_k, self.clip_v, self.page_table, slot_mapping,
                      self.int2_pages, self.scale_zero, stream, offset_k=self.offset_k)
 
@@ -206,14 +222,7 @@ class Kv8Cache:
         self._ws = {}  # by stream: the last one is used, smaller ones stay for captured graphs that point to them
 
     def _allocating(self, stream):
-        """The context in which what a call on ``stream`` uses is allocated."""
-        if stream is None or self.device.type != "cuda":
-            return contextlib.nullcontext()
-        if not isinstance(stream, torch.cuda.Stream):
-            handle = int(stream)
-            stream = (torch.cuda.ExternalStream(handle, device=self.device) if handle
-                      else torch.cuda.default_stream(self.device))
-        return torch.cuda.stream(stream)
+        return _allocating(self.device, stream)
 
     def _workspace(self, nbytes, stream):
         if nbytes == 0:

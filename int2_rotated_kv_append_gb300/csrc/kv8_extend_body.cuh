@@ -440,7 +440,10 @@ __device__ __forceinline__ void extend_body(const Args& args) {
     }
     __syncwarp();
     const bool there = mbar_wait_bounded(bar(kQRaw), 0);
-    if (!there) record_error(OSCAR_DEVERR_TIMEOUT);
+    if (!there) {
+      record_error(OSCAR_DEVERR_TIMEOUT);
+      mbar_wait_bounded(bar(kQRaw), 0);  // (copies still in flight)
+    }
     const int c = lane % kLanes;
 #pragma unroll 4
     for (int k = 0; k < kRounds; ++k) {

@@ -280,8 +280,7 @@ extern "C" oscar_status_t oscar_kv8_rope_append(
     return OSCAR_ERR_INVALID_ARG;
   if (q && (misaligned16(q) || misaligned16(q_out) || bad_stride(q_stride, Hq, D, 2) || bad_stride(q_out_stride, Hq, D, 2)))
     return OSCAR_ERR_INVALID_ARG;
-  if (batch > 65535 || static_cast<long long>(dims->max_pages_per_seq) * kPageSize > 0x7fffffffLL || Hq > 0x7ffffff)
-    return OSCAR_ERR_UNSUPPORTED;
+  if (batch > 65535 || static_cast<long long>(dims->max_pages_per_seq) * kPageSize > 0x7fffffffLL) return OSCAR_ERR_UNSUPPORTED;
   const long long most = max_tokens_per_seq < num_tokens ? max_tokens_per_seq : num_tokens;  // of one sequence
   const long long gx = (most + 2 * kPageSize - 2) / kPageSize;
   // Pages that get tokens, about; where they are few, their heads are dealt out to several blocks.

@@ -25,6 +25,7 @@ static inline oscar_status_t check_rope(const oscar_rope_t* r, const oscar_dims_
   if (r->rotary_dim <= 0 || r->rotary_dim > d->head_dim || (r->interleaved != 0 && r->interleaved != 1) ||
       !isfinite(r->magnitude))
     return OSCAR_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(d->num_q_heads) * d->head_dim > 0x7fffffffLL) return OSCAR_ERR_UNSUPPORTED;  // (a row's channels)
   return r->rotary_dim % 16 != 0 ? OSCAR_ERR_UNSUPPORTED : OSCAR_OK;
 }
 

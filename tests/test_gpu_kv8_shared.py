@@ -234,6 +234,13 @@ def test_some_of_the_sequences_in_any_order(groups):
 
 
 @pytest.mark.parametrize("groups", [SMALL, LARGE], ids=["small", "tiles"])
+def test_a_sequence_named_twice(groups):
+    c = Case(4, 2, 128, R.INT8, groups, seed=15)
+    m, n = c.members, len(groups[0][1])
+    c.check(c.run(lists=([m[0]] + m[:n] + [m[1]] + m[n:], [0, n + 2, len(m) + 2], c.prefix)))
+
+
+@pytest.mark.parametrize("groups", [SMALL, LARGE], ids=["small", "tiles"])
 def test_bad_numbers_are_flagged_and_nothing_else_is_touched(groups):
     c = Case(4, 2, 128, R.INT8, groups, seed=10)
     m, P, n, t, p = c.members, ok.OSCAR_DEVERR_POSITION, len(groups[0][1]), len(c.members), groups[0][0]

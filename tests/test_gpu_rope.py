@@ -309,3 +309,50 @@ def test_append_on_a_stream_of_its_own_and_captured():
         ok.oscar_kv8_rope_append(d, rope, R.E4M3, 2, 2, q, k, v, start, None, table, lens, *want, q2, stream=s)
         torch.cuda.synchronize()
     assert torch.equal(codes, want[0]) and torch.equal(scales, want[1]) and torch.equal(out, q2)
+
+
+def test_append_and_decode_in_pages_beyond_4_gb():
+    H, D, n = 8, 128, 140000  # pages of 32 KB
+    rope = ok.Rope(128)
+    codes, scales = torch.empty(n, H, 2, 16, D, device="cuda", dtype=torch.uint8), torch.empty(n, H, 2, device="cuda")
+    far = [n - 1, n - 3, 131072]
+    small = [torch.zeros(3, H, 2, 16, D, device="cuda", dtype=torch.uint8), torch.zeros(3, H, 2, device="cuda")]
+    x = torch.randn(40, 16 + 2 * H, D, device="cuda").bfloat16()
+    q, k, v = torch.split(x, [16, H, H], 1)
+    outs = []
+    for pool, ids, pages in (((codes, scales), far, n), (small, [0, 1, 2], 3)):
+        d = dims(16, H, D, pages, 3)
+        qo = torch.empty(40, 16, D, device="cuda", dtype=torch.bfloat16)
+        ok.oscar_kv8_rope_append(d, rope, R.INT8, 1, 40, q, k, v, i32([0, 40]), None, i32([ids]), i32([40]), *pool, qo)
+        out = torch.empty(1, 16, D, device="cuda", dtype=torch.bfloat16)
+        w = torch.empty(ok.oscar_kv8_decode_shared_workspace_bytes(d, 1, 48, 0, 48, 1, 1), dtype=torch.uint8, device="cuda")
+        ok.oscar_kv8_decode_shared(d, R.INT8, 1, 48, 0, 48, qo[-1:], *pool, i32([ids]), i32([40]), i32([0]), i32([0, 1]), i32([0]), 0.0,
+                                   out, w)
+        outs += [pool[0][ids, :, :, :8].clone(), pool[1][ids].clone(), out]
+    for a, b in zip(outs[:3], outs[3:]):
+        assert torch.equal(a, b)
+    assert ok.oscar_device_errors(reset=True) == 0
+
+
+def test_int2_cache_takes_keys_without_positions():
+    from int2_rotated_kv_append_gb300 import synth
+    from int2_rotated_kv_append_gb300.cache import Int2Cache
+    w = synth.make_workload(num_q_heads=8, num_kv_heads=2, head_dim=128, group_size=64, sink_len=16, window_len=64, seq_lens=[700], seed=3)
+    rope = ok.Rope(64, interleaved=True)
+    rows = torch.cat([w.k, w.v], 1).cuda()
+    k, v = rows[:, :2], w.v.cuda()
+    pos = w.tok_pos.cuda()
+    a, b = Int2Cache(w), Int2Cache(w)
+    a.append(k, v, w.slot_mapping.cuda(), rope=rope, positions=pos)
+    turned = torch.empty(k.shape, dtype=k.dtype, device="cuda")
+    ok.oscar_rope(w.dims, rope, pos, None, k, None, turned)
+    check(turned, k, w.tok_pos.numpy(), rope)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    b.append(turned, v, w.slot_mapping.cuda(), stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(a.int2_pages, b.int2_pages) and torch.equal(a.scale_zero.view(torch.int16), b.scale_zero.view(torch.int16))
+    assert torch.equal(rows[:, :2], w.k.cuda())
+    b.append(k, v, w.slot_mapping.cuda(), stream=s, rope=rope, positions=pos)
+    torch.cuda.synchronize()
+    assert torch.equal(a.int2_pages, b.int2_pages)
