@@ -68,6 +68,8 @@ class Int2Cache:
         """With ``rope`` (a ``Rope``) the keys come without positions and are rotated by ``positions`` (int32 device [T])
         first; k may then be a slice of longer rows."""
         if rope is not None:
+            if positions is None:
+                raise ValueError("keys that are to be rotated have positions")
             with _allocating(self.device, stream):
                 plain, k = k, torch.empty(k.shape, dtype=k.dtype, device=k.device)
             oscar_rope(self.dims, rope, positions, None, plain, None, k, stream)

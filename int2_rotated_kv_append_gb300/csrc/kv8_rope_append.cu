@@ -278,7 +278,8 @@ extern "C" oscar_status_t oscar_kv8_rope_append(
   if (misaligned16(k) || misaligned16(v) || misaligned16(kv8_pages) || misaligned16(kv8_scales) || bad_stride(k_stride, H, D, 2) ||
       bad_stride(v_stride, H, D, 2))
     return OSCAR_ERR_INVALID_ARG;
-  if (q && (misaligned16(q) || misaligned16(q_out) || bad_stride(q_stride, Hq, D, 2) || bad_stride(q_out_stride, Hq, D, 2)))
+  if (q && (misaligned16(q) || misaligned16(q_out) || bad_stride(q_stride, Hq, D, 2) || bad_stride(q_out_stride, Hq, D, 2) ||
+            bad_in_place(q, q_stride, q_out, q_out_stride, num_tokens)))
     return OSCAR_ERR_INVALID_ARG;
   if (batch > 65535 || static_cast<long long>(dims->max_pages_per_seq) * kPageSize > 0x7fffffffLL) return OSCAR_ERR_UNSUPPORTED;
   const long long most = max_tokens_per_seq < num_tokens ? max_tokens_per_seq : num_tokens;  // of one sequence

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) kv8_own_kernel(const __grid_co
     total += sums[w];
   }
   const long long warps = static_cast<long long>(gridDim.x) * kOwnWarps, all = total * a.H;
-  const int each = static_cast<int>(max((all + warps - 1) / warps, static_cast<long long>(kLeastPages)));
+  const long long each = max((all + warps - 1) / warps, static_cast<long long>(kLeastPages));
   begins[tid] = up;
   if (tid < mc && tid % gridDim.x == blockIdx.x)
     for (int h = 0; h < a.H; ++h) {

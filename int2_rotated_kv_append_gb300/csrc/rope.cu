@@ -169,7 +169,8 @@ extern "C" oscar_status_t oscar_rope(const oscar_dims_t* dims, const oscar_rope_
                    num_tokens};
   for (const Rows* r : {&a.q, &a.k}) {
     if (r->heads > 0 && (misaligned16(r->in) || misaligned16(r->out) || bad_stride(r->in_stride, r->heads, dims->head_dim, elem) ||
-                         bad_stride(r->out_stride, r->heads, dims->head_dim, elem)))
+                         bad_stride(r->out_stride, r->heads, dims->head_dim, elem) ||
+                         bad_in_place(r->in, r->in_stride, r->out, r->out_stride, num_tokens)))
       return OSCAR_ERR_INVALID_ARG;
   }
   const bool il = rope->interleaved != 0;

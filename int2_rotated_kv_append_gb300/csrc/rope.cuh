@@ -34,6 +34,11 @@ static inline bool bad_stride(int64_t stride, int heads, int dim, int elem) {
   return stride < static_cast<int64_t>(heads) * dim || stride * elem % 16 != 0;
 }
 
+// Rows that go over rows still to be read.
+static inline bool bad_in_place(const void* in, int64_t in_stride, const void* out, int64_t out_stride, int64_t rows) {
+  return in == out && in_stride != out_stride && rows > 1;
+}
+
 // (cos, sin) of pos * frequency, times magnitude.
 __device__ __forceinline__ float2 cos_sin(uint64_t turns, int pos, float magnitude) {
   const uint32_t top = static_cast<uint32_t>((turns * static_cast<uint64_t>(static_cast<int64_t>(pos))) >> 32);

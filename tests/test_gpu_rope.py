@@ -356,3 +356,5 @@ def test_int2_cache_takes_keys_without_positions():
     b.append(k, v, w.slot_mapping.cuda(), stream=s, rope=rope, positions=pos)
     torch.cuda.synchronize()
     assert torch.equal(a.int2_pages, b.int2_pages)
+    with pytest.raises(ValueError):
+        a.append(k, v, w.slot_mapping.cuda(), rope=rope)

@@ -158,6 +158,12 @@ def test_rope_refusals(lib):
         assert call(type=2, **{n: row + 2}) == BAD
 
 
+def test_rows_that_go_over_rows_still_to_be_read_are_refused(lib):
+    for qs, qos, ks, kos in ((2048, 1024, 256, 256), (1024, 1024, 256, 512)):
+        assert lib.oscar_rope(dims(), rope(), 0, 2, P, P, qs, 1 << 24, ks, P, qos, 1 << 24, kos, None) == BAD
+    assert lib.oscar_kv8_rope_append(dims(), rope(), 0, 1, 2, 2, P, 2048, P, 256, P, 256, P, None, P, P, None, P, P, P, 1024, None) == BAD
+
+
 def test_append_refusals(lib):
     def call(d=None, r=None, fmt=0, batch=2, tokens=4, most=3, **kw):
         a = {n: P for n in "q k v start table lens pages scales qo".split()}
