@@ -3,10 +3,11 @@
 //
 // A block has one page of one sequence (or a share of its heads, where there are few pages).  Its angles' cosines and sines
 // are computed once into shared memory, for all heads; then every warp takes items: a (head, K | V) block of the page,
-// rotated in fp32 (K), its largest magnitude by a warp butterfly, codes from the registers; or 16 rows of queries.  The
-// rotated key is not rounded before it becomes a code.  Bound by the bytes: 2 (Hq + 2 Hkv) in, 2 Hq + 2 Hkv out per channel:
-// six prompts, 56 thousand tokens, 32 query and 8 KV heads, D = 128, 1.11 GB: 187 us, 5.9 TB/s, 88% of a plain copy of as many
-// bytes (of 16 warps an SM; 20, with spills, take 207).  One token of each of 64 sequences: 3.6 us.
+// rotated in fp32 (K), its largest magnitude by a warp butterfly, then its codes; or 16 rows of queries.  The next item's rows
+// are on their way into shared memory meanwhile, the first one's beside the cosines.  The rotated key is not rounded before it
+// becomes a code.  Bound by the bytes: 2 (Hq + 2 Hkv) in, 2 Hq + 2 Hkv out per channel: six prompts, 56 thousand tokens, 32 query
+// and 8 KV heads, D = 128, 1.11 GB: 169 us, 6.6 TB/s, 98% of a plain copy of as many bytes (187 with each item's rows loaded into
+// registers; as long with 20 warps an SM as with 16).  One token of each of 64 sequences: 3.6 us.
 #include <type_traits>
 
 #include "kv8.cuh"
@@ -57,6 +58,11 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint4* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
 // The larger, or NaN where either is one.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -73,6 +79,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_rope_append_kernel(AppendArgs
   // puts in different banks
   constexpr int kRowPad = D / 2 + (D == 128 ? 8 : 4);
   __shared__ float2 table[kPageSize][kRowPad];
+  __shared__ uint4 stages[kWarps][2][2 * kIters][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.z;
   const int t0 = __ldg(a.t_start + b), t1 = __ldg(a.t_start + b + 1), L = __ldg(a.seq_lens + b);
@@ -96,6 +103,55 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_rope_append_kernel(AppendArgs
   if (j > (L - 1) / kPageSize) return;
   const int o0 = max(p_first - j * kPageSize, 0), o1 = min(L - j * kPageSize, kPageSize);  // new rows of the page
   const long long tok0 = static_cast<long long>(t0) + (j * kPageSize - p_first);  // token of the page's row 0
+  const int unit = lane % kUnits, row0 = lane / kUnits;
+  const bool turned = unit * 16 < a.rope.rotary;
+  const int c0 = first_channel<8, IL>(unit, a.rope.rotary), c1 = second_channel<8, IL>(unit, a.rope.rotary);
+  const int items_q = a.q != nullptr ? (a.Hq * (o1 - o0) + kPageSize - 1) / kPageSize : 0, items = items_kv + items_q;
+  // A lane's pairs of (row, query head), of 16 of the page's, are kRows apart.
+  auto first_pair = [&](int item, int& r, int& hd) {
+    const int y = (item - items_kv) * kPageSize + row0;
+    r = y / a.Hq;
+    hd = y - r * a.Hq;
+    r += o0;
+  };
+  auto next_pair = [&](int& r, int& hd) {
+    r += kRows / a.Hq;
+    hd += kRows % a.Hq;
+    if (hd >= a.Hq) {
+      hd -= a.Hq;
+      ++r;
+    }
+  };
+  // A lane's vectors of an item, on their way to memory that it alone reads, while it works on the item before.
+  auto fetch = [&](int item, int buf) {
+    uint4* to = &stages[warp][buf][0][lane];
+    if (item >= items) {
+    } else if (item >= items_kv) {
+      int r, hd;
+      first_pair(item, r, hd);
+#pragma unroll
+      for (int i = 0; i < kIters; ++i) {
+        const __nv_bfloat16* src = a.q + (tok0 + min(r, o1 - 1)) * a.q_stride + hd * D;
+        copy16(to + 64 * i, src + c0, r < o1);
+        copy16(to + 64 * i + 32, src + c1, r < o1);
+        next_pair(r, hd);
+      }
+    } else {
+      const __nv_bfloat16* src = (item & 1 ? a.v : a.k) + static_cast<size_t>(item >> 1) * D;
+      const long long stride = item & 1 ? a.v_stride : a.k_stride;
+#pragma unroll
+      for (int i = 0; i < kIters; ++i) {
+        const int r = i * kRows + row0;
+        const bool is_new = r >= o0 && r < o1;
+        const __nv_bfloat16* row = src + (tok0 + (is_new ? r : o0)) * stride;
+        copy16(to + 64 * i, row + c0, is_new);
+        copy16(to + 64 * i + 32, row + c1, is_new);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const int item0 = blockIdx.y * kWarps + warp, step = gridDim.y * kWarps;
+  fetch(item0, 0);
   int pid = __ldg(a.page_table + static_cast<size_t>(b) * a.max_pages + j);
   if (pid < 0 || pid >= a.num_pages) {  // (the queries go on)
     if (tid == 0 && blockIdx.y == 0) record_error(OSCAR_DEVERR_PAGE_ID);
@@ -108,86 +164,54 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_rope_append_kernel(AppendArgs
     table[r][(p & 7) * kUnits + (p >> 3)] = cos_sin(__ldg(a.rope.turns + p), pos, a.rope.magnitude);
   }
   __syncthreads();
-  const int unit = lane % kUnits, row0 = lane / kUnits;
-  const bool turned = unit * 16 < a.rope.rotary;
-  const int c0 = first_channel<8, IL>(unit, a.rope.rotary), c1 = second_channel<8, IL>(unit, a.rope.rotary);
-  const int new_rows = o1 - o0;
-  const int items_q = a.q != nullptr ? (a.Hq * new_rows + kPageSize - 1) / kPageSize : 0;
-  for (int item = blockIdx.y * kWarps + warp; item < items_kv + items_q; item += gridDim.y * kWarps) {
-    if (item >= items_kv) {  // 16 of the page's (row, query head) pairs
-      uint4 x[kIters][2];
-      const int y0 = (item - items_kv) * kPageSize + row0, first = y0 / a.Hq, first_head = y0 - first * a.Hq;
-      // (a lane's pairs are kRows apart)
-      auto next = [&](int& r, int& hd) {
-        r += kRows / a.Hq;
-        hd += kRows % a.Hq;
-        if (hd >= a.Hq) {
-          hd -= a.Hq;
-          ++r;
-        }
-      };
-      int r = o0 + first, hd = first_head;
+  int buf = 0;
+  for (int item = item0; item < items; item += step, buf ^= 1) {
+    fetch(item + step, buf ^ 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const uint4* in = &stages[warp][buf][0][lane];
+    if (item >= items_kv) {
+      int r, hd;
+      first_pair(item, r, hd);
 #pragma unroll
       for (int i = 0; i < kIters; ++i) {
         if (r < o1) {
-          const __nv_bfloat16* src = a.q + (tok0 + r) * a.q_stride + hd * D;
-          x[i][0] = *reinterpret_cast<const uint4*>(src + c0);
-          x[i][1] = *reinterpret_cast<const uint4*>(src + c1);
-        }
-        next(r, hd);
-      }
-      r = o0 + first;
-      hd = first_head;
-#pragma unroll
-      for (int i = 0; i < kIters; ++i) {
-        if (r < o1) {
+          uint4 v0 = in[64 * i], v1 = in[64 * i + 32];
           if (turned) {
             float y[16];
-            unpack8(x[i][0], y);
-            unpack8(x[i][1], y + 8);
+            unpack8(v0, y);
+            unpack8(v1, y + 8);
             turn_unit<8, IL>(y, [&](int p) { return table[r][p * kUnits + unit]; });
-            x[i][0] = pack8(y);
-            x[i][1] = pack8(y + 8);
+            v0 = pack8(y);
+            v1 = pack8(y + 8);
           }
           __nv_bfloat16* dst = a.q_out + (tok0 + r) * a.q_out_stride + hd * D;
-          *reinterpret_cast<uint4*>(dst + c0) = x[i][0];
-          *reinterpret_cast<uint4*>(dst + c1) = x[i][1];
+          *reinterpret_cast<uint4*>(dst + c0) = v0;
+          *reinterpret_cast<uint4*>(dst + c1) = v1;
         }
-        next(r, hd);
+        next_pair(r, hd);
       }
       continue;
     }
     if (pid < 0) continue;
     const int h = item >> 1, side = item & 1;
-    const __nv_bfloat16* src = side ? a.v + static_cast<size_t>(h) * D : a.k + static_cast<size_t>(h) * D;
-    const long long stride = side ? a.v_stride : a.k_stride;
     const size_t block = (static_cast<size_t>(pid) * a.H + h) * 2 + side;
     uint8_t* dst = a.pages + block * (kPageSize * D);
-    uint4 w[kIters][2];
-#pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-      const int r = i * kRows + row0;
-      w[i][0] = w[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (r >= o0 && r < o1) {
-        w[i][0] = __ldg(reinterpret_cast<const uint4*>(src + (tok0 + r) * stride + c0));
-        w[i][1] = __ldg(reinterpret_cast<const uint4*>(src + (tok0 + r) * stride + c1));
-      }
-    }
     const float stored = o0 > 0 ? a.scales[block] : 0.f;
     // Rows of a lane, rotated (K).  They are formed twice, for the largest magnitude and for the codes: 64 values kept would take
-    // the registers of half the warps that an SM holds (six prompts: 285 us, not 187).
+    // the registers of half the warps that an SM holds.
     const bool turns = side == 0 && turned;
-    auto values = [&](int r, uint4 v0, uint4 v1, float (&x)[16]) {
+    auto values = [&](int i, float (&x)[16]) {
       asm volatile("" ::: "memory");  // (a row at a time)
-      unpack8(v0, x);
-      unpack8(v1, x + 8);
+      const int r = i * kRows + row0;
+      unpack8(in[64 * i], x);
+      unpack8(in[64 * i + 32], x + 8);
       if (turns && r >= o0 && r < o1) turn_unit<8, IL>(x, [&](int p) { return table[r][p * kUnits + unit]; });
     };
     float top = 0.f;  // (a NaN stays one)
 #pragma unroll
     for (int i = 0; i < kIters; ++i) {
       float x[16];
-      values(i * kRows + row0, w[i][0], w[i][1], x);
+      values(i, x);
 #pragma unroll
       for (int c = 0; c < 16; ++c) top = max_nan(top, fabsf(x[c]));
     }
@@ -198,11 +222,9 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_rope_append_kernel(AppendArgs
       if (lane == 0) record_error(OSCAR_DEVERR_VALUE);
       top = 0.f;
 #pragma unroll 1
-      for (int r = row0; r < o1; r += kRows) {
-        if (r < o0) continue;
+      for (int i = 0; i < kIters; ++i) {
         float x[16];
-        values(r, *reinterpret_cast<const uint4*>(src + (tok0 + r) * stride + c0),
-               *reinterpret_cast<const uint4*>(src + (tok0 + r) * stride + c1), x);
+        values(i, x);
 #pragma unroll
         for (int c = 0; c < 16; ++c) top = fmaxf(top, fabsf(x[c]));  // (of a number and a NaN: the number)
       }
@@ -212,12 +234,6 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_rope_append_kernel(AppendArgs
     const float need = pow2i(scale_exponent<F>(__uint_as_float(mx)));
     const float scale = fmaxf(stored, need);
     const float inv = 1.f / scale;  // exact: a power of two between 2^-121 and 2^100
-    // (the compiler is to form the values again, not to keep them)
-#pragma unroll
-    for (int i = 0; i < kIters; ++i)
-#pragma unroll
-      for (int v = 0; v < 2; ++v)
-        asm volatile("" : "+r"(w[i][v].x), "+r"(w[i][v].y), "+r"(w[i][v].z), "+r"(w[i][v].w)::"memory");
 #pragma unroll
     for (int i = 0; i < kIters; ++i) {
       const int r = i * kRows + row0;
@@ -225,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_rope_append_kernel(AppendArgs
       uint2* at1 = reinterpret_cast<uint2*>(dst + r * D + c1);
       if (r >= o0 && r < o1) {
         float x[16];
-        values(r, w[i][0], w[i][1], x);
+        values(i, x);
         uint32_t o[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
