@@ -3,7 +3,7 @@
 // A thread has one unit (16 channels of bf16) of one token and goes over the heads, so that the angles' cosines and sines
 // are read once: a block computes them for its tokens, one each a thread, into shared memory.  A warp's loads are whole
 // rows of neighbouring heads.  Bound by the bytes, each element once in and once out: 16384 tokens of 40 heads, D = 128, bf16, 336 MB:
-// 58 us, 5.8 TB/s, 93% of a plain copy of as many bytes; 64 tokens 2.6 us.
+// 54.3 us, 6.2 TB/s, as long as a plain copy of as many bytes; 64 tokens 2.3 us.
 #include "rope.cuh"
 
 namespace {
@@ -83,57 +83,66 @@ struct Vec<float> {
   }
 };
 
-// TOK tokens of a block; blockIdx.y: every gridDim.y-th share of the heads.
+// TOK tokens of a block.  A thread has one head's row in flight, at five blocks an SM: 16384 tokens take 54.3 us, 57.5 at four, 55.5 with
+// two rows at four, 58 with the first rows loaded behind the cosines.
 template <typename T, int D, bool IL, int TOK>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, TOK == 1 ? 4 : 5) rope_kernel(RopeArgs a) {
   constexpr int E = Vec<T>::E, kUnits = D / (2 * E);
   constexpr int kGroups = kThreads / (TOK * kUnits);  // heads of a token at once
   __shared__ float2 table[TOK][D / 2];
   const long long t0 = static_cast<long long>(blockIdx.x) * TOK;
   const int half = a.rope.rotary / 2;
-  for (int i = threadIdx.x; i < TOK * half; i += kThreads) {
-    const int t = i / half, p = i - t * half;
-    if (t0 + t < a.tokens) table[t][p] = cos_sin(__ldg(a.rope.turns + p), __ldg(a.positions + t0 + t), a.rope.magnitude);
-  }
-  __syncthreads();
   const int unit = threadIdx.x % kUnits, tok = threadIdx.x / (kUnits * kGroups);
   const long long t = t0 + tok;
-  if (t >= a.tokens) return;
   const bool turned = unit * 2 * E < a.rope.rotary;
   const int c0 = first_channel<E, IL>(unit, a.rope.rotary), c1 = second_channel<E, IL>(unit, a.rope.rotary);
+  const int all = a.q.heads + a.k.heads;
+  // (channels that pass through, in place, are left alone)
+  const bool idle = !turned && a.q.in == a.q.out && a.k.in == a.k.out;
+  int h = t < a.tokens && !idle ? threadIdx.x / kUnits % kGroups : all;
+  uint4 v0, v1;
+  auto load = [&]() {
+    if (h >= all) return;
+    const T* src = h >= a.q.heads ? static_cast<const T*>(a.k.in) + t * a.k.in_stride + (h - a.q.heads) * D
+                                  : static_cast<const T*>(a.q.in) + t * a.q.in_stride + h * D;
+    v0 = *reinterpret_cast<const uint4*>(src + c0);
+    v1 = *reinterpret_cast<const uint4*>(src + c1);
+  };
+  load();  // the first head's row, beside the cosines
+  for (int i = threadIdx.x; i < TOK * half; i += kThreads) {
+    const int s = i / half, p = i - s * half;
+    if (t0 + s < a.tokens) table[s][p] = cos_sin(__ldg(a.rope.turns + p), __ldg(a.positions + t0 + s), a.rope.magnitude);
+  }
+  __syncthreads();
   float2 cs[E];
   if (turned) {
 #pragma unroll
     for (int j = 0; j < E; ++j) cs[j] = table[tok][unit * E + j];
   }
-  const int all = a.q.heads + a.k.heads;
-#pragma unroll 4
-  for (int h = blockIdx.y * kGroups + threadIdx.x / kUnits % kGroups; h < all; h += gridDim.y * kGroups) {
-    const bool key = h >= a.q.heads;
-    const int head = key ? h - a.q.heads : h;
-    const T* src = static_cast<const T*>(key ? a.k.in : a.q.in) + t * (key ? a.k.in_stride : a.q.in_stride) + head * D;
-    T* dst = static_cast<T*>(key ? a.k.out : a.q.out) + t * (key ? a.k.out_stride : a.q.out_stride) + head * D;
-    if (!turned && src == dst) continue;
-    float x[2 * E];
-    const uint4 v0 = *reinterpret_cast<const uint4*>(src + c0), v1 = *reinterpret_cast<const uint4*>(src + c1);
+  while (h < all) {
+    T* dst = h >= a.q.heads ? static_cast<T*>(a.k.out) + t * a.k.out_stride + (h - a.q.heads) * D
+                            : static_cast<T*>(a.q.out) + t * a.q.out_stride + h * D;
     if (turned) {
+      float x[2 * E];
       Vec<T>::unpack(v0, x);
       Vec<T>::unpack(v1, x + E);
       turn_unit<E, IL>(x, [&](int j) { return cs[j]; });
-      *reinterpret_cast<uint4*>(dst + c0) = Vec<T>::pack(x);
-      *reinterpret_cast<uint4*>(dst + c1) = Vec<T>::pack(x + E);
-    } else {
-      *reinterpret_cast<uint4*>(dst + c0) = v0;
-      *reinterpret_cast<uint4*>(dst + c1) = v1;
+      v0 = Vec<T>::pack(x);
+      v1 = Vec<T>::pack(x + E);
     }
+    *reinterpret_cast<uint4*>(dst + c0) = v0;
+    *reinterpret_cast<uint4*>(dst + c1) = v1;
+    h += kGroups;
+    load();
   }
 }
 
 template <typename T, int D, bool IL>
 cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
-  // (four tokens a block: 58 us where two take 65 and eight 58; one where there are too few for two blocks an SM)
+  // (four tokens a block: 16384 take 54.3 us, 59 with two and 55 with eight; one where they would be too few for a block an SM: 400
+  // of 40 heads 3.4 us; 1000 take 4.9 us with four, 5.8 with one)
   constexpr int kTok = 4;
-  if (a.tokens > kTok * 2LL * num_sms()) {
+  if (a.tokens > static_cast<long long>(kTok) * num_sms()) {
     rope_kernel<T, D, IL, kTok><<<static_cast<unsigned>((a.tokens + kTok - 1) / kTok), kThreads, 0, stream>>>(a);
   } else {
     rope_kernel<T, D, IL, 1><<<static_cast<unsigned>(a.tokens), kThreads, 0, stream>>>(a);
