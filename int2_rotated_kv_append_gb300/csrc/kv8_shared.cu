@@ -560,7 +560,9 @@ bool make_plan(const oscar_dims_t* d, int batch, int max_seq_len, int max_prefix
   int own_sms = sms;
   double best = 0;
   long long items = 0;
-  if (blocks > 0 && rows > 0 && groups > 0 && groups <= kTable) {
+  // Or every member by itself, by the decode's times: 8 x 2048 12.8 us (19 over tiles), 16 x 2048 18.9 (20), 32 x 2048 33 (22).
+  const double list_us = 7 + (own_bytes + 2.0 * members * H * max_prefix * d->head_dim) / (d->head_dim == 128 ? 6.2e6 : 5e6);
+  if (blocks > 0 && rows > 0 && groups > 0 && groups <= kTable && list_us >= block_us + start_us + merge_us) {  // (the least below)
     const long long tiles = rows / p->tm > likely ? rows / p->tm : likely;
     for (int k = 0; k < sms; k += 4) {
       for (int w = 1; w <= 4; ++w) {
@@ -578,8 +580,6 @@ bool make_plan(const oscar_dims_t* d, int batch, int max_seq_len, int max_prefix
     if (items > 0 && items < most_tiles) items = most_tiles;  // (0: more tiles than four waves have blocks)
     if (items > 0x7fffffffLL) return false;
   }
-  // ---- or every member by itself, by the decode's times: 8 x 2048 12.8 us (19 over tiles), 16 x 2048 18.9 (20), 32 x 2048 33 (22)
-  const double list_us = 7 + (own_bytes + 2.0 * members * H * max_prefix * d->head_dim) / (d->head_dim == 128 ? 6.2e6 : 5e6);
   p->list = items == 0 || list_us < best;
   size_t own;  // rows of partials
   if (p->list) {
