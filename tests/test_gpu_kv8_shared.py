@@ -460,6 +460,48 @@ def test_a_prompt_its_samples_and_their_steps(fmt, D, interleaved):
         c.decode_shared(q, groups, max_own_len=c.max_seq_len + 1)
 
 
+@pytest.mark.parametrize("B,prompt", [(5, 300), (64, 6000)])
+def test_captured_steps_read_what_the_step_before_wrote(B, prompt):
+    """Whole steps replayed without a pause, two at a time, and the last one's output, over the list and over tiles: the queries,
+    lengths, tables and lists that its kernels read are written by the kernels just before them."""
+    hq, H, D, steps = 8, 2, 128, 6
+    c = Kv8Cache(hq, H, D, num_pages=prompt // 16 + 5 * B, batch=B, max_seq_len=prompt + 2 * steps + 16)
+    g = torch.Generator("cuda").manual_seed(B)
+    rope = ok.Rope(D)
+    x = torch.randn(prompt, hq + 2 * H, D, device="cuda", generator=g).bfloat16()
+    assert c.reserve(i32([prompt] + [0] * (B - 1))).all()
+    c.rope_append(*torch.split(x, [hq, H, H], 1), rope, i32([0] + [prompt] * B), prompt)
+    c.fork(i32([0] * (B - 1)), i32(list(range(1, B))))
+    rows = torch.zeros(B, hq + 2 * H, D, dtype=torch.bfloat16, device="cuda")
+    source = torch.randn(2 * steps + 3, B, hq + 2 * H, D, device="cuda", generator=g).bfloat16()
+    at = torch.zeros(1, dtype=torch.int64, device="cuda")
+    start, ones = torch.arange(B + 1, dtype=torch.int32, device="cuda"), i32([1] * B)
+    out, qr = (torch.zeros(B, hq, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def step():
+        rows.copy_(source.index_select(0, at)[0])
+        at.add_(1)
+        c.reserve(ones)
+        c.rope_append(*torch.split(rows, [hq, H, H], 1), rope, start, 1, q_out=qr)
+        c.decode_shared(qr, c.groups(max_groups=2), out, max_prefix_len=prompt, max_own_len=64)
+
+    assert (ok.oscar_kv8_decode_shared_plan(c.dims, B, c.max_seq_len, prompt, 64, B, 2)["tile_rows"] > 0) == (B == 64)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(steps):
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        lens = c.seq_lens.tolist()
+        assert lens == [prompt + 3 + 2 * i] * B
+        ref, tol = R.attention(c.pages, c.scales, qr, list(range(B)), [n - 1 for n in lens], c.page_table.tolist(), R.E4M3, 0, 0)
+        assert ((out.double() - ref).abs() <= tol).all()
+    assert ok.oscar_device_errors(reset=True) == 0
+
+
 def test_a_cache_with_a_window_refuses():
     c = Kv8Cache(4, 2, 64, num_pages=8, batch=2, max_seq_len=64, window_len=16)
     with pytest.raises(ValueError):
