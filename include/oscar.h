@@ -663,12 +663,15 @@ oscar_status_t oscar_kv8_extend_varlen(const oscar_dims_t* dims, int32_t kv_form
  *   group_start   device int32 [num_groups + 1], non-decreasing, group_start[0] = 0: group g is members group_start[g] ..
  *                 group_start[g + 1] - 1; members from group_start[num_groups] <= num_members on are none
  *   prefix_lens   device int32 [num_groups]: the tokens that all members of the group share, of which whole pages are attended
- *                 together, read through any member's page table; 0 for sequences by themselves
+ *                 together, read through one member's page table (the first's that has all of them, else the longest's); 0 for
+ *                 sequences by themselves
  *   max_prefix_len  host bound: of a longer prefix the first max_prefix_len tokens (whole pages) are attended together, and the
  *                 rest with each member's own
  *   max_own_len   host bound on what any member has behind that; longer ones are cut off and flagged (OSCAR_DEVERR_SEQ_LEN)
  * q and out have a row for every sequence; rows of sequences that are no member are neither read nor written.  A member shorter
- * than its group's prefix attends what it has.  The work is split for these bounds: the nearer they and num_groups are to what
+ * than its group's prefix (one freed since the lists were made has length 0) attends what it has.  Lists hold while every member's
+ * pages within the prefix, as far as its length goes, are the group's; a member that has been freed and filled with something else
+ * makes them void.  The work is split for these bounds: the nearer they and num_groups are to what
  * the lists hold, the quicker.  A sequence is named once: of one named twice, either of the two results is left.  A
  * member out of [0, batch) is skipped and flagged (OSCAR_DEVERR_POSITION); lists that decrease or leave their range are flagged
  * and nothing is written.

@@ -85,6 +85,7 @@ struct alignas(16) BlockInfo {
   __half v_log2[kBlkPages];   // log2 of the V scale; -infinity: 0, or no page
   float v_top;                // the largest of them
   uint32_t flags;
+  int end;                    // SHARED: tokens of the sequence that is read
 };
 constexpr int kNoPage = 0x7fffffff - kPageSize;
 // flags: every row of row tile 0 / 1 sees the whole block; some row is behind the last token; V scales far apart
@@ -243,6 +244,31 @@ __device__ __forceinline__ Item item_of(const SharedArgs& s, int x, int limit, i
   return it;
 }
 
+// Tokens of the sequence that entry i of the list names; none where it is out of range (which is flagged where members' own parts are
+// attended).
+__device__ __forceinline__ int member_len(const SharedArgs& s, int i) {
+  const int b = __ldg(s.g.members + i), batch = s.e.a.batch;
+  const int L = max(__ldg(s.e.a.seq_lens + in_batch(b, batch)), 0);
+  return b == in_batch(b, batch) ? L : 0;
+}
+
+// One warp: the sequence through whose page table the prefix of the tile's group is read, and how many tokens of the prefix it has: the
+// first of the members that has all of it, else the longest, as nobody sees the rest.  (Not just the first: its entry may be out of
+// range, or its slot freed since the lists were made.)
+__device__ __forceinline__ int source_of(const SharedArgs& s, const Tile& t, int lane, int& len) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  int source = 0;
+  len = 0;
+  for (int i0 = 0; i0 < t.n && len < t.L; i0 += 32) {
+    const int i = t.q0 + i0 + lane, L = i0 + lane < t.n ? min(member_len(s, i), t.L) : 0;
+    const int top = __reduce_max_sync(kAll, L);
+    if (top <= len) continue;
+    len = top;
+    source = __ldg(s.g.members + t.q0 + i0 + __ffs(__ballot_sync(kAll, L == top)) - 1);
+  }
+  return source;
+}
+
 template <uint32_t N>
 __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -305,7 +331,7 @@ __device__ __forceinline__ void extend_body(const Args& args) {
     split = it.split;
     tile = it.tile;
     bps = it.bps;
-    b = in_batch(__ldg(args.g.members + it.start), a.batch);  // the sequence whose pages are read
+    b = in_batch(__ldg(args.g.members + it.start), a.batch);  // whose pages are read, as a rule
     T.q0 = it.start;
     T.n = it.n;
     T.L = it.prefix;
@@ -520,7 +546,7 @@ __device__ __forceinline__ void extend_body(const Args& args) {
       const int last_r = min(T.rows, wg * 128 + 128) - 1;  // rows behind it are zeros and not stored
       const int x_row = (T.r0 + min(r, last_r)) / gqa;
       int pos = T.L - T.n + x_row;
-      if constexpr (SHARED) pos = min(max(__ldg(a.seq_lens + in_batch(__ldg(args.g.members + T.q0 + x_row), a.batch)), 0), T.L) - 1;
+      if constexpr (SHARED) pos = min(member_len(args, T.q0 + x_row), T.L) - 1;
       const int after = a.window > 0 ? max(pos - a.window, -1) : -1;  // visible: behind it, or a sink
       if (PARTS == 2) {  // the other part's weights are 0
         uint32_t z[32];
@@ -866,7 +892,7 @@ __device__ __forceinline__ void extend_body(const Args& args) {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
           const int r = r0 + i * kStep;
-          if (bi.pos[r >> 4] + (r & 15) >= T.L)
+          if (bi.pos[r >> 4] + (r & 15) >= (SHARED ? bi.end : T.L))
             w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;  // any bits: behind the last token, or no page
         }
       }
@@ -920,11 +946,12 @@ __device__ __forceinline__ void extend_body(const Args& args) {
       // ---- page ids, scales, copies of codes: K by one warp, V by another (whole pages: four each) --------------
       const int side = warp == kFetchV;
       const int32_t* table = a.page_table + static_cast<size_t>(b) * a.max_pages;
+      int end = T.L, pages = T.vis.n;  // tokens of the sequence that is read, pages of them
       // Four blocks at a time, a page a lane: the ids are loaded two groups ahead and the scales one,
       // so that neither is waited for.
       auto look_up = [&](int g) {  // page id (-2: none)
         const int v = blk0 * kBlkPages + g * 32 + lane;
-        return g * 32 + lane < cnt * kBlkPages && v < T.vis.n ? __ldg(table + T.vis.page(v)) : -2;
+        return g * 32 + lane < cnt * kBlkPages && v < pages ? __ldg(table + T.vis.page(v)) : -2;
       };
       auto checked = [&](int id) {
         if (id != -2 && (id < 0 || id >= a.num_pages)) record_error(OSCAR_DEVERR_PAGE_ID);
@@ -943,7 +970,17 @@ __device__ __forceinline__ void extend_body(const Args& args) {
         p_after[t] = !SHARED && a.window > 0 ? T.L - T.n + (T.r0 + min(T.rows, t * 128 + 128) - 1) / gqa - a.window : -1;
       }
       const bool issuer = umma::elect_one();
-      int pid = -1, pid1 = checked(look_up(0)), pid2 = look_up(1);
+      int pid1 = look_up(0), pid2 = look_up(1);
+      if constexpr (SHARED) {
+        if (member_len(args, T.q0) < T.L) {  // (the first member's ids were on their way while its length was)
+          table = a.page_table + static_cast<size_t>(source_of(args, T, lane, end)) * a.max_pages;
+          pages = (end + kPageSize - 1) / kPageSize;
+          pid1 = look_up(0);
+          pid2 = look_up(1);
+        }
+      }
+      int pid = -1;
+      pid1 = checked(pid1);
       float2 sc = make_float2(1.f, 0.f), sc1 = scales(pid1);
       float v_top = -INFINITY;  // log2 of the largest V scale of all blocks looked at
       float v_own = -INFINITY, v_blk = -INFINITY;  // of this lane's page and block
@@ -992,7 +1029,7 @@ __device__ __forceinline__ void extend_body(const Args& args) {
           if (j == 0) {  // while the first codes are on their way: a sequence shorter than the prefix sees less of it
             int least = T.L;
             for (int i = T.r0 / gqa + lane; i <= (T.r0 + T.rows - 1) / gqa; i += 32)
-              least = min(least, max(__ldg(a.seq_lens + in_batch(__ldg(args.g.members + T.q0 + i), a.batch)), 0));
+              least = min(least, member_len(args, T.q0 + i));
             least = __reduce_min_sync(0xffffffffu, least);
 #pragma unroll
             for (int t = 0; t < MT; ++t) p_lo[t] = least - 1;
@@ -1030,7 +1067,7 @@ __device__ __forceinline__ void extend_body(const Args& args) {
           for (int t = 0; t < MT; ++t)
             if (!any((pos > p_lo[t] - (kPageSize - 1)) | ((pos <= p_after[t]) & (pos > a.sink - kPageSize))))
               flags |= kFull0 << t;
-          if (any((pid < 0) | (pos > T.L - kPageSize))) flags |= kTail;
+          if (any((pid < 0) | (pos > end - kPageSize))) flags |= kTail;
           if (any(wild)) flags |= kWild;
           if (mine) {
             BlockInfo& bi = infos[info];
@@ -1042,6 +1079,7 @@ __device__ __forceinline__ void extend_body(const Args& args) {
             if ((lane & 7) == 0) {
               bi.v_top = v_blk;
               bi.flags = flags;
+              if constexpr (SHARED) bi.end = end;
             }
           }
           __syncwarp();
