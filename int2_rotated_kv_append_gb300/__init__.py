@@ -445,6 +445,17 @@ def _here(t, now, what):
     return t.data_ptr()
 
 
+def _pool8(pages, scales, d, now):
+    """Pointers of an 8-bit cache's codes and scales, of num_pages pages or more."""
+    blocks = d.num_pages * d.num_kv_heads * 2
+    p = _here(pages, now, "kv8_pages")
+    if _nbytes(pages) < blocks * 16 * d.head_dim:
+        raise ValueError(f"kv8_pages has {d.num_pages} pages of [{d.num_kv_heads}][2][16][{d.head_dim}] bytes or more")
+    if scales.dtype is not torch.float32 or scales.numel() < blocks:
+        raise ValueError(f"kv8_scales is float32 with [{d.num_pages}][{d.num_kv_heads}][2] entries or more")
+    return p, _here(scales, now, "kv8_scales")
+
+
 def _rope(rope, now):
     if rope.turns.get_device() != now:
         raise ValueError(f"the Rope is on the current CUDA device ({now})")
@@ -481,13 +492,14 @@ def oscar_kv8_rope_append(dims, rope, kv_format, batch, max_tokens_per_seq, q, k
     kp, ks = _rows(k, tokens, hkv, dim, bf16, now, "k")
     vp, vs = _rows(v, tokens, hkv, dim, bf16, now, "v")
     op, os_ = _rows(q_out, tokens, hq, dim, bf16, now, "q_out")
+    pages, scales = _pool8(kv8_pages, kv8_scales, d, now)
     _check(lib.oscar_kv8_rope_append(
         d, _rope(rope, now), kv_format, batch, tokens, max_tokens_per_seq, qp, qs, kp, ks, vp, vs,
         _ints(t_start, batch + 1, now, "t_start"),
         None if positions is None else _ints(positions, tokens, now, "positions"),
         _ints(page_table, batch * d.max_pages_per_seq, now, "page_table"), _ints(seq_lens, batch, now, "seq_lens"),
-        None if granted is None else _ints(granted, batch, now, "granted"), _here(kv8_pages, now, "kv8_pages"),
-        _here(kv8_scales, now, "kv8_scales"), op, os_, _stream(stream)), "oscar_kv8_rope_append")
+        None if granted is None else _ints(granted, batch, now, "granted"), pages, scales, op, os_, _stream(stream)),
+        "oscar_kv8_rope_append")
 
 
 def _nbytes(t) -> int:
@@ -571,9 +583,9 @@ def oscar_kv8_decode_shared(dims, kv_format, batch, max_seq_len, max_prefix_len,
     op, _ = _rows(out, batch, d.num_q_heads, d.head_dim, torch.bfloat16, now, "out")
     if not (q.is_contiguous() and out.is_contiguous()):
         raise ValueError("q and out are contiguous")
+    pages, scales = _pool8(kv8_pages, kv8_scales, d, now)
     _check(lib.oscar_kv8_decode_shared(
-        d, kv_format, batch, max_seq_len, max_prefix_len, max_own_len, members.numel(), groups, qp,
-        _here(kv8_pages, now, "kv8_pages"), _here(kv8_scales, now, "kv8_scales"),
+        d, kv_format, batch, max_seq_len, max_prefix_len, max_own_len, members.numel(), groups, qp, pages, scales,
         _ints(page_table, batch * d.max_pages_per_seq, now, "page_table"), _ints(seq_lens, batch, now, "seq_lens"),
         _ints(members, 0, now, "members"), _ints(group_start, groups + 1, now, "group_start"),
         _ints(prefix_lens, 0, now, "prefix_lens"), sm_scale, op, _here(workspace, now, "workspace"), _nbytes(workspace),
