@@ -452,8 +452,9 @@ oscar_status_t oscar_calibrate(const oscar_dims_t* dims, int64_t num_samples, co
  *   y_a = magnitude (x_a cos - x_b sin),  y_b = magnitude (x_b cos + x_a sin)
  *   (a, b) = (i, i + rotary_dim / 2)  half layout (interleaved = 0), or (2 i, 2 i + 1)  (interleaved = 1)
  * The other channels pass through.  Frequencies are 64-bit fractions of a turn, turns[i] = f_i / (2 pi) 2^64 modulo 2^64, so that
- * an angle modulo a turn is exact at every 32-bit position (a negative position turns backwards: keys that move towards
- * the front of a cache).  Cosine and sine are fp32 to about a rounding, the products fp32, rounded once at the end.
+ * an angle modulo a turn is exact, for the fraction held, at every 32-bit position (a negative position turns backwards: keys that
+ * move towards the front of a cache).  Cosine and sine are fp32, off by 2^-22 of themselves at most; the products fp32, rounded
+ * once at the end.
  *   rotary_dim   a multiple of 16, at most head_dim
  *   magnitude    finite; 1 but for OSCAR_ROPE_YARN
  *   turns        device uint64 [rotary_dim / 2], from oscar_rope_turns
@@ -477,7 +478,8 @@ typedef struct {
  *   OSCAR_ROPE_BANDS     t = original_max_position f_i / (2 pi) turns within the original length: f_i where t >= high,
  *                        f_i / factor where t <= low, between them the mean weighted by (t - low) / (high - low)
  *   OSCAR_ROPE_DIVISORS  f_i / divisors[i] (host double [rotary_dim / 2], > 0)
- * Computed in double.  Invalid numbers, and frequencies over 10^6 radians a position, return OSCAR_ERR_INVALID_ARG.
+ * Computed in double: a frequency is off by about 2^-52 of itself (2^-24 of a turn for the fastest pairs at position 2^31).  Invalid
+ * numbers, and frequencies over 10^6 radians a position, return OSCAR_ERR_INVALID_ARG.
  */
 #define OSCAR_ROPE_PLAIN 0
 #define OSCAR_ROPE_LINEAR 1

@@ -2,9 +2,10 @@
 // rotates on the way.
 //
 // A frequency is held as a 64-bit fraction of a turn.  Its product with a position, modulo 2^64, is the angle modulo one
-// turn with nothing lost (within 2^-33 of a turn at any 32-bit position), so far positions are as good as near ones and no
-// table over positions is read.  The nearest quarter turn is taken off in whole numbers; what is left, within an eighth
-// of a turn, has all of fp32's bits.
+// turn, exact for the fraction that is held, so far positions are as good as near ones and no table over positions is read.  (The
+// fraction itself comes from a power in double, up to 2^-52 of the frequency off: 2^-24 of a turn for the fastest pairs at position 2^31.)
+// The nearest quarter turn is taken off in whole numbers; what is left, within an eighth of a turn, becomes fp32 from all 64 bits, so
+// that cosine and sine are good to 2^-22 of themselves, the sines of slow pairs' first positions too.
 #pragma once
 
 #include <math.h>
@@ -41,10 +42,10 @@ static inline bool bad_in_place(const void* in, int64_t in_stride, const void* o
 
 // (cos, sin) of pos * frequency, times magnitude.
 __device__ __forceinline__ float2 cos_sin(uint64_t turns, int pos, float magnitude) {
-  const uint32_t top = static_cast<uint32_t>((turns * static_cast<uint64_t>(static_cast<int64_t>(pos))) >> 32);
-  const uint32_t quarter = (top + 0x20000000u) >> 30;
+  const uint64_t whole = turns * static_cast<uint64_t>(static_cast<int64_t>(pos));
+  const uint64_t quarter = (whole + (1ull << 61)) >> 62;
   float s, c;
-  sincospif(static_cast<float>(static_cast<int32_t>(top - (quarter << 30))) * 0x1p-31f, &s, &c);
+  sincospif(static_cast<float>(static_cast<int64_t>(whole - (quarter << 62))) * 0x1p-63f, &s, &c);
   const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;  // |cos|, |sin| of the whole angle, up to their signs
   const bool neg_x = quarter == 1 || quarter == 2, neg_y = quarter >= 2;
   return make_float2((neg_x ? -x : x) * magnitude, (neg_y ? -y : y) * magnitude);
