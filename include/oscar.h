@@ -656,9 +656,11 @@ oscar_status_t oscar_kv8_extend_varlen(const oscar_dims_t* dims, int32_t kv_form
  * oscar_kv8_decode_shared -- oscar_kv8_decode (without a window) of sequences whose first pages are the same, as
  * oscar_pages_fork leaves them: each group's prefix is attended once for all its members, on tensor cores, what a member has
  * behind it by itself, and the two are joined by log-sum-exp.  The result is that of oscar_kv8_decode, but that weights are
- * held in 11 bits (as oscar_kv8_extend_varlen's over the prefixes, and with a step of 2^-30 of the row's largest elsewhere); the
- * output has 8.  Where that would take longer than each member by itself (small calls, short prefixes), each attends all of its
- * own.
+ * held in 11 bits (as oscar_kv8_extend_varlen's over the prefixes, so in 8 where their pages' V scales are more than 2^8 apart, and with
+ * a step of 2^-30 of the row's largest elsewhere); the output has 8.  Where that would take longer than each member by itself (small
+ * calls, short prefixes), and where the groups have more tiles than four waves of blocks (with 8 KV heads on 152 SMs 76, a tile at
+ * least for every group), each attends all of its own, with oscar_kv8_decode's weights.  oscar_kv8_decode_shared_plan tells which; it
+ * goes by the bounds and the numbers of members and groups alone.
  * Arguments beyond oscar_kv8_decode's
  *   num_members   entries of `members` at most; num_groups: of prefix_lens
  *   members       device int32 [num_members]: the sequences to decode, group after group
@@ -669,7 +671,8 @@ oscar_status_t oscar_kv8_extend_varlen(const oscar_dims_t* dims, int32_t kv_form
  *                 sequences by themselves
  *   max_prefix_len  host bound: of a longer prefix the first max_prefix_len tokens (whole pages) are attended together, and the
  *                 rest with each member's own
- *   max_own_len   host bound on what any member has behind that; longer ones are cut off and flagged (OSCAR_DEVERR_SEQ_LEN)
+ *   max_own_len   host bound on what any member has behind that (all of it, for members of a group without a prefix); longer ones
+ *                 are cut off and flagged (OSCAR_DEVERR_SEQ_LEN)
  * q and out have a row for every sequence; rows of sequences that are no member are neither read nor written.  A member shorter
  * than its group's prefix (one freed since the lists were made has length 0) attends what it has.  Lists hold while every member's
  * pages within the prefix, as far as its length goes, are the group's; a member that has been freed and filled with something else

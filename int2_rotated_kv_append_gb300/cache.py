@@ -283,8 +283,9 @@ class Kv8Cache:
 
     def groups(self, min_pages=1, max_groups=8, stream=None):
         """The sequences whose first min_pages pages are full and the same (as ``fork`` leaves them), max_groups - 1 groups of
-        them at most, and the rest.  They hold until a sequence of a group is forked, freed, trimmed or shortened: one call
-        serves every layer of a step, and later steps that only append."""
+        them at most, and the rest, which share nothing.  They hold while the sequences grow or end, until a slot that was freed is
+        filled again: one call serves every layer of a step, and later steps that only append.  ``decode_shared`` is the quicker
+        the nearer max_groups is to one more than there are."""
         with self._allocating(stream):
             new = lambda n: torch.empty(n, dtype=torch.int32, device=self.device)  # noqa: E731
             g = SharedPrefixes(new(self.batch), new(max_groups + 1), new(max_groups))
@@ -296,8 +297,9 @@ class Kv8Cache:
                       max_own_len=None):
         """``decode`` that attends what each group (a ``SharedPrefixes``) shares once for all its members, for caches without a
         window.  The bounds (None: max_seq_len's) size the work: on a group's prefix, of which more is attended by each
-        member, and on what a member has behind it.  Rows of sequences that are no member are left as they are in ``out``,
-        and mean nothing in an output made here."""
+        member, and on what a member has behind it, of which more is cut off and flagged (of sequences in no group: on all they
+        have).  Bounds near the truth make it up to twice as quick.  Rows of sequences that are no member are left as they are in
+        ``out``, and mean nothing in an output made here."""
         if self.window_len:
             raise ValueError("decode_shared is for caches without a window")
         bound = self._bound(max_seq_len)

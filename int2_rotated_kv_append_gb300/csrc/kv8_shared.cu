@@ -1,7 +1,7 @@
 // Decode attention of sequences that share prefixes (oscar_kv8_decode_shared), over the 8-bit paged cache.
 //
-// Where that would take longer than each member by itself, as in small calls, it is the decode's split kernel over the list, and a
-// merge.  Else three kernels, of which the first two run beside one another.  One takes every group's prefix once, for all its members: their
+// Where that would take longer than each member by itself, as in small calls, or has more tiles than four waves of blocks, it is the
+// decode's split kernel over the list, and a merge.  Else three kernels, of which the first two run beside one another.  One takes every group's prefix once, for all its members: their
 // queries are the rows of tiles on tcgen05, as in the extend, and the prefix is cut into splits so that the tiles of all groups
 // fill whole waves.  The lists are on the device, so the cut is made there, by every block for itself.  The other attends what
 // each member has of its own, as the decode does.  The former is bound by products and the latter by memory, and either fills an
@@ -9,9 +9,9 @@
 //
 // Against reading every member's whole sequence this trades the prefix's bytes, once instead of once a member, for products
 // at the tensor cores' rate.  Measured (GB300; 8 KV heads, D = 128): 64 members of one prefix of 16384 tokens with up to 1024 of
-// their own, 32 query heads, 101 MB and 18 GFLOP: 47 us (each by itself 325): 88 prefix CTAs of 40 us (10 before their first
+// their own, 32 query heads, 101 MB and 18 GFLOP: 48 us (each by itself 325): 88 prefix CTAs of 40 us (10 before their first
 // logits, 12 blocks of 2, 4 for 128 KB of partials), 60 SMs for 35 us with the 67 MB of the members' own, 7 for the merge.  128 of each
-// of two prefixes of 31 thousand, 64 query heads, 261 GFLOP: 264 us, 990 TFLOP/s (2360 each by itself): 128 CTAs of 122 blocks
+// of two prefixes of 31 thousand, 64 query heads, 261 GFLOP: 259 us, 1010 TFLOP/s (2360 each by itself): 128 CTAs of 122 blocks
 // at 1.5 GHz (the power limit), tensor pipes 44% busy, as in the extend.
 #include "kv8_decode_body.cuh"
 #include "kv8_extend_body.cuh"
