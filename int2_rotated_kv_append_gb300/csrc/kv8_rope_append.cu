@@ -7,7 +7,7 @@
 // are on their way into shared memory meanwhile, the first one's beside the cosines.  The rotated key is not rounded before it
 // becomes a code.  Bound by the bytes: 2 (Hq + 2 Hkv) in, 2 Hq + 2 Hkv out per channel: six prompts, 56 thousand tokens, 32 query
 // and 8 KV heads, D = 128, 1.11 GB: 169 us, 6.6 TB/s, 98% of a plain copy of as many bytes (187 with each item's rows loaded into
-// registers; as long with 20 warps an SM as with 16).  One token of each of 64 sequences: 3.6 us.
+// registers; as long with 20 warps an SM as with 16).  One token of each of 64 sequences: 4.0 us.
 #include <type_traits>
 
 #include "kv8.cuh"

@@ -3,7 +3,7 @@
 // A thread has one unit (16 channels of bf16) of one token and goes over the heads, so that the angles' cosines and sines
 // are read once: a block computes them for its tokens, one each a thread, into shared memory.  A warp's loads are whole
 // rows of neighbouring heads.  Bound by the bytes, each element once in and once out: 16384 tokens of 40 heads, D = 128, bf16, 336 MB:
-// 54.3 us, 6.2 TB/s, as long as a plain copy of as many bytes; 64 tokens 2.3 us.
+// 54.3 us, 6.2 TB/s, as long as a plain copy of as many bytes; 64 tokens 2.5 us.
 #include "rope.cuh"
 
 namespace {
